@@ -539,6 +539,83 @@ int verify_accept_greedy(const void* logits, va_dtype logits_dtype, int64_t tota
                          size_t workspace_bytes, void* stream);
 
 /*
+ * Sampled acceptance of draft trees: verify_accept_greedy's counterpart for
+ * sampling.  Each drafted token is verified against the target model's
+ * probabilities with the caller's random numbers, so that the emitted tokens
+ * are distributed as the target model's own samples.
+ *
+ * The tree arguments are verify_accept_greedy's.  p_v = softmax(logits[v] /
+ * T_b), T_b = temperature[b] (NULL: 1).  From the root, the children of node v
+ * are tried in index order.  Child c with token x = draft_tokens[c] was drawn
+ * from q = draft_probs[v] (row v: the distribution of node v's children;
+ * siblings are drawn independently).  With r = p_v at first, c is accepted iff
+ *   uniforms[c] * q(x) < r(x),
+ * and a rejection replaces r by max(r - q, 0), normalised.  draft_probs =
+ * NULL: drafts chosen without sampling (q(x) = 1 at the token): c is accepted
+ * iff uniforms[c] < r(x), and a rejection takes x out of r.  The first
+ * accepted child is the next node.  When none is accepted the bonus token is
+ * argmax_x r(x) / noise[b][x], the smallest x among equals -- a sample of r for
+ * noise drawn from Exp(1) -- or of p_v when rounding left r without mass.  T_b =
+ * 0 is greedy: a child is accepted iff its token is the first argmax of the
+ * row, and the bonus token is that argmax.
+ *
+ * Outputs: accept_len, accepted_nodes (-1 past the path) and bonus_token as
+ * in verify_accept_greedy; logprobs (nullable) [total_qo]: at qo_indptr[b] + k
+ * the natural log, under the p of its row, of the k-th emitted token -- the
+ * draft token of accepted node k + 1, and at k = accept_len - 1 the bonus token
+ * -- and 0 past them (0 throughout for T_b = 0).  Entries of rows outside every
+ * request are not written.
+ *
+ * uniforms [total_qo] fp32 in [0, 1); noise [batch, noise_stride] fp32, >= 0;
+ * logits bf16 or fp32 without NaN or +inf, -inf for a token of probability 0
+ * (a node whose row is all -inf accepts no child and gives bonus -1);
+ * draft_probs bf16 or fp32, >= 0.  A draft token outside [0, vocab) is
+ * rejected.  An empty request gives accept_len 0 and bonus -1; one whose
+ * parents, tables or temperature (negative, infinite, NaN) are invalid gives
+ * the same, its path -1, and raises VA_DEV_BAD_TABLE in status_d (nullable).
+ * Rows may start at any element (16-byte aligned rows of a vocabulary that is
+ * a multiple of 8 are read fastest).  Probabilities, sums and residuals are
+ * computed in fp32 with sums and decisions in fp64.  Rows of nodes that are
+ * not reached are not read.  No workspace.
+ * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED (dtypes, sizes past 32
+ * bits), VA_ERR_CUDA.
+ */
+int verify_accept_sample(const void* logits, va_dtype logits_dtype, int64_t total_qo, int vocab,
+                         int64_t row_stride, const int32_t* qo_indptr, int batch,
+                         const int32_t* draft_tokens, const int32_t* parents,
+                         const float* uniforms, const float* noise, int64_t noise_stride,
+                         const float* temperature, const void* draft_probs, va_dtype draft_dtype,
+                         int64_t draft_stride, int32_t* accept_len, int32_t* accepted_nodes,
+                         int32_t* bonus_token, float* logprobs, int* status_d, int num_sms,
+                         void* stream);
+
+/*
+ * Compaction of the accepted drafts in the paged cache: the step after
+ * acceptance.  The page tables are those of the step (kv_len_b = prefix +
+ * L_b).  For every layer, KV head and both caches, the row of the node
+ * accepted_nodes[qo_indptr[b] + k], position prefix + that node, is copied
+ * bit for bit to position prefix + k, k < accept_len[b], in place; the next
+ * step's kv length of the request is prefix + accept_len[b], which
+ * kv_len_out (nullable, [batch]) receives.  No other slot is written.  accept_len and
+ * accepted_nodes are verify_accept_greedy's or verify_accept_sample's outputs
+ * (a path strictly ascending and below L_b; any other is skipped whole, with
+ * VA_DEV_BAD_TABLE in status_d and the unchanged kv length in kv_len_out).
+ *
+ * k_cache / v_cache: num_layers caches of the same page table one after the
+ * other, each in the layout kv_layout ([num_layers, num_pages, ...],
+ * contiguous).  head_dim_v 0 means head_dim.  A row whose page id lies outside
+ * the pool is skipped with VA_DEV_BAD_PAGE.  Requests whose draft slots share
+ * a page slot are not supported (their order is not defined).
+ * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED, VA_ERR_CUDA.
+ */
+int paged_kv_compact(const int32_t* accept_len, const int32_t* accepted_nodes,
+                     const int32_t* qo_indptr, int64_t total_qo, const int32_t* kv_indptr,
+                     const int32_t* kv_indices, const int32_t* last_page_len, void* k_cache,
+                     void* v_cache, int num_layers, int batch, int num_kv_heads, int head_dim,
+                     int head_dim_v, int page_size, int num_pages, va_dtype kv_dtype,
+                     va_kv_layout kv_layout, int32_t* kv_len_out, int* status_d, void* stream);
+
+/*
  * verify_attn_run for callers that cannot allocate device memory.
  *
  * No page describes this entry point; it exists for callers that may not

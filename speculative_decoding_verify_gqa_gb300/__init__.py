@@ -33,7 +33,7 @@ __all__ = [
     "verify_attn_partial", "verify_attn_merge", "paged_kv_append",
     "verify_attn_device_status", "verify_attn_plan_bounds", "verify_attn_plan_host",
     "verify_attn_workspace_size", "verify_attn_run_static_scratch", "verify_attn_append_run",
-    "verify_accept_greedy",
+    "verify_accept_greedy", "verify_accept_sample", "paged_kv_compact",
     "status_string", "num_sms", "KV_BF16", "KV_FP8_E4M3", "library_path",
 ]
 
@@ -139,6 +139,10 @@ def lib():
         "verify_accept_workspace_size": (i32, [i64, i32, i32, Psz]),
         "verify_accept_greedy": (i32, [P, i32, i64, i32, i64, P, i32, P, P, P, P, P, P, P, i32,
                                        P, sz, P]),
+        "verify_accept_sample": (i32, [P, i32, i64, i32, i64, P, i32, P, P, P, P, i64, P, P, i32, i64,
+                                       P, P, P, P, P, i32, P]),
+        "paged_kv_compact": (i32, [P, P, P, i64, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32,
+                                   i32, P, P, P]),
         "verify_attn_merge": (i32, [P, i32, i32, i32, P, P, P, P, sz, P]),
         "verify_attn_plan_launches": (i32, [P, Pi]),
         "verify_attn_plan_upload": (i32, [P, P, sz, P]),
@@ -761,6 +765,113 @@ def verify_accept_greedy(logits, qo_indptr, draft_tokens, parents, workspace=Non
                                     workspace.numel(), _stream(stream))
     _check("verify_accept_greedy", rc)
     return acc, path[:total], bonus, None if am is None else am[:total]
+
+
+_CODES = {torch.bfloat16: 0, torch.float32: 2}
+
+
+def _current(t, name):
+    """Raise unless `t` lives on the current CUDA device (kernels are launched there)."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError("%s must be on the current CUDA device" % name)
+
+
+def _arg(t, name, dtype, shape, device):
+    """Device address of a contiguous tensor of this dtype, shape and device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                         % (name, dtype, tuple(shape), device))
+    return t.data_ptr()
+
+
+def _rows(t, name, rows, vocab, device):
+    """(address, row stride) of a [rows, vocab] matrix with unit column stride; rows may be padded."""
+    if t.shape != (rows, vocab) or t.device != device or (rows and vocab > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be [%d, %d] on %s with unit column stride" % (name, rows, vocab, device))
+    stride = t.stride(0) if rows > 1 else vocab
+    if stride < vocab:
+        raise ValueError("%s has overlapping rows" % name)
+    return t.data_ptr(), stride
+
+
+def verify_accept_sample(logits, qo_indptr, draft_tokens, parents, uniforms, noise,
+                         temperature=None, draft_probs=None, want_logprobs=False, status=None,
+                         out=None, stream=None):
+    """Sampled acceptance of draft trees (see include/verify_attn.h): logits
+    [total, vocab] bf16 or fp32, uniforms [total] fp32 in [0, 1), noise
+    [B, vocab] fp32 drawn from Exp(1), temperature [B] fp32 (None: 1; 0 is
+    greedy), draft_probs [total, vocab] bf16 or fp32 -- row v the distribution
+    node v's children were drawn from -- or None for drafts that were chosen,
+    not sampled.  All on the current device.  Returns (accept_len [B],
+    accepted_nodes [total], bonus_token [B], logprobs [total] or None), int32
+    and fp32, written into `out` (such a tuple) when given."""
+    _current(logits, "logits")
+    if logits.dim() != 2 or logits.dtype not in _CODES:
+        raise ValueError("logits must be [total, vocab], bfloat16 or float32")
+    total, vocab = logits.shape
+    dev, batch = logits.device, qo_indptr.shape[0] - 1
+    lp, ls = _rows(logits, "logits", total, vocab, dev)
+    np_, ns = _rows(noise, "noise", batch, vocab, dev)
+    if noise.dtype != torch.float32:
+        raise ValueError("noise must be float32")
+    dp, ds, dc = None, 0, 0
+    if draft_probs is not None:
+        if draft_probs.dtype not in _CODES:
+            raise ValueError("draft_probs must be bfloat16 or float32")
+        dp, ds = _rows(draft_probs, "draft_probs", total, vocab, dev)
+        dc = _CODES[draft_probs.dtype]
+    i32, f32, n, b = torch.int32, torch.float32, (total,), (batch,)
+    if out is None:
+        out = (torch.empty(b, dtype=i32, device=dev), torch.empty(n, dtype=i32, device=dev),
+               torch.empty(b, dtype=i32, device=dev),
+               torch.empty(n, dtype=f32, device=dev) if want_logprobs else None)
+    acc, path, bonus, logprobs = out
+    rc = lib().verify_accept_sample(
+        lp, _CODES[logits.dtype], total, vocab, ls, _arg(qo_indptr, "qo_indptr", i32, (batch + 1,), dev),
+        batch, _arg(draft_tokens, "draft_tokens", i32, n, dev), _arg(parents, "parents", i32, n, dev),
+        _arg(uniforms, "uniforms", f32, n, dev), np_, ns, _arg(temperature, "temperature", f32, b, dev),
+        dp, dc, ds, _arg(acc, "accept_len", i32, b, dev), _arg(path, "accepted_nodes", i32, n, dev),
+        _arg(bonus, "bonus_token", i32, b, dev), _arg(logprobs, "logprobs", f32, n, dev),
+        _arg(status, "status", i32, (1,), dev), 0, _stream(stream))
+    _check("verify_accept_sample", rc)
+    return out
+
+
+def paged_kv_compact(accept_len, accepted_nodes, qo_indptr, kv_indptr, kv_indices, last_page_len,
+                     k_cache, v_cache, kv_layout="hnd", kv_len_out=None, status=None, stream=None):
+    """Move the accepted drafts' K/V rows to the front of their request's
+    draft slots, in place (see include/verify_attn.h): position prefix +
+    accepted_nodes[k] to prefix + k.  The tables are the step's (prefix +
+    drafts); k_cache / v_cache are one layer's pool, or [layers, ...] pools of
+    several layers moved in one call.  kv_len_out [B] int32 receives prefix +
+    accept_len, the next step's kv lengths.  All on the current device."""
+    _current(k_cache, "k_cache")
+    if k_cache.dim() not in (4, 5) or v_cache.shape[:-1] != k_cache.shape[:-1]:
+        raise ValueError("k_cache / v_cache must be [pages, ...] or [layers, pages, ...] pools of like shape")
+    if k_cache.dtype != v_cache.dtype or k_cache.dtype not in _DTYPES:
+        raise ValueError("k_cache / v_cache must both be bfloat16 or float8_e4m3fn")
+    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    layout = _LAYOUTS[kv_layout]
+    num_pages, a, c, d = k_cache.shape[-4:]
+    page_size, h_kv = (a, c) if layout == LAYOUT_NHD else (c, a)
+    dev, i32, batch = k_cache.device, torch.int32, qo_indptr.shape[0] - 1
+    total, b = accepted_nodes.shape[0], (batch,)
+    if kv_indices.dim() != 1:
+        raise ValueError("kv_indices must be one-dimensional")
+    rc = lib().paged_kv_compact(
+        _arg(accept_len, "accept_len", i32, b, dev), _arg(accepted_nodes, "accepted_nodes", i32, (total,), dev),
+        _arg(qo_indptr, "qo_indptr", i32, (batch + 1,), dev), total,
+        _arg(kv_indptr, "kv_indptr", i32, (batch + 1,), dev),
+        _arg(kv_indices, "kv_indices", i32, kv_indices.shape, dev),
+        _arg(last_page_len, "last_page_len", i32, b, dev),
+        _arg(k_cache, "k_cache", k_cache.dtype, k_cache.shape, dev),
+        _arg(v_cache, "v_cache", v_cache.dtype, v_cache.shape, dev), layers, batch, h_kv, d,
+        v_cache.shape[-1], page_size, num_pages, _DTYPES[k_cache.dtype], layout,
+        _arg(kv_len_out, "kv_len_out", i32, b, dev), _arg(status, "status", i32, (1,), dev),
+        _stream(stream))
+    _check("paged_kv_compact", rc)
 
 
 STATIC_SCRATCH_BYTES = 32 << 20

@@ -913,6 +913,123 @@ int verify_accept_greedy(const void* logits, va_dtype logits_dtype, int64_t tota
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }
 
+// CTAs per request of the sampled acceptance: enough that the batch fills the
+// GPU twice over (two CTAs fit an SM), each with at least 4096 vocabulary
+// entries.  A power of two up to the portable cluster size.
+static int sample_cluster(int batch, int vocab, int num_sms) {
+  int c = 1;
+  while (c < 8 && (int64_t)batch * c * 2 <= 2LL * num_sms && vocab > 4096 * c) c *= 2;
+  return c;
+}
+
+int verify_accept_sample(const void* logits, va_dtype logits_dtype, int64_t total_qo, int vocab,
+                         int64_t row_stride, const int32_t* qo_indptr, int batch,
+                         const int32_t* draft_tokens, const int32_t* parents,
+                         const float* uniforms, const float* noise, int64_t noise_stride,
+                         const float* temperature, const void* draft_probs, va_dtype draft_dtype,
+                         int64_t draft_stride, int32_t* accept_len, int32_t* accepted_nodes,
+                         int32_t* bonus_token, float* logprobs, int* status_d, int num_sms,
+                         void* stream) {
+  if (batch < 0 || total_qo < 0 || vocab <= 0 || row_stride < vocab || noise_stride < vocab ||
+      (draft_probs && draft_stride < vocab))
+    return VA_ERR_INVALID_ARGUMENT;
+  if (logits_dtype != VA_BF16 && logits_dtype != VA_F32) return VA_ERR_UNSUPPORTED;
+  if (draft_probs && draft_dtype != VA_BF16 && draft_dtype != VA_F32) return VA_ERR_UNSUPPORTED;
+  constexpr int64_t kMaxElems = (int64_t)1 << 47;
+  if (total_qo > 0x7fffffffLL || batch > 0x7fffffff / 8 || vocab > 0x7fffffff - 65536 ||
+      (total_qo > 0 && (row_stride > kMaxElems / total_qo ||
+                        (draft_probs && draft_stride > kMaxElems / total_qo))) ||
+      (batch > 0 && noise_stride > kMaxElems / batch))
+    return VA_ERR_UNSUPPORTED;
+  if (batch == 0) return VA_OK;
+  if (!qo_indptr || !accept_len || !bonus_token || !noise ||
+      (total_qo > 0 && (!logits || !draft_tokens || !parents || !uniforms || !accepted_nodes)))
+    return VA_ERR_INVALID_ARGUMENT;
+  const int les = logits_dtype == VA_BF16 ? 2 : 4, qes = draft_dtype == VA_BF16 ? 2 : 4;
+  const uintptr_t la = reinterpret_cast<uintptr_t>(logits), qa = reinterpret_cast<uintptr_t>(draft_probs),
+                  na = reinterpret_cast<uintptr_t>(noise);
+  if (la % les || na % 4 || (draft_probs && qa % qes)) return VA_ERR_INVALID_ARGUMENT;
+  if (num_sms <= 0) {
+    int rc = query_sms(&num_sms);
+    if (rc) return rc;
+  }
+  SampleParams p;
+  memset(&p, 0, sizeof(p));
+  p.logits = logits;
+  p.draft = draft_probs;
+  p.noise = noise;
+  p.uniforms = uniforms;
+  p.temperature = temperature;
+  p.qo_indptr = qo_indptr;
+  p.tokens = draft_tokens;
+  p.parents = parents;
+  p.accept_len = accept_len;
+  p.path = accepted_nodes;
+  p.bonus = bonus_token;
+  p.logprobs = logprobs;
+  p.status = status_d;
+  p.row_stride = row_stride;
+  p.draft_stride = draft_stride;
+  p.noise_stride = noise_stride;
+  p.total = (int)total_qo;
+  p.vocab = vocab;
+  p.batch = batch;
+  p.cluster = sample_cluster(batch, vocab, num_sms);
+  p.slice = ((vocab + p.cluster - 1) / p.cluster + 7) / 8 * 8;
+  p.vec = vocab % 8 == 0 && la % 16 == 0 && row_stride * les % 16 == 0 && na % 16 == 0 &&
+          noise_stride % 4 == 0 && (!draft_probs || (qa % 16 == 0 && draft_stride * qes % 16 == 0));
+  const int draft = !draft_probs ? 0 : draft_dtype == VA_BF16 ? 1 : 2;
+  cudaError_t e = launch_accept_sample(p, logits_dtype == VA_BF16, draft, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
+}
+
+int paged_kv_compact(const int32_t* accept_len, const int32_t* accepted_nodes,
+                     const int32_t* qo_indptr, int64_t total_qo, const int32_t* kv_indptr,
+                     const int32_t* kv_indices, const int32_t* last_page_len, void* k_cache,
+                     void* v_cache, int num_layers, int batch, int num_kv_heads, int head_dim,
+                     int head_dim_v, int page_size, int num_pages, va_dtype kv_dtype,
+                     va_kv_layout kv_layout, int32_t* kv_len_out, int* status_d, void* stream) {
+  if (batch < 0 || total_qo < 0 || num_layers <= 0 || num_kv_heads <= 0 || head_dim_v < 0)
+    return VA_ERR_INVALID_ARGUMENT;
+  int rc = check_common(num_kv_heads, num_kv_heads, head_dim, page_size, VA_DTYPE_BF16, kv_dtype);
+  if (rc) return rc;
+  if (head_dim_v == 0) head_dim_v = head_dim;
+  if (head_dim_v != 64 && head_dim_v != 128) return VA_ERR_UNSUPPORTED;
+  if (kv_layout != VA_LAYOUT_HND && kv_layout != VA_LAYOUT_NHD) return VA_ERR_INVALID_ARGUMENT;
+  if (batch > 65535 || total_qo > 0x7fffffffLL) return VA_ERR_UNSUPPORTED;
+  if (batch == 0) return VA_OK;
+  if (!accept_len || !qo_indptr || !kv_indptr || !last_page_len || !k_cache || !v_cache ||
+      num_pages <= 0 || (total_qo > 0 && (!accepted_nodes || !kv_indices)))
+    return VA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return VA_ERR_INVALID_ARGUMENT;
+  CompactParams p;
+  memset(&p, 0, sizeof(p));
+  p.accept_len = accept_len;
+  p.path = accepted_nodes;
+  p.qo_indptr = qo_indptr;
+  p.kv_indptr = kv_indptr;
+  p.kv_indices = kv_indices;
+  p.last_page_len = last_page_len;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.kv_len_out = kv_len_out;
+  p.status = status_d;
+  p.total_qo = total_qo;
+  p.batch = batch;
+  p.layers = num_layers;
+  p.h_kv = num_kv_heads;
+  p.page_size = page_size;
+  p.log2_page = log2_int(page_size);
+  p.num_pages = num_pages;
+  const int es = kv_dtype == VA_DTYPE_FP8_E4M3 ? 1 : 2;
+  p.k_chunks = head_dim * es / 16;
+  p.v_chunks = head_dim_v * es / 16;
+  p.nhd = kv_layout == VA_LAYOUT_NHD;
+  if ((int64_t)num_layers * num_kv_heads * (p.k_chunks + p.v_chunks) > 0x7fffffffLL) return VA_ERR_UNSUPPORTED;
+  cudaError_t e = launch_compact(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
+}
+
 int paged_kv_append(const void* k_new, const void* v_new, const int32_t* append_indptr,
                     const int32_t* kv_indptr, const int32_t* kv_indices,
                     const int32_t* last_page_len, void* k_cache, void* v_cache, int batch,

@@ -111,6 +111,49 @@ struct AcceptParams {
 };
 cudaError_t launch_accept(const AcceptParams& p, bool bf16, cudaStream_t stream);
 
+// Sampled acceptance (see k_accept_sample.cu).
+struct SampleParams {
+  const void* logits;         // [total, row_stride] bf16 or fp32
+  const void* draft;          // nullable [total, draft_stride]: row v = the distribution node v's
+                              // children were drawn from (bf16 or fp32)
+  const float* noise;         // [batch, noise_stride] Exp(1) numbers
+  const float* uniforms;      // [total] numbers in [0, 1)
+  const float* temperature;   // nullable [batch]
+  const int32_t* qo_indptr;   // [batch + 1]
+  const int32_t* tokens;      // [total]
+  const int32_t* parents;     // [total] local parent index, -1 for the root
+  int32_t* accept_len;        // [batch]
+  int32_t* path;              // [total]
+  int32_t* bonus;             // [batch]
+  float* logprobs;            // nullable [total]
+  int* status;                // nullable
+  int64_t row_stride, draft_stride, noise_stride;  // elements
+  int total, vocab, batch;
+  int cluster;                // CTAs per request
+  int slice;                  // vocabulary entries per CTA (a multiple of 8)
+  int vec;                    // every row starts on 16 bytes and holds a multiple of 8 entries
+};
+cudaError_t launch_accept_sample(const SampleParams& p, bool logits_bf16, int draft, cudaStream_t stream);
+
+// Compaction of accepted drafts (see k_compact.cu).
+struct CompactParams {
+  const int32_t* accept_len;  // [batch]
+  const int32_t* path;        // [total_qo]
+  const int32_t* qo_indptr;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* last_page_len;
+  void* k_cache;              // [layers, num_pages, ...]
+  void* v_cache;
+  int32_t* kv_len_out;        // nullable [batch]
+  int* status;                // nullable
+  int64_t total_qo;
+  int batch, layers, h_kv, page_size, log2_page, num_pages;
+  int k_chunks, v_chunks;     // 16-byte chunks of a K / V row
+  int nhd;
+};
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+
 // Launch `func` with void** args; pdl = true lets the grid be scheduled
 // before the previous kernel in the stream finishes (programmatic dependent
 // launch); such kernels call grid_dependency_wait() before touching memory.
