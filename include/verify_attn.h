@@ -350,6 +350,52 @@ int verify_attn_merge(const int32_t* qo_indptr, int num_qo_heads, int num_kv_hea
 int verify_attn_plan_upload(const void* plan_h, void* workspace_d, size_t workspace_bytes,
                             void* stream);
 
+/*
+ * Plans for batches that share a prefix: requests that start with the same
+ * pages (one system prompt, several samples of one prompt).  The shared keys
+ * are read and multiplied once for all query rows of the group, each
+ * request's own keys as before, and the parts are merged by LSE; out and lse
+ * are those of a plan without groups, to rounding.
+ *
+ * Groups are ranges of consecutive requests: group g is requests
+ * group_indptr_h[g] .. group_indptr_h[g + 1] (group_indptr_h[0] = 0,
+ * group_indptr_h[num_groups] = batch; groups may be empty or of one request),
+ * whose first shared_pages_h[g] page ids are equal: the kernels read them
+ * from the group's first request.  Every request of a group lists at least
+ * that many pages, and with query tokens has its drafts behind them (prefix >=
+ * shared_pages * page_size).  A group whose sharing would not save memory
+ * traffic is planned request by request.
+ *
+ * verify_attn_plan_shared_host is verify_attn_plan_host with the groups; its
+ * plan goes through verify_attn_plan_upload, verify_attn_run(_ex),
+ * verify_attn_partial(_ex), verify_attn_merge, verify_attn_append_run and
+ * verify_attn_run_static_scratch like any other.  Bounds of its sizes, as
+ * verify_attn_plan_bounds gives them: verify_attn_plan_shared_bounds.
+ * Errors: those of verify_attn_plan_host; VA_ERR_INVALID_ARGUMENT for groups
+ * that break the rules above; VA_ERR_UNSUPPORTED for a full-prefix mask
+ * layout and for draft_items = 1.
+ *
+ * verify_attn_shared_groups finds such groups from host copies of the page
+ * tables: consecutive requests that start with at least min_pages equal
+ * pages, joined while that does not lower the number of page reads saved.
+ * group_indptr_h holds batch + 1 entries, shared_pages_h batch.  No CUDA call.
+ */
+int verify_attn_shared_groups(const int32_t* kv_indptr_h, const int32_t* kv_indices_h,
+                              const int32_t* qo_indptr_h, const int32_t* last_page_len_h, int batch,
+                              int page_size, int min_pages, int32_t* group_indptr_h,
+                              int32_t* shared_pages_h, int* num_groups);
+int verify_attn_plan_shared_bounds(int batch, int num_groups, int64_t total_qo, int num_qo_heads,
+                                   int num_kv_heads, int head_dim, int num_sms, size_t* plan_bytes,
+                                   size_t* workspace_bytes);
+int verify_attn_plan_shared_host(const int32_t* kv_indptr_h, const int32_t* qo_indptr_h,
+                                 const int32_t* last_page_len_h, const int32_t* mask_indptr_h,
+                                 int batch, const int32_t* group_indptr_h,
+                                 const int32_t* shared_pages_h, int num_groups, int num_qo_heads,
+                                 int num_kv_heads, int head_dim, int page_size, va_dtype q_dtype,
+                                 va_dtype kv_dtype, int has_mask, int num_sms,
+                                 const va_plan_options_t* options, void* plan_h, size_t plan_bytes,
+                                 size_t* workspace_bytes);
+
 /* Number of kernel launches verify_attn_run makes for this plan (1 or 2; 0
  * when the batch has no query token). */
 int verify_attn_plan_launches(const void* plan_h, int* launches);

@@ -33,6 +33,8 @@ __all__ = [
     "verify_attn_partial", "verify_attn_merge", "paged_kv_append",
     "verify_attn_device_status", "verify_attn_plan_bounds", "verify_attn_plan_host",
     "verify_attn_workspace_size", "verify_attn_run_static_scratch", "verify_attn_append_run",
+    "verify_attn_shared_groups", "verify_attn_plan_shared_bounds", "verify_attn_plan_shared_host",
+    "verify_attn_plan_shared",
     "verify_accept_greedy", "verify_accept_sample", "paged_kv_compact",
     "status_string", "num_sms", "KV_BF16", "KV_FP8_E4M3", "library_path",
 ]
@@ -139,6 +141,10 @@ def lib():
         "verify_accept_workspace_size": (i32, [i64, i32, i32, Psz]),
         "verify_accept_greedy": (i32, [P, i32, i64, i32, i64, P, i32, P, P, P, P, P, P, P, i32,
                                        P, sz, P]),
+        "verify_attn_shared_groups": (i32, [P, P, P, P, i32, i32, i32, P, P, Pi]),
+        "verify_attn_plan_shared_bounds": (i32, [i32, i32, i64, i32, i32, i32, i32, Psz, Psz]),
+        "verify_attn_plan_shared_host": (i32, [P, P, P, P, i32, P, P, i32, i32, i32, i32, i32, i32,
+                                               i32, i32, i32, P, P, sz, Psz]),
         "verify_accept_sample": (i32, [P, i32, i64, i32, i64, P, i32, P, P, P, P, i64, P, P, i32, i64,
                                        P, P, P, P, P, i32, P]),
         "paged_kv_compact": (i32, [P, P, P, i64, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32,
@@ -441,6 +447,87 @@ def verify_attn_plan(kv_indptr_h, qo_indptr_h, last_page_len_h, mask_indptr_h, n
     ws_bytes = int(host[136:144].view(np.uint64)[0])   # the header's workspace size
     return Plan(host, workspace, ws_bytes, batch, num_qo_heads, num_kv_heads, head_dim,
                 page_size, _kv_code(kv_dtype), bool(has_mask), total_qo)
+
+
+def verify_attn_shared_groups(kv_indptr_h, kv_indices_h, qo_indptr_h, last_page_len_h, page_size,
+                              min_pages=1):
+    """Groups of consecutive requests whose page lists start alike, from HOST
+    tables: (group_indptr, shared_pages), int32 numpy arrays for
+    verify_attn_plan_shared."""
+    kvp, ids, qop, lpl = (_host_i32(kv_indptr_h), _host_i32(kv_indices_h), _host_i32(qo_indptr_h),
+                          _host_i32(last_page_len_h))
+    batch = len(qop) - 1
+    if len(kvp) != batch + 1 or len(lpl) < batch or (batch > 0 and kvp[-1] > len(ids)):
+        raise ValueError("the host tables do not match")
+    groups, pages = np.zeros(batch + 1, np.int32), np.zeros(max(batch, 1), np.int32)
+    n = ctypes.c_int(0)
+    _check("verify_attn_shared_groups",
+           lib().verify_attn_shared_groups(_hp(kvp), _hp(ids), _hp(qop), _hp(lpl), batch,
+                                           int(page_size), int(min_pages), _hp(groups), _hp(pages),
+                                           ctypes.byref(n)))
+    return groups[:n.value + 1].copy(), pages[:n.value].copy()
+
+
+def verify_attn_plan_shared_bounds(batch, num_groups, total_qo, num_qo_heads, num_kv_heads, head_dim,
+                                   num_sms=0):
+    """(plan bytes, workspace bytes) that serve every plan of such a batch and its groups."""
+    pb, wb = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check("verify_attn_plan_shared_bounds",
+           lib().verify_attn_plan_shared_bounds(int(batch), int(num_groups), int(total_qo),
+                                                int(num_qo_heads), int(num_kv_heads), int(head_dim),
+                                                int(num_sms), ctypes.byref(pb), ctypes.byref(wb)))
+    return pb.value, wb.value
+
+
+def verify_attn_plan_shared_host(kv_indptr_h, qo_indptr_h, last_page_len_h, mask_indptr_h,
+                                 group_indptr_h, shared_pages_h, num_qo_heads, num_kv_heads, head_dim,
+                                 page_size, kv_dtype="bf16", has_mask=None, num_sms=0, **options) -> Plan:
+    """Host-only plan of a batch whose requests share prefixes (no CUDA call
+    when num_sms > 0): group g is requests group_indptr_h[g] ..
+    group_indptr_h[g + 1], whose first shared_pages_h[g] pages are the same."""
+    kvp, qop, lpl, mip, grp, shp = (_host_i32(a) for a in (kv_indptr_h, qo_indptr_h, last_page_len_h,
+                                                          mask_indptr_h, group_indptr_h, shared_pages_h))
+    batch, groups = len(qop) - 1, len(grp) - 1
+    if batch < 0 or groups < 0 or len(kvp) != batch + 1 or len(lpl) < batch or len(shp) != groups or \
+            (mip is not None and len(mip) != batch + 1):
+        raise ValueError("the host tables do not match")
+    if has_mask is None:
+        has_mask = mip is not None
+    total_qo = int(qop[-1])
+    if num_sms <= 0:
+        num_sms = globals()["num_sms"]()
+    pb, _ = verify_attn_plan_shared_bounds(batch, groups, max(total_qo, 0), num_qo_heads, num_kv_heads,
+                                           head_dim, num_sms)
+    host = np.zeros(pb, dtype=np.uint8)
+    need = ctypes.c_size_t(0)
+    tp, _keep = _tables(kvp, qop, lpl, mip, grp, shp)
+    rc = lib().verify_attn_plan_shared_host(
+        *tp[:4], batch, tp[4], tp[5], groups, int(num_qo_heads), int(num_kv_heads), int(head_dim),
+        int(page_size), 0, _kv_code(kv_dtype), int(bool(has_mask)), int(num_sms),
+        ctypes.byref(_options(**options)), _hp(host), host.nbytes, ctypes.byref(need))
+    _check("verify_attn_plan_shared_host", rc)
+    return Plan(host, None, need.value, batch, num_qo_heads, num_kv_heads, head_dim, page_size,
+                _kv_code(kv_dtype), bool(has_mask), total_qo)
+
+
+def verify_attn_plan_shared(kv_indptr_h, qo_indptr_h, last_page_len_h, mask_indptr_h, group_indptr_h,
+                            shared_pages_h, num_qo_heads, num_kv_heads, head_dim, page_size,
+                            kv_dtype="bf16", has_mask=None, workspace: Optional[torch.Tensor] = None,
+                            device=None, stream=None, num_sms=0, **options) -> Plan:
+    """verify_attn_plan for a batch whose requests share prefixes (see
+    verify_attn_plan_shared_host): the plan, uploaded to `workspace` (uint8,
+    at least the plan's workspace_bytes) or to one allocated here.  It runs
+    through verify_attn_run, verify_attn_append_run and the other run calls."""
+    plan = verify_attn_plan_shared_host(kv_indptr_h, qo_indptr_h, last_page_len_h, mask_indptr_h,
+                                        group_indptr_h, shared_pages_h, num_qo_heads, num_kv_heads,
+                                        head_dim, page_size, kv_dtype, has_mask, num_sms, **options)
+    if workspace is None:
+        workspace = torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=device or "cuda")
+    plan.workspace = workspace
+    _check("verify_attn_plan_upload",
+           lib().verify_attn_plan_upload(_hp_buf(plan.host), _dp(workspace),
+                                         workspace.numel() * workspace.element_size(), _stream(stream)))
+    return plan
 
 
 def _run_args(q, k_cache, v_cache, kv_indptr, kv_indices, last_page_len, qo_indptr, mask,

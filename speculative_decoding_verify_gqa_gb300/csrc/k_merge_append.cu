@@ -21,7 +21,11 @@ namespace {
 // split count -- enough to merge a row in one round trip, and no more, since
 // the loaded rows live in registers and the registers bound how many rows
 // are in flight.
-template <int D, int CH>
+//
+// SHARED (a plan with shared prefixes): the rows of a request in a group also
+// have the group's partials, laid out by the group's rows (see GroupRec); they
+// follow the request's own in the same loop.
+template <int D, int CH, bool SHARED>
 __global__ void __launch_bounds__(128) verify_merge_kernel(const MergeParams p) {
   constexpr int V = D / 32;
   // After this library's split kernel in an append-and-run call, the merge
@@ -40,16 +44,30 @@ __global__ void __launch_bounds__(128) verify_merge_kernel(const MergeParams p) 
   const int qo0 = item_ok ? p.qo_indptr[it.b] : 0;
   const bool row_ok = item_ok && r < it.nrows &&
                       (it.row0 + r) / p.group < p.qo_indptr[it.b + 1] - qo0;
+  // the group's partials of this row: split s at group_row + s * group_rows
+  int group_splits = 0, group_rows = 0;
+  long long group_row = 0;
+  if (SHARED && row_ok && it.group > 0 && it.group <= p.n_groups) {
+    const GroupRec gr = p.groups[it.group - 1];
+    if (gr.r0 >= 0 && gr.r0 <= it.b && it.b < gr.r1 && gr.nsplit > 0 && gr.part_row0 >= 0) {
+      const long long rg = (long long)(qo0 - p.qo_indptr[gr.r0]) * p.group + it.row0 + r;
+      group_row = gr.part_row0 + (long long)it.h * gr.nsplit * gr.rows + rg;
+      if (rg >= 0 && rg < gr.rows && group_row + (long long)(gr.nsplit - 1) * gr.rows < p.part_rows) {
+        group_splits = gr.nsplit;
+        group_rows = gr.rows;
+      }
+    }
+  }
   // the partials come from the preceding split kernel; every thread waits,
   // so that this grid's completion implies that kernel's
   grid_dependency_wait();
   if (!row_ok) return;
-  const float* lse_base = p.part_lse + it.part_row0 + r;
   float m = -INFINITY, den = 0.f;
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (int s0 = 0; s0 < it.nsplit; s0 += CH) {
+  const int n_parts = it.nsplit + group_splits;
+  for (int s0 = 0; s0 < n_parts; s0 += CH) {
     float ls[CH];
     float x[CH][V];
 #pragma unroll
@@ -58,9 +76,11 @@ __global__ void __launch_bounds__(128) verify_merge_kernel(const MergeParams p) 
       ls[c] = -INFINITY;
 #pragma unroll
       for (int i = 0; i < V; ++i) x[c][i] = 0.f;
-      if (s < it.nsplit) {
-        ls[c] = lse_base[(size_t)s * it.nrows];
-        const float* src = p.part_out + ((size_t)it.part_row0 + (size_t)s * it.nrows + r) * D + lane * V;
+      if (s < n_parts) {
+        size_t prow = (size_t)it.part_row0 + (size_t)s * it.nrows + r;
+        if (SHARED && s >= it.nsplit) prow = (size_t)group_row + (size_t)(s - it.nsplit) * group_rows;
+        ls[c] = p.part_lse[prow];
+        const float* src = p.part_out + prow * D + lane * V;
         if constexpr (V == 4) {
           const float4 v = *reinterpret_cast<const float4*>(src);
           x[c][0] = v.x; x[c][1] = v.y; x[c][2] = v.z; x[c][3] = v.w;
@@ -258,22 +278,27 @@ __global__ void __launch_bounds__(256) paged_kv_append_kernel(const AppendParams
 
 }  // namespace
 
-template <int D>
+template <int D, bool SHARED>
 static cudaError_t launch_merge_d(const MergeParams& p, int n_merge, int block_rows,
                                   int max_nsplit, cudaStream_t stream) {
   dim3 grid(n_merge, (block_rows + 3) / 4);
   void* args[] = {const_cast<MergeParams*>(&p)};
-  const void* k = max_nsplit <= 4   ? reinterpret_cast<const void*>(verify_merge_kernel<D, 4>)
-                  : max_nsplit <= 8 ? reinterpret_cast<const void*>(verify_merge_kernel<D, 8>)
-                                    : reinterpret_cast<const void*>(verify_merge_kernel<D, 24>);
+  const void* k = max_nsplit <= 4   ? reinterpret_cast<const void*>(verify_merge_kernel<D, 4, SHARED>)
+                  : max_nsplit <= 8 ? reinterpret_cast<const void*>(verify_merge_kernel<D, 8, SHARED>)
+                                    : reinterpret_cast<const void*>(verify_merge_kernel<D, 24, SHARED>);
   return launch_kernel(k, grid, dim3(128), 0, stream, args, /*pdl=*/true);
 }
 
 cudaError_t launch_merge(const MergeParams& p, int head_dim, int n_merge, int block_rows,
                          int max_nsplit, cudaStream_t stream) {
   if (n_merge <= 0) return cudaSuccess;
-  if (head_dim == 128) return launch_merge_d<128>(p, n_merge, block_rows, max_nsplit, stream);
-  if (head_dim == 64) return launch_merge_d<64>(p, n_merge, block_rows, max_nsplit, stream);
+  const bool shared = p.n_groups > 0;
+  if (head_dim == 128)
+    return shared ? launch_merge_d<128, true>(p, n_merge, block_rows, max_nsplit, stream)
+                  : launch_merge_d<128, false>(p, n_merge, block_rows, max_nsplit, stream);
+  if (head_dim == 64)
+    return shared ? launch_merge_d<64, true>(p, n_merge, block_rows, max_nsplit, stream)
+                  : launch_merge_d<64, false>(p, n_merge, block_rows, max_nsplit, stream);
   return cudaErrorInvalidValue;
 }
 

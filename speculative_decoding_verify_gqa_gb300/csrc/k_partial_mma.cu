@@ -75,15 +75,28 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
   // Request geometry, from the device tables the caller passed (nothing is
   // read for a work item that names a request or head outside this call's
   // tables, as one left in the workspace by another plan may).
-  const bool idx_ok = b >= 0 && b < p.batch && h >= 0 && h < p.h_kv;
-  const int qo0 = idx_ok ? p.qo_indptr[b] : 0;
-  const int L = idx_ok ? p.qo_indptr[b + 1] - qo0 : -1;
-  const int pg0 = idx_ok ? p.kv_indptr[b] : 0;
-  const int npg = idx_ok ? p.kv_indptr[b + 1] - pg0 : -1;
-  const int lpl = npg > 0 ? p.last_page_len[b] : 1;
+  bool idx_ok = b >= 0 && b < p.batch && h >= 0 && h < p.h_kv;
+  int r0 = b, r1 = b + 1;  // requests whose rows the item holds
+  // an item of a group with a shared prefix: every row of its requests
+  // against the leading pages of its first, all of them visible
+  const bool shared = p.n_groups > 0 && b >= p.batch && b - p.batch < p.n_groups && h >= 0 && h < p.h_kv;
+  int gpages = 0;
+  if (shared) {
+    const GroupRec gr = p.groups[b - p.batch];
+    r0 = gr.r0;
+    r1 = gr.r1;
+    gpages = gr.pages;
+    idx_ok = r0 >= 0 && r0 < r1 && r1 <= p.batch && gpages >= 0;
+  }
+  const int qo0 = idx_ok ? p.qo_indptr[r0] : 0;
+  const int L = idx_ok ? p.qo_indptr[r1] - qo0 : -1;
+  const int pg0 = idx_ok ? p.kv_indptr[r0] : 0;
+  int npg = idx_ok ? p.kv_indptr[r0 + 1] - pg0 : -1;
+  if (shared) npg = gpages <= npg ? gpages : -1;
+  const int lpl = shared ? p.page_size : npg > 0 ? p.last_page_len[r0] : 1;
   const long long kv_len_ll = npg > 0 ? (long long)(npg - 1) * p.page_size + lpl : 0;
   const int kv_len = (int)kv_len_ll;
-  const int prefix = kv_len - L;
+  const int prefix = shared ? kv_len : kv_len - L;
   const bool ok = L >= 0 && npg >= 0 && lpl >= 1 && lpl <= p.page_size && prefix >= 0 &&
                   it.row0 >= 0 && it.nrows > 0 && it.nrows <= C::BM &&
                   (long long)it.row0 + it.nrows <= (long long)G * L && it.kv_lo >= 0 &&
@@ -212,7 +225,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
   // keys past it are masked for every row of the warp (causal drafts only: a
   // custom mask may open later drafts)
   const int warp_kv_end = p.mask ? kv_len : prefix + (row0 + w_last) / G + 1;
-  const int moff = p.mask ? p.mask_indptr[b] : 0;
+  const int moff = p.mask && !shared ? p.mask_indptr[b] : 0;
   const float sl2 = p.scale_log2;
 
   uint32_t qa[D / 16][4];

@@ -150,21 +150,35 @@ __device__ __forceinline__ ItemGeo decode_item(const PartialParams& p, int i) {
   g.part_row = it.part_row;
   // a work list left in the workspace by another plan may name requests
   // past this call's tables: nothing is read for those
-  const bool idx_ok = g.b >= 0 && g.b < p.batch && g.h >= 0 && g.h < p.h_kv;
-  g.qo0 = idx_ok ? p.qo_indptr[g.b] : 0;
-  g.L = idx_ok ? p.qo_indptr[g.b + 1] - g.qo0 : -1;
-  g.pg0 = idx_ok ? p.kv_indptr[g.b] : 0;
-  const int npg = idx_ok ? p.kv_indptr[g.b + 1] - g.pg0 : -1;
-  const int lpl = npg > 0 ? p.last_page_len[g.b] : 1;
+  bool idx_ok = g.b >= 0 && g.b < p.batch && g.h >= 0 && g.h < p.h_kv;
+  int r0 = g.b, r1 = g.b + 1;  // requests whose rows the item holds
+  // an item of a group with a shared prefix: every row of its requests
+  // against the leading pages of its first, all of them visible
+  const bool shared = p.n_groups > 0 && g.b >= p.batch && g.b - p.batch < p.n_groups && g.h >= 0 && g.h < p.h_kv;
+  int pages = 0;
+  if (shared) {
+    const GroupRec gr = p.groups[g.b - p.batch];
+    r0 = gr.r0;
+    r1 = gr.r1;
+    pages = gr.pages;
+    idx_ok = r0 >= 0 && r0 < r1 && r1 <= p.batch && pages >= 0;
+  }
+  g.qo0 = idx_ok ? p.qo_indptr[r0] : 0;
+  g.L = idx_ok ? p.qo_indptr[r1] - g.qo0 : -1;
+  g.pg0 = idx_ok ? p.kv_indptr[r0] : 0;
+  int npg = idx_ok ? p.kv_indptr[r0 + 1] - g.pg0 : -1;
+  if (shared) npg = pages <= npg ? pages : -1;
+  const int lpl = shared ? p.page_size : npg > 0 ? p.last_page_len[r0] : 1;
   const long long kv_len = npg > 0 ? (long long)(npg - 1) * p.page_size + lpl : 0;
-  g.prefix = (int)kv_len - g.L;
+  g.prefix = shared ? (int)kv_len : (int)kv_len - g.L;
   g.ok = g.L >= 0 && npg >= 0 && lpl >= 1 && lpl <= p.page_size && kv_len <= 0x7fffffffLL &&
          g.prefix >= 0 && g.row0 >= 0 && g.nrows > 0 && g.nrows <= BLOCK_ROWS &&
          g.row0 % BLOCK_ROWS == 0 && (long long)g.row0 + g.nrows <= (long long)p.group * g.L &&
          g.lov >= 0 && g.lov < g.hi && g.hi <= kv_len &&
          (g.part_row < 0 || (long long)g.part_row + g.nrows <= p.part_rows);
   g.n_tiles = g.ok ? (g.hi - g.lo + KEYS - 1) / KEYS : 0;
-  g.moff = g.ok && p.mask ? p.mask_indptr[g.b] : 0;
+  g.moff = g.ok && !shared && p.mask ? p.mask_indptr[g.b] : 0;
+  if (shared && g.ok) g.L = 0;  // no draft column: the mask is not read
   g.nq = (g.nrows + ROWS - 1) / ROWS;  // live Q tiles (1 .. NQ)
   return g;
 }

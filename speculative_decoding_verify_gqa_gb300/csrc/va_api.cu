@@ -23,6 +23,17 @@ int plan_host(const int32_t* kv_indptr, const int32_t* qo_indptr, const int32_t*
               int head_dim, int page_size, int q_dtype, int kv_dtype, int has_mask, int num_sms,
               const va_plan_options_t* opts, void* plan_h, size_t plan_bytes,
               size_t* workspace_bytes);
+int shared_groups(const int32_t* kv_indptr, const int32_t* kv_indices, const int32_t* qo_indptr,
+                  const int32_t* last_page_len, int batch, int page_size, int min_pages,
+                  int32_t* group_indptr, int32_t* shared_pages, int* num_groups);
+int plan_shared_bounds(int batch, int num_groups, int64_t total_qo, int num_qo_heads, int num_kv_heads,
+                       int head_dim, int num_sms, size_t* plan_bytes, size_t* workspace_bytes);
+int plan_shared_host(const int32_t* kv_indptr, const int32_t* qo_indptr, const int32_t* last_page_len,
+                     const int32_t* mask_indptr, int batch, const int32_t* group_indptr,
+                     const int32_t* shared_pages, int num_groups, int num_qo_heads, int num_kv_heads,
+                     int head_dim, int page_size, int q_dtype, int kv_dtype, int has_mask, int num_sms,
+                     const va_plan_options_t* opts, void* plan_h, size_t plan_bytes,
+                     size_t* workspace_bytes);
 }  // namespace va
 
 using namespace va;
@@ -135,6 +146,8 @@ PartialParams make_partial(const void* q, const void* k_cache, const void* v_cac
   p.part_lse = reinterpret_cast<float*>(ws + hd->off_part_lse);
   p.status = reinterpret_cast<int*>(ws + hd->off_status);
   p.batch = hd->batch;
+  p.groups = reinterpret_cast<const GroupRec*>(ws + hd->off_merge + (size_t)hd->n_merge * sizeof(MergeItem));
+  p.n_groups = plan_groups(*hd);
   p.part_rows = hd->part_rows;
   p.h_q = hd->h_q;
   p.h_kv = hd->h_kv;
@@ -294,6 +307,8 @@ static int verify_attn_merge_impl(const int32_t* qo_indptr, int num_qo_heads, in
   m.h_kv = hd->h_kv;
   m.group = hd->group;
   m.early_inputs = early;
+  m.groups = reinterpret_cast<const GroupRec*>(ws + hd->off_merge + (size_t)hd->n_merge * sizeof(MergeItem));
+  m.n_groups = plan_groups(*hd);
   cudaError_t e = launch_merge(m, (int)hd->head_dim_v, hd->n_merge, hd->block_rows,
                                (int)hd->max_nsplit,
                                static_cast<cudaStream_t>(stream));
@@ -414,6 +429,42 @@ int verify_attn_plan(const int32_t* kv_indptr_h, const int32_t* qo_indptr_h,
   return verify_attn_plan_upload(plan_h, workspace_d, workspace_bytes, stream);
 }
 
+int verify_attn_shared_groups(const int32_t* kv_indptr_h, const int32_t* kv_indices_h,
+                              const int32_t* qo_indptr_h, const int32_t* last_page_len_h, int batch,
+                              int page_size, int min_pages, int32_t* group_indptr_h,
+                              int32_t* shared_pages_h, int* num_groups) {
+  return shared_groups(kv_indptr_h, kv_indices_h, qo_indptr_h, last_page_len_h, batch, page_size, min_pages,
+                       group_indptr_h, shared_pages_h, num_groups);
+}
+
+int verify_attn_plan_shared_bounds(int batch, int num_groups, int64_t total_qo, int num_qo_heads,
+                                   int num_kv_heads, int head_dim, int num_sms, size_t* plan_bytes,
+                                   size_t* workspace_bytes) {
+  if (num_sms <= 0) {
+    int rc = query_sms(&num_sms);
+    if (rc) return rc;
+  }
+  return plan_shared_bounds(batch, num_groups, total_qo, num_qo_heads, num_kv_heads, head_dim, num_sms,
+                            plan_bytes, workspace_bytes);
+}
+
+int verify_attn_plan_shared_host(const int32_t* kv_indptr_h, const int32_t* qo_indptr_h,
+                                 const int32_t* last_page_len_h, const int32_t* mask_indptr_h,
+                                 int batch, const int32_t* group_indptr_h,
+                                 const int32_t* shared_pages_h, int num_groups, int num_qo_heads,
+                                 int num_kv_heads, int head_dim, int page_size, va_dtype q_dtype,
+                                 va_dtype kv_dtype, int has_mask, int num_sms,
+                                 const va_plan_options_t* options, void* plan_h, size_t plan_bytes,
+                                 size_t* workspace_bytes) {
+  if (num_sms <= 0) {
+    int rc = query_sms(&num_sms);
+    if (rc) return rc;
+  }
+  return plan_shared_host(kv_indptr_h, qo_indptr_h, last_page_len_h, mask_indptr_h, batch, group_indptr_h,
+                          shared_pages_h, num_groups, num_qo_heads, num_kv_heads, head_dim, page_size, q_dtype,
+                          kv_dtype, has_mask, num_sms, options, plan_h, plan_bytes, workspace_bytes);
+}
+
 int verify_attn_plan_upload(const void* plan_h, void* workspace_d, size_t workspace_bytes,
                             void* stream) {
   const PlanHeader* hd = plan_header(plan_h);
@@ -423,7 +474,7 @@ int verify_attn_plan_upload(const void* plan_h, void* workspace_d, size_t worksp
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace_d);
   if (cudaMemsetAsync(ws + hd->off_status, 0, sizeof(int), s) != cudaSuccess) return VA_ERR_CUDA;
-  size_t list = (size_t)hd->n_items * sizeof(WorkItem) + (size_t)hd->n_merge * sizeof(MergeItem);
+  const size_t list = plan_list_bytes(*hd);
   if (list > 0 &&
       cudaMemcpyAsync(ws + hd->off_items, static_cast<const char*>(plan_h) + sizeof(PlanHeader),
                       list, cudaMemcpyHostToDevice, s) != cudaSuccess)
@@ -590,8 +641,7 @@ int verify_attn_run_static_scratch(const void* q, const void* k_cache, const voi
   char* ws = static_cast<char*>(scratch);
   // the status word starts at zero; the work list comes from this plan
   if (cudaMemsetAsync(ws + hd->off_status, 0, sizeof(int), s) != cudaSuccess) return VA_ERR_CUDA;
-  const size_t list =
-      (size_t)hd->n_items * sizeof(WorkItem) + (size_t)hd->n_merge * sizeof(MergeItem);
+  const size_t list = plan_list_bytes(*hd);
   if (list > 0 &&
       cudaMemcpyAsync(ws + hd->off_items, static_cast<const char*>(plan_h) + sizeof(PlanHeader),
                       list, cudaMemcpyHostToDevice, s) != cudaSuccess)

@@ -48,21 +48,35 @@ struct WorkItem {
 static_assert(sizeof(WorkItem) == 32, "WorkItem layout");
 
 // One split unit to merge: nsplit partials of nrows rows each, split s at
-// part rows part_row0 + s * nrows.
+// part rows part_row0 + s * nrows; group > 0: and the partials of group
+// group - 1 (a plan with shared prefixes).
 struct MergeItem {
   int32_t b, h, row0, nrows;
-  int32_t part_row0, nsplit, pad0, pad1;
+  int32_t part_row0, nsplit, group, pad1;
 };
 static_assert(sizeof(MergeItem) == 32, "MergeItem layout");
 
+// A group of a plan with shared prefixes: requests r0 .. r1 - 1, whose first
+// `pages` pages are those of request r0.  rows > 0: the group's rows (all of
+// its requests' G * L_b rows, in q's order) have work items of their own over
+// the shared keys, WorkItem::b = batch + group, nsplit partials a row: row r
+// of KV head h in split s at part row part_row0 + (h * nsplit + s) * rows + r.
+struct GroupRec {
+  int32_t r0, r1, pages, rows;
+  int32_t part_row0, nsplit, pad0, pad1;
+};
+static_assert(sizeof(GroupRec) == 32, "GroupRec layout");
+
 // Host plan buffer: PlanHeader, then n_items WorkItems, then n_merge
-// MergeItems.  The WorkItems and MergeItems are uploaded verbatim to the
+// MergeItems, then plan_groups() GroupRecs.  They are uploaded verbatim to the
 // device workspace at off_items.
 // PlanHeader::flags: the call features the plan was made for.
 constexpr int64_t kPlanMaskFull = 1;  // mask rows of kv_len bits (prefix included)
 constexpr int64_t kPlanNhd = 2;       // cache layout [pages, P, h_kv, d]
 constexpr int64_t kPlanRope = 4;      // queries rotated at their positions
 constexpr int64_t kPlanF8Mma = 8;     // e4m3 MMAs: queries quantised per row, P as e4m3
+
+constexpr int kPlanGroupShift = 32;   // the bits above: number of GroupRecs
 
 struct PlanHeader {
   uint32_t magic, version;
@@ -78,6 +92,13 @@ struct PlanHeader {
   int64_t max_nsplit;  // largest split count of a merge item (0: no merges)
 };
 static_assert(sizeof(PlanHeader) == 184, "PlanHeader layout (read by the Python binding)");
+
+inline int plan_groups(const PlanHeader& h) { return (int)(h.flags >> kPlanGroupShift); }
+// bytes of the records after the header
+inline size_t plan_list_bytes(const PlanHeader& h) {
+  return (size_t)h.n_items * sizeof(WorkItem) + (size_t)h.n_merge * sizeof(MergeItem) +
+         (size_t)plan_groups(h) * sizeof(GroupRec);
+}
 
 constexpr size_t kWsAlign = 256;
 constexpr int kMaxHeadDimV = 128;  // widest value row a plan may have

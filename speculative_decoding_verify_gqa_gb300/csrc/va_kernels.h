@@ -33,7 +33,10 @@ struct PartialParams {
   float* part_out;            // [part_rows, D]
   float* part_lse;            // [part_rows]
   int* status;                // device status word
-  int batch;                  // requests in the plan: a work item's b must be below it
+  int batch;                  // requests in the plan: a work item's b must be below it, or
+                              // below batch + n_groups (a group's item)
+  const GroupRec* groups;     // shared prefixes
+  int n_groups;
   int64_t part_rows;          // partial rows in the workspace: a split item's rows lie below
   int h_q, h_kv, group, page_size, log2_page, num_pages;
   float scale_log2;           // sm_scale * k_scale * log2(e)
@@ -64,6 +67,8 @@ struct MergeParams {
   int64_t part_rows;          // partial rows in the workspace
   int batch, h_q, h_kv, group;
   int early_inputs;           // 1: the merge list and qo_indptr may be read before the wait
+  const GroupRec* groups;     // shared prefixes
+  int n_groups;
 };
 
 struct AppendParams {

@@ -23,22 +23,119 @@
 
 #include "../../include/verify_attn.h"
 #include "va_internal.h"
+#include "va_planner.h"
 
 namespace va {
 
 namespace {
 
-constexpr int kMaxTargetPerSm = 4;
-
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Unit {
   int32_t b, row0, nrows, kv_end;
 };
 
 }  // namespace
+
+void sort_items(std::vector<PlanItem>& items) {
+  // sorted as 24-byte keys (cost descending, then b, h, kv_lo, row0, all
+  // non-negative here) and the items permuted once
+  struct Key {
+    uint64_t k0, k1, k2;
+    uint32_t idx;
+  };
+  std::vector<Key> keys(items.size());
+  for (size_t i = 0; i < items.size(); ++i) {
+    const WorkItem& w = items[i].it;
+    keys[i] = {~(uint64_t)items[i].cost, ((uint64_t)(uint32_t)w.b << 32) | (uint32_t)w.h,
+               ((uint64_t)(uint32_t)w.kv_lo << 32) | (uint32_t)w.row0, (uint32_t)i};
+  }
+  std::sort(keys.begin(), keys.end(), [](const Key& a, const Key& b) {
+    if (a.k0 != b.k0) return a.k0 < b.k0;
+    if (a.k1 != b.k1) return a.k1 < b.k1;
+    return a.k2 < b.k2;
+  });
+  std::vector<PlanItem> sorted(items.size());
+  for (size_t i = 0; i < keys.size(); ++i) sorted[i] = items[keys[i].idx];
+  items.swap(sorted);
+}
+
+int64_t deal_chains(std::vector<PlanItem>& items, int num_sms, int TK) {
+  const int64_t n_ctas = std::min<int64_t>((int64_t)items.size(), num_sms);
+  if ((int64_t)items.size() <= n_ctas) {
+    // one item per CTA: item c is chain c
+    for (auto& t : items) t.it.next = -1;
+  } else {
+    // LPT: each item (longest first) to the least-loaded chain, the
+    // lowest chain index among equal loads; then the items are laid out
+    // chain by chain (a counting sort on the owner), chain c's first at
+    // index c.  The chain loads are kept as levels (load -> its chains,
+    // ascending), and a run of items of equal increment is dealt a level
+    // at a time: the lowest level's chains take the next items in index
+    // order and move up together -- the same owners as dealing the items
+    // one by one from a min-heap of (load, chain).
+    // key tiles plus one of overhead; a tile of two Q tiles costs 5/3 of one
+    auto inc = [&](const WorkItem& w) -> int64_t {
+      return (ceil_div(w.kv_hi - w.kv_lo, TK) + 1) * (w.nrows > kTcRowsPerTile ? 5 : 3);
+    };
+    std::map<int64_t, std::vector<int32_t>> levels;
+    {
+      std::vector<int32_t>& all = levels[0];
+      all.resize((size_t)n_ctas);
+      for (int64_t c = 0; c < n_ctas; ++c) all[(size_t)c] = (int32_t)c;
+    }
+    std::vector<int32_t> owner(items.size()), moved, merged;
+    for (size_t i = 0; i < items.size();) {
+      const int64_t x = inc(items[i].it);
+      size_t run = 1;
+      while (i + run < items.size() && inc(items[i + run].it) == x) ++run;
+      while (run > 0) {
+        auto lo = levels.begin();
+        const int64_t level = lo->first;
+        std::vector<int32_t>& ids = lo->second;
+        const size_t take = std::min(run, ids.size());
+        for (size_t t = 0; t < take; ++t) owner[i++] = ids[t];
+        moved.assign(ids.begin(), ids.begin() + (std::ptrdiff_t)take);
+        if (take == ids.size()) levels.erase(lo);
+        else ids.erase(ids.begin(), ids.begin() + (std::ptrdiff_t)take);
+        std::vector<int32_t>& up = levels[level + x];
+        if (up.empty()) {
+          up.swap(moved);
+        } else {
+          merged.resize(up.size() + moved.size());
+          std::merge(up.begin(), up.end(), moved.begin(), moved.end(), merged.begin());
+          up.swap(merged);
+        }
+        run -= take;
+      }
+    }
+    // chain c: its first item at index c, the rest after all the firsts, in
+    // chain order, each linked to the next
+    std::vector<int32_t> count((size_t)n_ctas, 0), first((size_t)n_ctas, -1);
+    for (size_t i = 0; i < items.size(); ++i) ++count[(size_t)owner[i]];
+    std::vector<int64_t> start((size_t)n_ctas + 1, 0);  // of the chains' tails
+    for (int64_t c = 0; c < n_ctas; ++c) start[(size_t)c + 1] = start[(size_t)c] + count[(size_t)c] - 1;
+    std::vector<PlanItem> out(items.size());
+    std::vector<int64_t> fill(start.begin(), start.end() - 1);
+    std::vector<int32_t> last((size_t)n_ctas, -1);
+    for (size_t i = 0; i < items.size(); ++i) {
+      const int32_t c = owner[i];
+      int64_t pos;
+      if (first[(size_t)c] < 0) {
+        pos = c;
+        first[(size_t)c] = c;
+      } else {
+        pos = n_ctas + fill[(size_t)c]++;
+      }
+      out[(size_t)pos] = items[i];
+      out[(size_t)pos].it.next = -1;
+      if (last[(size_t)c] >= 0) out[(size_t)last[(size_t)c]].it.next = (int32_t)pos;
+      last[(size_t)c] = (int32_t)pos;
+    }
+    items.swap(out);
+  }
+  return n_ctas;
+}
 
 int check_common(int num_qo_heads, int num_kv_heads, int head_dim, int page_size, int q_dtype,
                  int kv_dtype) {
@@ -305,11 +402,7 @@ int plan_host(const int32_t* kv_indptr, const int32_t* qo_indptr, const int32_t*
     best_lpt = best;
   }
 
-  struct Tmp {
-    WorkItem it;
-    int64_t cost;
-  };
-  std::vector<Tmp> items;
+  std::vector<PlanItem> items;
   std::vector<MergeItem> merges;
   int64_t part_rows = 0;
   std::vector<int64_t> cuts;
@@ -349,7 +442,7 @@ int plan_host(const int32_t* kv_indptr, const int32_t* qo_indptr, const int32_t*
     if ((double)finish < best_lpt * 0.97) {
       stream = true;
       n_ctas = n;
-      std::vector<std::vector<Tmp>> runs;  // pieces of each run, in order (one plan's worth)
+      std::vector<std::vector<PlanItem>> runs;  // pieces of each run, in order (one plan's worth)
       runs.resize((size_t)n);
       g = 0;
       c = 0;
@@ -467,107 +560,14 @@ int plan_host(const int32_t* kv_indptr, const int32_t* qo_indptr, const int32_t*
   // later ones find the chunk in L2.  (b, h, kv_lo, row0) identifies an item,
   // so the order is total.
   if (!stream) {
-    // sorted as 24-byte keys (cost descending, then b, h, kv_lo, row0, all
-    // non-negative here) and the items permuted once
-    struct Key {
-      uint64_t k0, k1, k2;
-      uint32_t idx;
-    };
-    std::vector<Key> keys(items.size());
-    for (size_t i = 0; i < items.size(); ++i) {
-      const WorkItem& w = items[i].it;
-      keys[i] = {~(uint64_t)items[i].cost, ((uint64_t)(uint32_t)w.b << 32) | (uint32_t)w.h,
-                 ((uint64_t)(uint32_t)w.kv_lo << 32) | (uint32_t)w.row0, (uint32_t)i};
-    }
-    std::sort(keys.begin(), keys.end(), [](const Key& a, const Key& b) {
-      if (a.k0 != b.k0) return a.k0 < b.k0;
-      if (a.k1 != b.k1) return a.k1 < b.k1;
-      return a.k2 < b.k2;
-    });
-    std::vector<Tmp> sorted(items.size());
-    for (size_t i = 0; i < keys.size(); ++i) sorted[i] = items[keys[i].idx];
-    items.swap(sorted);
+    sort_items(items);
   }
 
   // Persistent tcgen05 variants: one CTA per SM walks a chain of items.  The
   // longest-first list is dealt onto the CTAs by LPT (each item to the
   // least-loaded CTA, with a per-item overhead of one key tile), chain c's
   // first item is put at index c and the rest follow, linked through next.
-  if (!stream && kernel_is_tc(kernel) && !items.empty()) {
-    n_ctas = std::min<int64_t>((int64_t)items.size(), num_sms);
-    if ((int64_t)items.size() <= n_ctas) {
-      // one item per CTA: item c is chain c
-      for (auto& t : items) t.it.next = -1;
-    } else {
-      // LPT: each item (longest first) to the least-loaded chain, the
-      // lowest chain index among equal loads; then the items are laid out
-      // chain by chain (a counting sort on the owner), chain c's first at
-      // index c.  The chain loads are kept as levels (load -> its chains,
-      // ascending), and a run of items of equal increment is dealt a level
-      // at a time: the lowest level's chains take the next items in index
-      // order and move up together -- the same owners as dealing the items
-      // one by one from a min-heap of (load, chain).
-      // key tiles plus one of overhead; a tile of two Q tiles costs 5/3 of one
-      auto inc = [&](const WorkItem& w) -> int64_t {
-        return (ceil_div(w.kv_hi - w.kv_lo, TK) + 1) * (w.nrows > kTcRowsPerTile ? 5 : 3);
-      };
-      std::map<int64_t, std::vector<int32_t>> levels;
-      {
-        std::vector<int32_t>& all = levels[0];
-        all.resize((size_t)n_ctas);
-        for (int64_t c = 0; c < n_ctas; ++c) all[(size_t)c] = (int32_t)c;
-      }
-      std::vector<int32_t> owner(items.size()), moved, merged;
-      for (size_t i = 0; i < items.size();) {
-        const int64_t x = inc(items[i].it);
-        size_t run = 1;
-        while (i + run < items.size() && inc(items[i + run].it) == x) ++run;
-        while (run > 0) {
-          auto lo = levels.begin();
-          const int64_t level = lo->first;
-          std::vector<int32_t>& ids = lo->second;
-          const size_t take = std::min(run, ids.size());
-          for (size_t t = 0; t < take; ++t) owner[i++] = ids[t];
-          moved.assign(ids.begin(), ids.begin() + (std::ptrdiff_t)take);
-          if (take == ids.size()) levels.erase(lo);
-          else ids.erase(ids.begin(), ids.begin() + (std::ptrdiff_t)take);
-          std::vector<int32_t>& up = levels[level + x];
-          if (up.empty()) {
-            up.swap(moved);
-          } else {
-            merged.resize(up.size() + moved.size());
-            std::merge(up.begin(), up.end(), moved.begin(), moved.end(), merged.begin());
-            up.swap(merged);
-          }
-          run -= take;
-        }
-      }
-      // chain c: its first item at index c, the rest after all the firsts, in
-      // chain order, each linked to the next
-      std::vector<int32_t> count((size_t)n_ctas, 0), first((size_t)n_ctas, -1);
-      for (size_t i = 0; i < items.size(); ++i) ++count[(size_t)owner[i]];
-      std::vector<int64_t> start((size_t)n_ctas + 1, 0);  // of the chains' tails
-      for (int64_t c = 0; c < n_ctas; ++c) start[(size_t)c + 1] = start[(size_t)c] + count[(size_t)c] - 1;
-      std::vector<Tmp> out(items.size());
-      std::vector<int64_t> fill(start.begin(), start.end() - 1);
-      std::vector<int32_t> last((size_t)n_ctas, -1);
-      for (size_t i = 0; i < items.size(); ++i) {
-        const int32_t c = owner[i];
-        int64_t pos;
-        if (first[(size_t)c] < 0) {
-          pos = c;
-          first[(size_t)c] = c;
-        } else {
-          pos = n_ctas + fill[(size_t)c]++;
-        }
-        out[(size_t)pos] = items[i];
-        out[(size_t)pos].it.next = -1;
-        if (last[(size_t)c] >= 0) out[(size_t)last[(size_t)c]].it.next = (int32_t)pos;
-        last[(size_t)c] = (int32_t)pos;
-      }
-      items.swap(out);
-    }
-  }
+  if (!stream && kernel_is_tc(kernel) && !items.empty()) n_ctas = deal_chains(items, num_sms, TK);
 
   size_t need = sizeof(PlanHeader) + items.size() * sizeof(WorkItem) +
                 merges.size() * sizeof(MergeItem);
