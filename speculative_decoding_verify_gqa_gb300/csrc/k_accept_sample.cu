@@ -19,9 +19,14 @@
 // reduction enters the result.
 //
 // One cluster of CTAs per request walks its tree, each CTA on its slice of
-// the vocabulary, so a step is one pass over the node's row and one exchange
-// through distributed shared memory.  Rows of nodes that are not accepted are
-// never read: a 64-node tree whose path is two nodes long reads two rows.
+// the vocabulary.  A pass reads the rows of the current node and of its first
+// child, that one's first child and so on (kRows of them at most), since a walk
+// is a chain of dependent steps -- load, reduce, exchange, decide -- whose
+// latency and not its bytes sets the time: the rows of a pass share one
+// exchange through distributed shared memory, and a warp for each decides about
+// its children at the same time.  The walk then follows the decisions as far as
+// they lead along those rows.  Rows further off are read only when the walk
+// gets there, so a 64-node tree whose path is two nodes long reads four rows.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -36,7 +41,10 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kRows = 4;        // rows of a pass at most
 constexpr int kChildList = 64;  // children's tokens kept in shared memory (further ones are searched)
+constexpr int kMarks = 32;
+constexpr int kNodes = 128;     // a tree of at most so many nodes is kept in shared memory
 
 __device__ __forceinline__ uint64_t race_key(float v, uint32_t idx) {  // v >= 0
   return ((uint64_t)(__float_as_uint(v) | 0x80000000u) << 32) | (uint64_t)(0xffffffffu - idx);
@@ -52,8 +60,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+  cluster_arrive();
+  cluster_wait();
 }
 // Store 8 bytes at shared address `addr` (of this CTA) in the shared memory
 // of CTA `cta` of the cluster.
@@ -61,6 +72,21 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t cta, uint6
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(cta));
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+
+// Ask for [p, p + bytes) to be brought into L2, rounded inwards to 16 bytes:
+// one instruction, by one thread.
+__device__ __forceinline__ void prefetch_l2(const void* p, int64_t bytes) {
+  const uintptr_t a = (reinterpret_cast<uintptr_t>(p) + 15) & ~(uintptr_t)15,
+                  z = (reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes) & ~(uintptr_t)15;
+  if (z > a)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"((uint32_t)(z - a)) : "memory");
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 template <bool BF16>
@@ -90,14 +116,53 @@ __device__ __forceinline__ void load8(const void* row, int64_t i, float* x) {
   }
 }
 
-struct Shared {
-  uint64_t warp_a[kWarps], warp_b[kWarps];
-  uint64_t ex_a[2][kMaxCluster], ex_b[2][kMaxCluster];  // the cluster's exchange, two phases
-  int child_tok[kChildList];
+// What is known of one row of a pass.
+struct RowState {
+  double sum;               // of its weights 2^((x - m) log2(e) / T)
+  float m, inv, as;         // maximum; 1 / sum; A after the children tried so far, times the sum
+  float x;                  // logit of the accepted child's token
+  int am, dead;             // first argmax (T = 0); nothing of the row is possible
+  int next, more;           // the accepted child, or -1; a residual's sum is wanted first
   int n_child;
-  int next, more;    // the accepted child (or -1); a residual's sum is wanted
-  double a;          // A after the children tried so far
+  uint32_t marks[kMarks];   // bit (x >> 3) mod 32 kMarks for every child's token x
+  int child_tok[kChildList];
 };
+struct Shared {
+  uint64_t part_a[kRows][kWarps], part_b[kRows][kWarps];
+  uint64_t ex_a[2][kRows][kMaxCluster], ex_b[2][kRows][kMaxCluster];  // the cluster's exchange, two phases
+  RowState row[kRows];
+  int par[kNodes], tok[kNodes], first[kNodes];  // parents, tokens, first children
+  float u[kNodes];
+  float lx[kNodes], lm[kNodes];                 // emitted tokens' logits and their rows' maxima and sums
+  double lsum[kNodes];
+  // read again where fp64 needs them: kept in registers, their conversions
+  // would be hoisted and done by every thread, on a pipe of two lanes a cycle
+  volatile float c_hi, c_lo, temp;
+};
+
+// Sums of weights and residuals cross threads as fixed-point integers: adding
+// them is exact, takes the integer pipe (fp64 adds run at a 64th of its rate
+// here) and needs no order.
+__device__ __forceinline__ uint64_t warp_add64(uint64_t v) {
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+  return v;
+}
+__device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) v = max64(v, __shfl_xor_sync(0xffffffffu, v, k));
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
+  return v;
+}
+
+// a * w for a weight w in [0, 1], in half of a's units (the product's upper bits).
+__device__ __forceinline__ uint64_t scale64(uint64_t a, float w) {
+  return __umul64hi(a, __float2ull_rn(w * 4294967296.f) << 31);
+}
 
 // LB: logits bf16 (else fp32).  QT: draft distributions: 0 none, 1 bf16, 2 fp32.
 template <bool LB, int QT>
@@ -106,19 +171,47 @@ __global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const Sample
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = p.cluster;
   const int rank = (int)cluster_rank(), b = blockIdx.x / C;
+  cluster_arrive();  // waited for before the first store to another CTA's shared memory
   grid_dependency_wait();
   grid_dependents_launch();
   const int o = p.qo_indptr[b];
   const int L = p.qo_indptr[b + 1] - o;
   const float temp = p.temperature ? p.temperature[b] : 1.f;
   const bool table_ok = o >= 0 && L >= 0 && (int64_t)o + L <= p.total;
+  const int V = p.vocab;
+  const int c0 = (int)min((int64_t)V, (int64_t)rank * p.slice), c1 = (int)min((int64_t)V, (int64_t)c0 + p.slice);
+  const float* noise = p.noise + (size_t)b * p.noise_stride;
+  constexpr int LES = LB ? 2 : 4, QES = QT == 1 ? 2 : 4;
+  const bool greedy = temp == 0.f;
+  auto row_of = [&](int i) -> const void* {
+    return static_cast<const uint8_t*>(p.logits) + (size_t)(o + i) * p.row_stride * LES;
+  };
+  auto qrow_of = [&](int i) -> const void* {
+    return QT ? static_cast<const uint8_t*>(p.draft) + (size_t)(o + i) * p.draft_stride * QES : nullptr;
+  };
+  // this CTA's slice of node i's row, and of the noise (read last, but
+  // always), towards L2 while the walk waits on other things
+  auto prefetch_row = [&](int i) {
+    prefetch_l2(static_cast<const uint8_t*>(row_of(i)) + (size_t)c0 * LES, (int64_t)(c1 - c0) * LES);
+  };
+  if (tid == 0 && table_ok && L > 0) {
+    prefetch_row(0);
+    if (!greedy) prefetch_l2(noise + c0, (int64_t)(c1 - c0) * 4);
+  }
   int bad = 0;
+  if (tid < kNodes) sh.first[tid] = kNodes;
   if (table_ok)
     for (int i = tid; i < L; i += kThreads) {
       const int par = p.parents[o + i];
       bad |= i == 0 ? par >= 0 : (par < 0 || par >= i);
+      if (L <= kNodes) {
+        sh.par[i] = par;
+        sh.tok[i] = p.tokens[o + i];
+        sh.u[i] = p.uniforms[o + i];
+      }
     }
   bad = __syncthreads_or(bad) || !table_ok || !(temp >= 0.f && temp < INFINITY);
+  cluster_wait();
   if (bad || L == 0) {  // the same in every CTA of the cluster
     if (rank == 0) {
       if (tid == 0) {
@@ -134,19 +227,22 @@ __global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const Sample
     }
     return;
   }
+  if (L <= kNodes && tid > 0 && tid < L) atomicMin(&sh.first[sh.par[tid]], tid);
 
-  cluster_sync();  // every CTA of the cluster runs before its shared memory is written
-
-  const int V = p.vocab;
-  const int c0 = (int)min((int64_t)V, (int64_t)rank * p.slice), c1 = (int)min((int64_t)V, (int64_t)c0 + p.slice);
-  const float* noise = p.noise + (size_t)b * p.noise_stride;
-  constexpr int LES = LB ? 2 : 4, QES = QT == 1 ? 2 : 4;
-  const bool greedy = temp == 0.f;
   // log2(e) / T as a float pair: a rounded factor alone would tilt the whole
-  // distribution by |logit difference| * 2^-25
-  // (both parts > 0, so that -inf logits stay -inf)
-  const double cd = greedy ? 1.0 : fmin(1.4426950408889634 / (double)temp, 3e38);
-  const float c_hi = __double2float_rd(cd), c_lo = fmaxf((float)(cd - (double)c_hi), 1.1754944e-38f);
+  // distribution by |logit difference| * 2^-25.  Rounded down, so that both
+  // parts are positive and a logit of -inf stays -inf (log2(e) itself is
+  // 1.4426950216 + 1.926e-8).
+  const float c_hi = greedy ? 1.f : __fdiv_rd(1.4426950216293335f, temp);
+  const float c_lo =
+      greedy ? 1.f
+             : fminf(fmaxf((fmaf(-c_hi, temp, 1.4426950216293335f) + 1.925963033500e-8f) / temp, 1e-45f), 3e38f);
+  if (tid == 0) {
+    sh.c_hi = c_hi;
+    sh.c_lo = c_lo;
+    sh.temp = temp;
+  }
+  __syncthreads();
   const uint64_t ch2 = f32x2(c_hi, c_hi), cl2 = f32x2(c_lo, c_lo);
   // 2^((x - m) log2(e) / T) of a pair: the difference first (exact for bf16
   // logits of like size), then the two-term product
@@ -161,72 +257,134 @@ __global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const Sample
     return ex2(fmaf(d, c_hi, d * c_lo));
   };
 
-  // Exchange one pair of words with the cluster: every CTA gets all of them
-  // in sh.ex_a / ex_b [phase][0 .. C).  The two phases alternate, so a CTA that
-  // runs ahead never writes what a slower one still reads.
+  // The exchange: lane k of a warp that has a row's words sends them to CTA k,
+  // and after the barrier every CTA has all of them in sh.ex_a / ex_b
+  // [phase][row][0 .. C).  The two phases alternate, so a CTA that runs ahead
+  // never writes what a slower one still reads.
   int phase = 0;
-  auto exchange = [&](uint64_t a, uint64_t v) {  // called by every thread, values of thread 0
-    phase ^= 1;
-    if (tid == 0)
-      for (int k = 0; k < C; ++k) {
-        cluster_store(smem_u32(&sh.ex_a[phase][rank]), k, a);
-        cluster_store(smem_u32(&sh.ex_b[phase][rank]), k, v);
-      }
+  auto send = [&](int r, uint64_t x, uint64_t y) {
+    if (lane < C) {
+      cluster_store(smem_u32(&sh.ex_a[phase][r][rank]), lane, x);
+      cluster_store(smem_u32(&sh.ex_b[phase][r][rank]), lane, y);
+    }
     __syncwarp();
-    cluster_sync();
   };
-  // Cluster-wide maximum of a key / sum of a double; the result in every thread.
-  auto cluster_max = [&](uint64_t key) -> uint64_t {
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) key = max64(key, __shfl_xor_sync(0xffffffffu, key, s));
-    if (lane == 0) sh.warp_a[warp] = key;
-    __syncthreads();
-    if (tid == 0)
-      for (int w = 1; w < kWarps; ++w) key = max64(key, sh.warp_a[w]);
-    exchange(key, 0);
-    key = sh.ex_a[phase][0];
-    for (int k = 1; k < C; ++k) key = max64(key, sh.ex_a[phase][k]);
-    return key;
-  };
-  auto cluster_sum = [&](float v) -> double {
-    double s = v;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    if (lane == 0) sh.warp_a[warp] = __double_as_longlong(s);
-    __syncthreads();
-    if (tid == 0)
-      for (int w = 1; w < kWarps; ++w) s += __longlong_as_double(sh.warp_a[w]);
-    exchange(__double_as_longlong(s), 0);
-    s = __longlong_as_double(sh.ex_a[phase][0]);
-    for (int k = 1; k < C; ++k) s += __longlong_as_double(sh.ex_a[phase][k]);
-    return s;
+
+  const int32_t* par = L <= kNodes ? sh.par : p.parents + o;
+  const int32_t* tok = L <= kNodes ? sh.tok : p.tokens + o;
+  const float* uni = L <= kNodes ? sh.u : p.uniforms + o;
+  // weights of at most 1 in units of 2^-sum_bits: V of them stay below 2^63
+  const int sum_bits = V <= (1 << 22) ? 40 : 31;
+  const float sum_unit = __int_as_float((127 + sum_bits) << 23);
+
+  // (x - m) / T - ln(sum): the logarithm of the sum's fraction in fp32, the
+  // rest in fp64, a handful of operations
+  auto log_p = [&](float x, float rm, double t) -> float {
+    const int e = (int)(__double_as_longlong(t) >> 52) - 1023;
+    const float f = (float)(t * __longlong_as_double((long long)(1023 - e) << 52));
+    const double d = ((double)x - (double)rm) * ((double)sh.c_hi + (double)sh.c_lo) - (double)e;
+    return (float)(d * 0.6931471805599453 - (double)logf(f));
   };
 
   int v = 0, k = 0;
+  if (tid == 0 && rank == 0) p.path[o] = 0;
   for (;;) {
-    const void* row = static_cast<const uint8_t*>(p.logits) + (size_t)(o + v) * p.row_stride * LES;
-    const void* qrow = QT ? static_cast<const uint8_t*>(p.draft) + (size_t)(o + v) * p.draft_stride * QES : nullptr;
-    if (tid == 0 && rank == 0) p.path[o + k] = v;
+    // ---- the rows of this pass
+    int node[kRows], n = 1;
+    node[0] = v;
+#pragma unroll
+    for (int r = 1; r < kRows; ++r) {
+      node[r] = -1;
+      if (n == r && r < p.rows && L <= kNodes && sh.first[node[r - 1]] < kNodes) {
+        node[r] = sh.first[node[r - 1]];
+        ++n;
+      }
+    }
+    int mine = -1;   // the node that this warp decides about
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+      if (warp == r) mine = node[r];
+    if (mine >= 0 && lane == 0) prefetch_row(mine);
 
-    // ---- the row's maximum and sum (T = 0: its first argmax)
-    float m = -INFINITY;
-    double sum = 0.0;
-    int am = -1;
-    {
+    // ---- its children, 32 nodes at a time: what each lane's node needs is
+    // asked for before the pass over the rows, so it arrives meanwhile
+    RowState& rs = sh.row[warp & (kRows - 1)];
+    const void* const row = row_of(max(mine, 0));
+    const void* const qrow = qrow_of(max(mine, 0));
+    int base = mine + 1 - 32;
+    uint32_t win = 0;   // children in the window base .. base + 31 not yet tried
+    int ctok = -1;
+    float cx = -INFINITY, cq = 0.f, cu = 0.f;   // token's logit and draft probability, the child's number
+    auto load_window = [&]() {
+      for (base += 32; base < L && win == 0; base += 32) {
+        const int i = base + lane;
+        win = __ballot_sync(0xffffffffu, i < L && par[i] == mine);
+        if (win == 0) continue;
+        ctok = -1;
+        cx = -INFINITY;
+        cq = cu = 0.f;
+        if ((win >> lane) & 1u) {
+          ctok = tok[i];
+          cu = uni[i];
+          if (ctok >= 0 && ctok < V) {
+            cx = load_elem<LB>(row, ctok);
+            if (QT) cq = load_elem<QT == 1>(qrow, ctok);
+          }
+        }
+        if (!QT) {
+          // q one-hot: an earlier sibling's equal token was rejected before
+          // this one, so nothing of it is left
+          const uint32_t before = win & ((1u << lane) - 1u);
+          bool dup = (__match_any_sync(0xffffffffu, ctok) & before) != 0;
+          const int n0 = rs.n_child, at = n0 + __popc(before);
+          for (int j = 0; j < min(n0, kChildList); ++j) dup |= rs.child_tok[j] == ctok;
+          if (n0 > kChildList)
+            for (int j = mine + 1; j < base; ++j) dup |= par[j] == mine && tok[j] == ctok;
+          if (dup) cx = -INFINITY;
+          if ((win >> lane) & 1u) {
+            if (at < kChildList) rs.child_tok[at] = ctok;
+            atomicOr(&rs.marks[(ctok >> 8) & (kMarks - 1)], 1u << ((ctok >> 3) & 31));
+          }
+          __syncwarp();
+          if (lane == 0) rs.n_child = n0 + __popc(win);
+          __syncwarp();
+        }
+        break;
+      }
+    };
+    if (mine >= 0) {
+      rs.marks[lane] = 0;
+      if (lane == 0) rs.n_child = 0;
+      __syncwarp();
+      load_window();
+    }
+
+    // ---- each row's maximum and sum over the slice (T = 0: its first argmax).
+    // The warps are shared out among the rows, so that every row's loads are in
+    // flight at once and each warp reduces once.
+    const int row_warps = kWarps / (n > 2 ? 4 : n);
+    const int r_mine = warp / row_warps, w_mine = warp - r_mine * row_warps;
+    if (r_mine < n) {
+      int i_row = node[0];
+#pragma unroll
+      for (int j = 1; j < kRows; ++j)
+        if (r_mine == j) i_row = node[j];
+      const void* x_row = row_of(i_row);
+      const int t0 = w_mine * 32 + lane, step = row_warps * 32;
       // 16-byte loads over the aligned middle of the slice, single elements at the ends
       constexpr int EPV = 16 / LES;
-      const uintptr_t a0 = reinterpret_cast<uintptr_t>(row) + (uintptr_t)c0 * LES;
+      const uintptr_t a0 = reinterpret_cast<uintptr_t>(x_row) + (uintptr_t)c0 * LES;
       const int head = min(c1 - c0, (int)(((16 - (a0 & 15)) & 15) / LES));
       const int nvec = (c1 - c0 - head) / EPV, v0 = c0 + head, v1 = v0 + nvec * EPV;
-      const uint4* vp = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + (size_t)v0 * LES);
+      const uint4* vp = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x_row) + (size_t)v0 * LES);
       const int n_end = head + (c1 - v1);
       auto end_at = [&](int i) { return i < head ? c0 + i : v1 + (i - head); };
       if (greedy) {
         uint64_t best = 0;
-        for (int i = tid; i < n_end; i += kThreads)
-          best = max64(best, logit_key(load_elem<LB>(row, end_at(i)), (uint32_t)end_at(i)));
+        for (int i = t0; i < n_end; i += step)
+          best = max64(best, logit_key(load_elem<LB>(x_row, end_at(i)), (uint32_t)end_at(i)));
 #pragma unroll 4
-        for (int i = tid; i < nvec; i += kThreads) {
+        for (int i = t0; i < nvec; i += step) {
           const uint4 w = __ldg(vp + i);
           const uint32_t u[4] = {w.x, w.y, w.z, w.w};
           const uint32_t e = (uint32_t)(v0 + i * EPV);
@@ -240,259 +398,319 @@ __global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const Sample
             }
           }
         }
-        am = (int)(0xffffffffu - (uint32_t)cluster_max(best));
+        best = warp_max64(best);
+        if (lane == 0) sh.part_a[r_mine][w_mine] = best;
       } else {
-        // running maximum and sum, four vectors at a time
-        float s = 0.f;
-        constexpr int NV = 4;
-        for (int i0 = tid; i0 < nvec; i0 += NV * kThreads) {
-          uint4 w[NV];
+      // running maximum and sum, eight vectors at a time
+      float m = -INFINITY, s = 0.f;
+      constexpr int NV = 8;
+      for (int i0 = t0; i0 < nvec; i0 += NV * step) {
+        uint4 w[NV];
 #pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            const int i = i0 + j * kThreads;
-            const uint32_t ninf = LB ? 0xff80ff80u : 0xff800000u;
-            w[j] = i < nvec ? __ldg(vp + i) : make_uint4(ninf, ninf, ninf, ninf);
-          }
-          float x[NV][EPV];
-          float mx = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (LB) {
-                x[j][2 * q] = __uint_as_float(u[q] << 16);
-                x[j][2 * q + 1] = __uint_as_float(u[q] & 0xffff0000u);
-                mx = fmaxf(mx, fmaxf(x[j][2 * q], x[j][2 * q + 1]));
-              } else {
-                x[j][q] = __uint_as_float(u[q]);
-                mx = fmaxf(mx, x[j][q]);
-              }
-            }
-          }
-          if (mx > m) {
-            s = m == -INFINITY ? 0.f : s * weight(m, mx);
-            m = mx;
-          }
-          if (m == -INFINITY) continue;
-          float t0 = 0.f, t1 = 0.f;
+        for (int j = 0; j < NV; ++j) {
+          const int i = i0 + j * step;
+          const uint32_t ninf = LB ? 0xff80ff80u : 0xff800000u;
+          w[j] = i < nvec ? __ldg(vp + i) : make_uint4(ninf, ninf, ninf, ninf);
+        }
+        float mx;
+        if constexpr (LB) {   // the maximum in bf16 pairs
+          uint32_t v2 = w[0].x;
 #pragma unroll
           for (int j = 0; j < NV; ++j)
+            v2 = max_bf16x2(max_bf16x2(v2, w[j].x), max_bf16x2(w[j].y, max_bf16x2(w[j].z, w[j].w)));
+          mx = fmaxf(__uint_as_float(v2 << 16), __uint_as_float(v2 & 0xffff0000u));
+        } else {
+          mx = -INFINITY;
 #pragma unroll
-            for (int q = 0; q < EPV; q += 2) {
-              float w0, w1;
-              weight2(x[j][q], x[j][q + 1], m, &w0, &w1);
-              t0 += w0;
-              t1 += w1;
-            }
-          s += t0 + t1;
+          for (int j = 0; j < NV; ++j)
+            mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(w[j].x), __uint_as_float(w[j].y))),
+                       fmaxf(__uint_as_float(w[j].z), __uint_as_float(w[j].w)));
         }
-        for (int i = tid; i < n_end; i += kThreads) {
-          const float x = load_elem<LB>(row, end_at(i));
-          if (x > m) {
-            s = m == -INFINITY ? 0.f : s * weight(m, x);
-            m = x;
+        if (mx > m) {
+          s = m == -INFINITY ? 0.f : s * weight(m, mx);
+          m = mx;
+        }
+        if (m == -INFINITY) continue;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (i0 + j * step >= nvec) break;
+          const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+          for (int q = 0; q < (LB ? 4 : 2); ++q) {
+            float w0, w1;
+            if (LB) weight2(__uint_as_float(u[q] << 16), __uint_as_float(u[q] & 0xffff0000u), m, &w0, &w1);
+            else weight2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]), m, &w0, &w1);
+            s0 += w0;
+            s1 += w1;
           }
-          if (m > -INFINITY) s += weight(x, m);
         }
-        // thread -> warp -> CTA -> cluster: the maximum first, then the sums
-        // against it in double
-        float wm = m;
+        s += s0 + s1;
+      }
+      for (int i = t0; i < n_end; i += step) {
+        const float x = load_elem<LB>(x_row, end_at(i));
+        if (x > m) {
+          s = m == -INFINITY ? 0.f : s * weight(m, x);
+          m = x;
+        }
+        if (m > -INFINITY) s += weight(x, m);
+      }
+      // thread -> warp -> CTA -> cluster: each part against its own maximum,
+      // joined against the common one
+      const float wm = warp_max(m);
+      const uint64_t wsum = warp_add64(__float2ull_rn(m == -INFINITY ? 0.f : s * weight(m, wm) * sum_unit));
+      if (lane == 0) {
+        sh.part_a[r_mine][w_mine] = __float_as_uint(wm);
+        sh.part_b[r_mine][w_mine] = wsum;
+      }
+      }
+    }
+    __syncthreads();
+    phase ^= 1;
+    // `count` parts, one a lane, joined in every lane
+    auto join = [&](const uint64_t* pa, const uint64_t* pb, int count, float* mo) -> uint64_t {
+      const float pm = lane < count ? __uint_as_float((uint32_t)pa[lane]) : -INFINITY;
+      const float jm = warp_max(pm);
+      *mo = jm;
+      return warp_add64(pm > -INFINITY ? scale64(pb[lane], weight(pm, jm)) : 0);
+    };
+    float m = -INFINITY;
+    double sum = 0.0;
+    int am = -1;
+    if (mine >= 0) {
+      if (greedy) {
+        send(warp, warp_max64(lane < row_warps ? sh.part_a[warp][lane] : 0), 0);
+      } else {
+        const uint64_t f = join(sh.part_a[warp], sh.part_b[warp], row_warps, &m);
+        send(warp, __float_as_uint(m), f);
+      }
+    }
+    cluster_sync();
+
+    // ---- each row's warp tries its children in index order.  The row's warp
+    // of every CTA comes to the same decisions: the same numbers, read and
+    // joined in the same order.
+    bool dead = false, pending = false;   // pending (QT): a child was rejected and its B not yet summed
+    float cw = 0.f, sf = 0.f;             // weight of the child's token: sum times its probability
+    double A = 0.0, B = 1.0;
+    auto child_w = [&]() { return greedy ? (ctok == am && cx > -INFINITY ? 1.f : 0.f) : weight(cx, m); };
+    auto decide = [&]() {
+      int next = -1, more = 0;
+      float nx = 0.f;
+      while (!dead) {
+        if (win == 0) {
+          load_window();
+          if (win == 0) break;
+          cw = child_w();
+        }
+        if (pending) {
+          more = 1;
+          break;
+        }
+        const int j = __ffs(win) - 1;
+        win &= win - 1;
+        const float wj = __shfl_sync(0xffffffffu, cw, j), xj = __shfl_sync(0xffffffffu, cx, j);
+        const float qj = QT ? __shfl_sync(0xffffffffu, cq, j) : 1.f, uj = __shfl_sync(0xffffffffu, cu, j);
+        bool ok;
+        if (greedy) {
+          ok = wj > 0.f;
+        } else {
+          // u q B < p - A q, times the sum.  In fp32, and once more in fp64
+          // where that is too close to tell.
+          const float lhs = uj * (float)B * qj * sf, aq = QT ? (float)A * qj * sf : 0.f;
+          ok = lhs < wj - aq;
+          if (fabsf(wj - aq - lhs) <= 4e-6f * (wj + aq + lhs) && xj > -INFINITY) {
+            const double w = exp(((double)xj - (double)m) / (double)sh.temp);
+            ok = (double)uj * B * (double)qj * sum < w - (QT ? A * (double)qj * sum : 0.0);
+          }
+        }
+        if (ok) {
+          next = base + j;
+          nx = xj;
+          break;
+        }
+        if (greedy) continue;
+        if (QT) {
+          A += B;
+          pending = true;
+        } else {
+          B -= (double)(wj / sf);
+        }
+      }
+      pending = false;
+      if (lane == 0) {
+        rs.next = next;
+        rs.more = more;
+        rs.as = (float)A * sf;
+        rs.x = nx;
+      }
+    };
+    if (mine >= 0) {
+      if (greedy) {
+        am = (int)(0xffffffffu - (uint32_t)warp_max64(lane < C ? sh.ex_a[phase][warp][lane] : 0));
+        dead = !(load_elem<LB>(row, am) > -INFINITY);
+      } else {
+        const uint64_t f = join(sh.ex_a[phase][warp], sh.ex_b[phase][warp], C, &m);
+        dead = f == 0;
+        // (two joins halved the unit twice)
+        sum = (double)f * __longlong_as_double((long long)(1025 - sum_bits) << 52);
+        sf = (float)sum;
+      }
+      if (!dead) cw = child_w();
+      if (lane == 0) {
+        rs.m = m;
+        rs.sum = sum;
+        rs.inv = 1.f / sf;
+        rs.am = am;
+        rs.dead = dead;
+      }
+      decide();
+    }
+    __syncthreads();
+
+    // ---- follow the decisions along the rows of the pass
+    int r = 0, at = v, to;
+    for (;;) {
+      while (QT && sh.row[r].more) {
+        // B = sum_x (p(x) - A q(x))+ of this row, in units of 2^-50
+        const void *x_row = row_of(at), *q_row = qrow_of(at);
+        const float rm = sh.row[r].m, inv = sh.row[r].inv, as = sh.row[r].as;
+        float t = 0.f;
+        if (p.vec) {
+#pragma unroll 2
+          for (int i = c0 + 8 * tid; i < c1; i += 8 * kThreads) {
+            float x[8], q[8];
+            load8<LB>(x_row, i, x);
+            load8<QT == 1>(q_row, i, q);
 #pragma unroll
-        for (int j = 16; j > 0; j >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, j));
-        double ws = m == -INFINITY ? 0.0 : (double)(s * weight(m, wm));
-#pragma unroll
-        for (int j = 16; j > 0; j >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, j);
-        if (lane == 0) {
-          sh.warp_a[warp] = __float_as_uint(wm);
-          sh.warp_b[warp] = __double_as_longlong(ws);
+            for (int e = 0; e < 8; e += 2) {
+              float w0, w1;
+              weight2(x[e], x[e + 1], rm, &w0, &w1);
+              t += fmaxf(fmaf(-as, q[e], w0), 0.f) + fmaxf(fmaf(-as, q[e + 1], w1), 0.f);
+            }
+          }
+        } else {
+#pragma unroll 4
+          for (int i = c0 + tid; i < c1; i += kThreads)
+            t += fmaxf(fmaf(-as, load_elem<QT == 1>(q_row, i), weight(load_elem<LB>(x_row, i), rm)), 0.f);
+        }
+        uint64_t f = warp_add64(__float2ull_rn(t * inv * 0x1p50f));
+        if (lane == 0) sh.part_a[0][warp] = f;
+        __syncthreads();
+        phase ^= 1;
+        if (warp == 0) send(0, warp_add64(lane < kWarps ? sh.part_a[0][lane] : 0), 0);
+        cluster_sync();
+        if (warp == r) {
+          f = 0;
+          for (int j = 0; j < C; ++j) f += sh.ex_a[phase][0][j];
+          B = (double)f * 0x1p-50;
+          decide();
         }
         __syncthreads();
-        // the sums of parts against their common maximum, in part order
-        auto join = [&](const uint64_t* pm, const uint64_t* ps, int n, float* mo) -> double {
-          float mm = -INFINITY;
-          for (int j = 0; j < n; ++j) mm = fmaxf(mm, __uint_as_float((uint32_t)pm[j]));
-          double t = 0.0;
-          for (int j = 0; j < n; ++j) {
-            const float pj = __uint_as_float((uint32_t)pm[j]);
-            if (pj > -INFINITY) t += __longlong_as_double(ps[j]) * (double)weight(pj, mm);
-          }
-          *mo = mm;
-          return t;
-        };
-        float cm = -INFINITY;
-        double cs = 0.0;
-        if (tid == 0) cs = join(sh.warp_a, sh.warp_b, kWarps, &cm);
-        exchange(__float_as_uint(cm), __double_as_longlong(cs));
-        sum = join(sh.ex_a[phase], sh.ex_b[phase], C, &m);
       }
-    }
-    const bool dead = greedy ? !(load_elem<LB>(row, am) > -INFINITY) : !(sum > 0.0);
-
-    // ---- the children in index order.  Warp 0 of every CTA comes to the
-    // same decisions: the same numbers, read and reduced in the same order.
-    double A = 0.0, B = 1.0;
-    int base = v + 1 - 32;
-    uint32_t win = 0;       // children in the window base .. base + 31 not yet tried
-    bool pending = false;   // QT: a child was rejected and its B not yet summed
-    double cp = 0.0, cq = 0.0, cu = 0.0;
-    int ctok = -1;
-    if (tid == 0) sh.n_child = 0;
-    // the next window that holds a child of v: each lane its child's token,
-    // number and probabilities
-    auto load_window = [&]() -> bool {
-      for (base += 32; base < L; base += 32) {
-        const int i = base + lane;
-        const bool is = i < L && p.parents[o + i] == v;
-        win = __ballot_sync(0xffffffffu, is);
-        if (win) {
-          cp = cq = cu = 0.0;
-          ctok = -1;
-          if (is) {
-            ctok = p.tokens[o + i];
-            cu = p.uniforms[o + i];
-            if (ctok >= 0 && ctok < V) {
-              if (greedy) cp = ctok == am ? 1.0 : 0.0;
-              else cp = exp(((double)load_elem<LB>(row, ctok) - (double)m) / (double)temp) / sum;
-              if (QT) cq = load_elem<QT == 1>(qrow, ctok);
-            }
-          }
-          if (!QT) {
-            // q one-hot: an earlier sibling's equal token was rejected before
-            // this one, so nothing of it is left
-            bool dup = false;
-            for (int j = 0; j < 32; ++j) {
-              const int tj = __shfl_sync(0xffffffffu, ctok, j);
-              dup |= j < lane && ((win >> j) & 1u) && tj == ctok;
-            }
-            for (int j = v + 1; j < base; ++j) dup |= p.parents[o + j] == v && p.tokens[o + j] == ctok;
-            if (dup) cp = 0.0;
-            const int n0 = sh.n_child, at = n0 + __popc(win & ((1u << lane) - 1u));
-            if (is && at < kChildList) sh.child_tok[at] = ctok;
-            __syncwarp();
-            if (lane == 0) sh.n_child = n0 + __popc(win);
-            __syncwarp();
-          }
-          return true;
+      to = sh.row[r].next;
+      if (to < 0) break;
+      if (tid == 0 && rank == 0) {
+        p.path[o + k + 1] = to;
+        if (k < kNodes) {
+          sh.lx[k] = sh.row[r].x;
+          sh.lm[k] = sh.row[r].m;
+          sh.lsum[k] = sh.row[r].sum;
+        } else if (p.logprobs) {
+          p.logprobs[o + k] = greedy ? 0.f : log_p(sh.row[r].x, sh.row[r].m, sh.row[r].sum);
         }
       }
-      return false;
-    };
-    int to = -1;
-    for (;;) {
-      __syncthreads();
-      if (warp == 0) {
-        int next = -1, more = 0;
-        while (!dead) {
-          if (win == 0 && !load_window()) break;
-          if (pending) {
-            more = 1;
-            break;
-          }
-          const int j = __ffs(win) - 1;
-          win &= win - 1;
-          const double pj = __shfl_sync(0xffffffffu, cp, j), qj = __shfl_sync(0xffffffffu, cq, j),
-                       uj = __shfl_sync(0xffffffffu, cu, j);
-          const bool ok = greedy ? pj > 0.0 : QT ? uj * B * qj < pj - A * qj : uj * B < pj;
-          if (ok) {
-            next = base + j;
-            break;
-          }
-          if (greedy) continue;
-          if (QT) {
-            A += B;
-            pending = true;
-          } else {
-            B -= pj;
-          }
-        }
-        pending = false;
-        if (lane == 0) {
-          sh.next = next;
-          sh.more = more;
-          sh.a = A;
-        }
-      }
-      __syncthreads();
-      to = sh.next;
-      A = sh.a;
-      if (!QT || !sh.more) break;
-      // B = sum_x (p(x) - A q(x))+
-      const float inv = (float)(1.0 / sum), af = (float)A;
-      float t = 0.f;
-      if (p.vec) {
-#pragma unroll 2
-        for (int i = c0 + 8 * tid; i < c1; i += 8 * kThreads) {
-          float x[8], q[8];
-          load8<LB>(row, i, x);
-          load8<QT == 1>(qrow, i, q);
+      ++k;
+      at = to;
+      int ahead = -1;   // the node of the pass's next row
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t += fmaxf(fmaf(-af, q[e], weight(x[e], m) * inv), 0.f);
-        }
-      } else {
-#pragma unroll 4
-        for (int i = c0 + tid; i < c1; i += kThreads)
-          t += fmaxf(fmaf(-af, load_elem<QT == 1>(qrow, i), weight(load_elem<LB>(row, i), m) * inv), 0.f);
-      }
-      B = cluster_sum(t);
+      for (int j = 1; j < kRows; ++j)
+        if (j == r + 1) ahead = node[j];
+      if (to != ahead) break;
+      ++r;
     }
     if (to >= 0) {
-      if (tid == 0 && rank == 0 && p.logprobs) {
-        double lp = 0.0;
-        if (!greedy)
-          lp = ((double)load_elem<LB>(row, p.tokens[o + to]) - (double)m) / (double)temp - log(sum);
-        p.logprobs[o + k] = (float)lp;
-      }
       v = to;
-      ++k;
       continue;
     }
 
     // ---- no child accepted: the bonus token
+    const RowState& last = sh.row[r];
+    const void *x_row = row_of(at), *q_row = qrow_of(at);
     int bonus = -1;
-    if (!dead && greedy) {
-      bonus = am;
-    } else if (!dead) {
-      const float inv = (float)(1.0 / sum);
-      float af = (float)A;
-      const int n_child = QT ? 0 : sh.n_child;
-      bool plain = false;   // draw from p_v itself: nothing is left of the residual
+    // all of its slice asked for at once: the loads below run behind it
+    if (QT && tid == 0 && !last.dead && !greedy)
+      prefetch_l2(static_cast<const uint8_t*>(q_row) + (size_t)c0 * QES, (int64_t)(c1 - c0) * QES);
+    if (!last.dead && greedy) {
+      bonus = last.am;
+    } else if (!last.dead) {
+      const float rm = last.m, as = last.as;
+      const int n_child = QT ? 0 : last.n_child;
+      bool plain = n_child == 0 && !QT;   // draw from p_v itself: nothing rejected, or nothing left of the residual
       for (;;) {
-        uint64_t best = 0;
-        auto rejected = [&](int x) {
-          for (int j = 0; j < min(n_child, kChildList); ++j)
-            if (sh.child_tok[j] == x) return true;
+        // the best of this thread's entries so far: w / e of the largest
+        float best_w = 0.f, best_e = 1.f;
+        int best_i = -1;
+        // which of the entries i .. i + 7 (i a multiple of 8) are rejected tokens
+        auto rejected8 = [&](int i) -> uint32_t {
+          if (QT || plain || !((last.marks[(i >> 8) & (kMarks - 1)] >> ((i >> 3) & 31)) & 1u)) return 0u;
+          uint32_t hit = 0;
+          for (int j = 0; j < min(n_child, kChildList); ++j) {
+            const uint32_t d = (uint32_t)(last.child_tok[j] - i);
+            if (d < 8) hit |= 1u << d;
+          }
           if (n_child > kChildList)
-            for (int j = v + 1; j < L; ++j)
-              if (p.parents[o + j] == v && p.tokens[o + j] == x) return true;
-          return false;
+            for (int j = at + 1; j < L; ++j)
+              if (par[j] == at && (uint32_t)(tok[j] - i) < 8u) hit |= 1u << (tok[j] - i);
+          return hit;
         };
-        auto take = [&](float x, float q, float e, int i) {
-          float w = weight(x, m) * inv;
-          if (QT && !plain) w = fmaf(-af, q, w);
-          if (!(w > 0.f)) return;
-          const uint64_t key = race_key(__fdiv_rn(w, e), (uint32_t)i);
-          // a rejected token is looked for only when it would win
-          if (key > best && (QT || plain || !rejected(i))) best = key;
+        // w / e compared by cross products (each within 2^-24, as the weights
+        // are): no division or reciprocal an entry.  A thread's entries come in
+        // rising order: an equal one does not replace.
+        auto take = [&](float w, float q, float e, int i) {
+          if (QT && !plain) w = fmaf(-as, q, w);
+          const bool better = w * best_e > best_w * e;
+          best_w = better ? w : best_w;
+          best_e = better ? e : best_e;
+          best_i = better ? i : best_i;
         };
         if (p.vec) {
 #pragma unroll 2
           for (int i = c0 + 8 * tid; i < c1; i += 8 * kThreads) {
             float x[8], q[8], e[8];
-            load8<LB>(row, i, x);
-            if (QT) load8<QT == 1>(qrow, i, q);
+            load8<LB>(x_row, i, x);
+            if (QT) load8<QT == 1>(q_row, i, q);
             load8<false>(noise, i, e);
+            const uint32_t hit = rejected8(i);
+            if (!QT && hit) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) take(x[j], QT ? q[j] : 0.f, e[j], i + j);
+              for (int j = 0; j < 8; ++j) x[j] = (hit >> j) & 1u ? -INFINITY : x[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+              float w0, w1;
+              weight2(x[j], x[j + 1], rm, &w0, &w1);
+              take(w0, QT ? q[j] : 0.f, e[j], i + j);
+              take(w1, QT ? q[j + 1] : 0.f, e[j + 1], i + j + 1);
+            }
           }
         } else {
 #pragma unroll 4
-          for (int i = c0 + tid; i < c1; i += kThreads)
-            take(load_elem<LB>(row, i), QT ? load_elem<QT == 1>(qrow, i) : 0.f, __ldg(noise + i), i);
+          for (int i = c0 + tid; i < c1; i += kThreads) {
+            const float x = (rejected8(i & ~7) >> (i & 7)) & 1u ? -INFINITY : load_elem<LB>(x_row, i);
+            take(weight(x, rm), QT ? load_elem<QT == 1>(q_row, i) : 0.f, __ldg(noise + i), i);
+          }
         }
-        best = cluster_max(best);
-        if (best != 0) {
-          bonus = (int)(0xffffffffu - (uint32_t)best);
+        uint64_t key = warp_max64(best_i >= 0 ? race_key(__fdiv_rn(best_w, best_e), (uint32_t)best_i) : 0);
+        if (lane == 0) sh.part_a[0][warp] = key;
+        __syncthreads();
+        phase ^= 1;
+        if (warp == 0) send(0, warp_max64(lane < kWarps ? sh.part_a[0][lane] : 0), 0);
+        cluster_sync();
+        key = 0;
+        for (int j = 0; j < C; ++j) key = max64(key, sh.ex_a[phase][0][j]);
+        if (key != 0) {
+          bonus = (int)(0xffffffffu - (uint32_t)key);
           break;
         }
         if (plain) break;
@@ -503,11 +721,15 @@ __global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const Sample
       if (tid == 0) {
         p.accept_len[b] = k + 1;
         p.bonus[b] = bonus;
-        if (p.logprobs) {
-          double lp = 0.0;
-          if (!greedy && bonus >= 0)
-            lp = ((double)load_elem<LB>(row, bonus) - (double)m) / (double)temp - log(sum);
-          p.logprobs[o + k] = (float)lp;
+      }
+      if (p.logprobs && warp == 0) {
+        // every emitted token's, a lane each
+        __syncwarp();
+        for (int i = lane; i <= k; i += 32) {
+          if (i == k)
+            p.logprobs[o + k] = greedy || bonus < 0 ? 0.f : log_p(load_elem<LB>(x_row, bonus), last.m, last.sum);
+          else if (i < kNodes)
+            p.logprobs[o + i] = greedy ? 0.f : log_p(sh.lx[i], sh.lm[i], sh.lsum[i]);
         }
       }
       for (int i = k + 1 + tid; i < L; i += kThreads) {
