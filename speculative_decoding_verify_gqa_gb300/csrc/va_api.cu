@@ -1025,7 +1025,6 @@ int verify_accept_sample(const void* logits, va_dtype logits_dtype, int64_t tota
   p.vocab = vocab;
   p.batch = batch;
   p.cluster = sample_cluster(batch, vocab, num_sms);
-  p.rows = 4;
   p.slice = ((vocab + p.cluster - 1) / p.cluster + 7) / 8 * 8;
   p.vec = vocab % 8 == 0 && la % 16 == 0 && row_stride * les % 16 == 0 && na % 16 == 0 &&
           noise_stride % 4 == 0 && (!draft_probs || (qa % 16 == 0 && draft_stride * qes % 16 == 0));

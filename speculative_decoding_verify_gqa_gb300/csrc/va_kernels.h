@@ -136,7 +136,6 @@ struct SampleParams {
   int total, vocab, batch;
   int cluster;                // CTAs per request
   int slice;                  // vocabulary entries per CTA (a multiple of 8)
-  int rows;                   // rows of a pass (see the kernel), at most 4
   int vec;                    // every row starts on 16 bytes and holds a multiple of 8 entries
 };
 cudaError_t launch_accept_sample(const SampleParams& p, bool logits_bf16, int draft, cudaStream_t stream);
