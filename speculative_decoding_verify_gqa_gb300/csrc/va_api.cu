@@ -309,7 +309,7 @@ static int verify_attn_merge_impl(const int32_t* qo_indptr, int num_qo_heads, in
   m.early_inputs = early;
   m.groups = reinterpret_cast<const GroupRec*>(ws + hd->off_merge + (size_t)hd->n_merge * sizeof(MergeItem));
   m.n_groups = plan_groups(*hd);
-  cudaError_t e = launch_merge(m, (int)hd->head_dim_v, hd->n_merge, hd->block_rows,
+  cudaError_t e = launch_merge(m, (int)hd->head_dim_v, hd->n_merge, plan_merge_rows(*hd),
                                (int)hd->max_nsplit,
                                static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;

@@ -76,7 +76,8 @@ constexpr int64_t kPlanNhd = 2;       // cache layout [pages, P, h_kv, d]
 constexpr int64_t kPlanRope = 4;      // queries rotated at their positions
 constexpr int64_t kPlanF8Mma = 8;     // e4m3 MMAs: queries quantised per row, P as e4m3
 
-constexpr int kPlanGroupShift = 32;   // the bits above: number of GroupRecs
+constexpr int kPlanMergeRowsShift = 16;  // bits 16 .. 31: most rows of a merge item (0: block_rows)
+constexpr int kPlanGroupShift = 32;      // the bits above: number of GroupRecs
 
 struct PlanHeader {
   uint32_t magic, version;
@@ -93,6 +94,10 @@ struct PlanHeader {
 };
 static_assert(sizeof(PlanHeader) == 184, "PlanHeader layout (read by the Python binding)");
 
+inline int plan_merge_rows(const PlanHeader& h) {
+  const int rows = (int)(h.flags >> kPlanMergeRowsShift) & 0xffff;
+  return rows ? rows : h.block_rows;
+}
 inline int plan_groups(const PlanHeader& h) { return (int)(h.flags >> kPlanGroupShift); }
 // bytes of the records after the header
 inline size_t plan_list_bytes(const PlanHeader& h) {

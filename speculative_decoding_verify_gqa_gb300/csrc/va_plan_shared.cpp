@@ -184,77 +184,79 @@ int plan_shared_host(const int32_t* kv_indptr, const int32_t* qo_indptr, const i
     for (int b = r0; b < r1; ++b) group_of[(size_t)b] = g;
     max_rows = std::max(max_rows, (int64_t)gr.rows);
   }
-  int kernel = o.kernel;
-  if (kernel == VA_KERNEL_AUTO) {
-    if (tc_ok) kernel = max_rows > 128 ? kKernelTc256 : kKernelTc128;
-    else kernel = max_rows <= 64 ? kKernelMma64 : kKernelMma128;
-  }
-  const int BM = kernel_rows(kernel), TK = kernel_is_tc(kernel) ? kTcTileKeys : kTileKeys;
-
-  // Units of work.
+  // Units of work for a kernel, and how it would cut and pack them.
   std::vector<SharedUnit> units;
-  auto add_units = [&](int32_t b, int64_t R, int64_t lo, int32_t group, auto&& end_of) {
-    for (int64_t row0 = 0; row0 < R; row0 += BM) {
-      const int32_t nrows = (int32_t)std::min<int64_t>(BM, R - row0);
-      units.push_back({b, (int32_t)row0, nrows, (int32_t)lo, (int32_t)end_of(row0 + nrows - 1), group});
+  int BM = 0, TK = 0;
+  int64_t slots = 0, tile1 = 0, tile2 = 0, fixed = 0;
+  const int64_t cap = (int64_t)kMaxTargetPerSm * num_sms;
+  auto set_kernel = [&](int kernel) {
+    BM = kernel_rows(kernel);
+    TK = kernel_is_tc(kernel) ? kTcTileKeys : kTileKeys;
+    slots = (int64_t)num_sms * (kernel_is_tc(kernel) ? 1 : kernel_ctas_per_sm(kernel));
+    // Measured on one GB300, in units of 0.1 us: a key tile of the one-Q-tile
+    // kernel 1.5 us (fp8 caches: 1.7), of the two-Q-tile kernel 2.3 us with two
+    // (2.6) and 1.9 us with one in use (2.0), and what an item costs beside its
+    // tiles (loads, pipeline fill, epilogue), 2 to 3.5 us.
+    const bool fp8 = kv_dtype == VA_DTYPE_FP8_E4M3;
+    tile1 = kernel == kKernelTc256 ? (fp8 ? 20 : 19) : (fp8 ? 17 : 15);
+    tile2 = fp8 ? 26 : 23;
+    fixed = kernel == kKernelTc256 ? 35 : 25;
+    units.clear();
+    auto add_units = [&](int32_t b, int64_t R, int64_t lo, int32_t group, auto&& end_of) {
+      for (int64_t row0 = 0; row0 < R; row0 += BM) {
+        const int32_t nrows = (int32_t)std::min<int64_t>(BM, R - row0);
+        units.push_back({b, (int32_t)row0, nrows, (int32_t)lo, (int32_t)end_of(row0 + nrows - 1), group});
+      }
+    };
+    for (int g = 0; g < num_groups; ++g) {
+      const int64_t S = (int64_t)groups[(size_t)g].pages * page_size;
+      if (groups[(size_t)g].rows > 0)
+        add_units(batch + g, groups[(size_t)g].rows, 0, -1, [&](int64_t) { return S; });
+    }
+    for (int b = 0; b < batch; ++b) {
+      const int32_t g = group_of[(size_t)b];
+      const int64_t lo = g >= 0 ? (int64_t)groups[(size_t)g].pages * page_size : 0, pre = prefix[(size_t)b];
+      const int64_t L = qlen[(size_t)b];
+      // without a mask a row block's last visible key is that of its last token
+      add_units(b, G * L, lo, g, [&](int64_t r) { return has_mask ? pre + L : pre + r / G + 1; });
     }
   };
-  for (int g = 0; g < num_groups; ++g) {
-    const int64_t S = (int64_t)groups[(size_t)g].pages * page_size;
-    if (groups[(size_t)g].rows > 0)
-      add_units(batch + g, groups[(size_t)g].rows, 0, -1, [&](int64_t) { return S; });
-  }
-  for (int b = 0; b < batch; ++b) {
-    const int32_t g = group_of[(size_t)b];
-    const int64_t lo = g >= 0 ? (int64_t)groups[(size_t)g].pages * page_size : 0, pre = prefix[(size_t)b];
-    const int64_t L = qlen[(size_t)b];
-    // without a mask a row block's last visible key is that of its last token
-    add_units(b, G * L, lo, g, [&](int64_t r) { return has_mask ? pre + L : pre + r / G + 1; });
-  }
   auto tiles_of = [&](const SharedUnit& u) { return ceil_div(u.hi - u.lo, TK); };
-  // Cost of a key tile: two Q tiles cost 5/3 of one (as the dealing counts
-  // them); the row blocks of a group all as its first, so that they are cut alike.
+  // cost of a key tile; the row blocks of a group all as its first, so that they are cut alike
   auto tile_cost = [&](const SharedUnit& u) -> int64_t {
     const int32_t rows = u.b >= batch ? std::min(BM, groups[(size_t)(u.b - batch)].rows) : u.nrows;
-    return rows > kTcRowsPerTile ? 5 : 3;
+    return rows > kTcRowsPerTile ? tile2 : tile1;
   };
-  // fp32 partials of one row, in tile cost (a 64 KB tile of K and V costs 3)
-  auto part_cost = [&](const SharedUnit& u) -> int64_t { return ceil_div(3LL * u.nrows * 4 * dv, 64 * 1024); };
-  int64_t W = 0, key_tiles = 0;
-  for (const SharedUnit& u : units) {
-    W += tiles_of(u) * tile_cost(u) * num_kv_heads;
-    key_tiles += tiles_of(u) * num_kv_heads;
-  }
-  // chunks of a unit when items of cost T are aimed at
-  const int64_t min_tiles = std::max<int64_t>(1, o.min_chunk > 0 ? ceil_div(o.min_chunk, TK) : 2);
-  auto chunk_of = [&](const SharedUnit& u, int64_t T) -> int64_t {  // in keys
-    const int64_t t = tiles_of(u);
+  // chunk length of a unit, in keys, when items of cost T are aimed at
+  const int64_t min_chunk = o.min_chunk;
+  auto chunk_of = [&](const SharedUnit& u, int64_t T) -> int64_t {
+    const int64_t t = tiles_of(u), min_tiles = std::max<int64_t>(1, min_chunk > 0 ? ceil_div(min_chunk, TK) : 2);
     int64_t n = std::min(ceil_div(t * tile_cost(u), T), std::max<int64_t>(1, t / min_tiles));
     if (o.max_splits > 0) n = std::min<int64_t>(n, o.max_splits);
     return ceil_div(t, std::max<int64_t>(1, n)) * TK;
   };
   auto splits_of = [&](const SharedUnit& u, int64_t cu) { return ceil_div(u.hi - u.lo, cu); };
-  const int64_t slots = (int64_t)num_sms * (kernel_is_tc(kernel) ? 1 : kernel_ctas_per_sm(kernel));
-  const int64_t cap = (int64_t)kMaxTargetPerSm * num_sms;
-  int64_t T = 0;
-  if (o.target_ctas > 0) {
-    T = std::max<int64_t>(1, ceil_div(W, std::min<int64_t>(o.target_ctas, cap)));
-  } else {
+  // The aimed-at item cost T and the finish it is estimated to give.
+  auto choose = [&](bool tc, int64_t* T) -> int64_t {
+    int64_t W = 0, key_tiles = 0;
+    for (const SharedUnit& u : units) {
+      W += tiles_of(u) * tile_cost(u) * num_kv_heads;
+      key_tiles += tiles_of(u) * num_kv_heads;
+    }
     // Few key tiles per SM: two thirds of the SMs, as in the planner without
     // groups (the set-up of more CTAs and a merge of more partials cost more).
-    const bool latency = kernel_is_tc(kernel) && key_tiles * TK * key_bytes <= 4LL * 64 * 1024 * num_sms;
+    const bool latency = tc && key_tiles * TK * key_bytes <= 4LL * 64 * 1024 * num_sms;
     const int64_t cand_slots = latency ? std::max<int64_t>(1, 2 * (int64_t)num_sms / 3) : slots;
-    // candidates: items aimed at 1/2 .. 4 waves of the slots, packed longest first
     int64_t best = -1;
     std::vector<std::pair<int64_t, int64_t>> load_of;
+    // candidates: items aimed at 1 .. 4 waves of the slots, packed longest first
     for (int half_waves = 2; half_waves <= 8; ++half_waves) {
-      const int64_t target = std::min(half_waves * cand_slots / 2, cap);
+      int64_t target = std::min(half_waves * cand_slots / 2, cap);
+      if (o.target_ctas > 0) target = std::min<int64_t>(o.target_ctas, cap);
       const int64_t t = std::max<int64_t>(1, ceil_div(W, std::max<int64_t>(1, target)));
       load_of.clear();   // (cost, items)
       for (const SharedUnit& u : units) {
         const int64_t cu = chunk_of(u, t), n = splits_of(u, cu);
-        const bool part = n > 1 || u.group >= 0 || u.b >= batch;
-        const int64_t fixed = tile_cost(u) + (part ? part_cost(u) : 0);
         const int64_t last = tiles_of(u) - (n - 1) * (cu / TK);
         if (n > 1) load_of.push_back({fixed + cu / TK * tile_cost(u), (n - 1) * num_kv_heads});
         load_of.push_back({fixed + last * tile_cost(u), (int64_t)num_kv_heads});
@@ -273,11 +275,34 @@ int plan_shared_host(const int32_t* kv_indptr, const int32_t* qo_indptr, const i
       const int64_t finish = levels.rbegin()->first;
       if (best < 0 || finish * 100 < best * 97) {
         best = finish;
-        T = t;
+        *T = t;
       }
+      if (o.target_ctas > 0) break;
     }
-    T = std::max<int64_t>(1, T);
+    return best;
+  };
+  int kernel = o.kernel;
+  int64_t T = 1;
+  if (kernel == VA_KERNEL_AUTO) {
+    if (!tc_ok) {
+      kernel = max_rows <= 64 ? kKernelMma64 : kKernelMma128;
+    } else if (max_rows <= 128) {
+      kernel = kKernelTc128;
+    } else {
+      // Two Q tiles a CTA do more per key tile, but items that fill only one
+      // run slower there: the kernel with the earlier finish.
+      int64_t t256 = 1;
+      set_kernel(kKernelTc128);
+      const int64_t f128 = choose(true, &T);
+      set_kernel(kKernelTc256);
+      const int64_t f256 = choose(true, &t256);
+      kernel = f256 < f128 ? kKernelTc256 : kKernelTc128;
+      if (kernel == kKernelTc256) T = t256;
+    }
   }
+  const bool chosen = T > 1;
+  if (units.empty() || BM != kernel_rows(kernel) || !kernel_is_tc(kernel)) set_kernel(kernel);
+  if (!chosen) choose(kernel_is_tc(kernel), &T);
 
   // The items and their partials.
   std::vector<PlanItem> items;
@@ -314,19 +339,22 @@ int plan_shared_host(const int32_t* kv_indptr, const int32_t* qo_indptr, const i
       for (int64_t s = 0; s < n; ++s) {
         const int64_t lo = u.lo + s * cu, hi = s == n - 1 ? u.hi : lo + cu;
         WorkItem w{u.b, h, u.row0, u.nrows, (int32_t)lo, (int32_t)hi, part ? (int32_t)(base + s * stride) : -1, -1};
-        items.push_back({w, (ceil_div(hi - lo, TK) + 1) * tile_cost(u)});
+        const int64_t cost = u.nrows > kTcRowsPerTile ? tile2 : tile1;
+        items.push_back({w, fixed + ceil_div(hi - lo, TK) * cost});
       }
     }
   }
   if (part_rows > INT32_MAX) return VA_ERR_UNSUPPORTED;
   sort_items(items);
-  const int64_t n_ctas = kernel_is_tc(kernel) && !items.empty() ? deal_chains(items, num_sms, TK) : 0;
+  const int64_t n_ctas = kernel_is_tc(kernel) && !items.empty() ? deal_chains(items, num_sms, TK, true) : 0;
 
   const size_t need = sizeof(PlanHeader) + (items.size() + merges.size() + groups.size()) * 32;
   if (plan_bytes < need) {
     *workspace_bytes = need;
     return VA_ERR_PLAN_BUFFER_TOO_SMALL;
   }
+  int64_t merge_rows = 0;   // requests' row blocks are short next to the groups': the merge's grid
+  for (const MergeItem& m : merges) merge_rows = std::max<int64_t>(merge_rows, m.nrows);
   PlanHeader hd;
   std::memset(&hd, 0, sizeof(hd));
   hd.magic = kPlanMagic;
@@ -362,7 +390,7 @@ int plan_shared_host(const int32_t* kv_indptr, const int32_t* qo_indptr, const i
   hd.plan_bytes = need;
   hd.n_ctas = n_ctas;
   hd.flags = (o.kv_layout == VA_LAYOUT_NHD ? kPlanNhd : 0) | (o.rope ? kPlanRope : 0) | (o.q_fp8 ? kPlanF8Mma : 0) |
-             ((int64_t)num_groups << kPlanGroupShift);
+             (merge_rows << kPlanMergeRowsShift) | ((int64_t)num_groups << kPlanGroupShift);
   char* dst = static_cast<char*>(plan_h);
   std::memcpy(dst, &hd, sizeof(hd));
   dst += sizeof(hd);

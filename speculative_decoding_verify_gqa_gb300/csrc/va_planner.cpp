@@ -60,7 +60,7 @@ void sort_items(std::vector<PlanItem>& items) {
   items.swap(sorted);
 }
 
-int64_t deal_chains(std::vector<PlanItem>& items, int num_sms, int TK) {
+int64_t deal_chains(std::vector<PlanItem>& items, int num_sms, int TK, bool by_cost) {
   const int64_t n_ctas = std::min<int64_t>((int64_t)items.size(), num_sms);
   if ((int64_t)items.size() <= n_ctas) {
     // one item per CTA: item c is chain c
@@ -75,7 +75,9 @@ int64_t deal_chains(std::vector<PlanItem>& items, int num_sms, int TK) {
     // order and move up together -- the same owners as dealing the items
     // one by one from a min-heap of (load, chain).
     // key tiles plus one of overhead; a tile of two Q tiles costs 5/3 of one
-    auto inc = [&](const WorkItem& w) -> int64_t {
+    auto inc = [&](const PlanItem& x) -> int64_t {
+      const WorkItem& w = x.it;
+      if (by_cost) return x.cost;
       return (ceil_div(w.kv_hi - w.kv_lo, TK) + 1) * (w.nrows > kTcRowsPerTile ? 5 : 3);
     };
     std::map<int64_t, std::vector<int32_t>> levels;
@@ -86,9 +88,9 @@ int64_t deal_chains(std::vector<PlanItem>& items, int num_sms, int TK) {
     }
     std::vector<int32_t> owner(items.size()), moved, merged;
     for (size_t i = 0; i < items.size();) {
-      const int64_t x = inc(items[i].it);
+      const int64_t x = inc(items[i]);
       size_t run = 1;
-      while (i + run < items.size() && inc(items[i + run].it) == x) ++run;
+      while (i + run < items.size() && inc(items[i + run]) == x) ++run;
       while (run > 0) {
         auto lo = levels.begin();
         const int64_t level = lo->first;

@@ -27,9 +27,9 @@ struct PlanItem {
 void sort_items(std::vector<PlanItem>& items);
 
 // The chains of the persistent tcgen05 variants: the sorted items dealt to at
-// most num_sms chains, reordered and linked through next.  Returns the number
-// of chains.
-int64_t deal_chains(std::vector<PlanItem>& items, int num_sms, int TK);
+// most num_sms chains, reordered and linked through next.  An item weighs its
+// key tiles plus one, or (by_cost) its cost.  Returns the number of chains.
+int64_t deal_chains(std::vector<PlanItem>& items, int num_sms, int TK, bool by_cost = false);
 
 int check_common(int num_qo_heads, int num_kv_heads, int head_dim, int page_size, int q_dtype,
                  int kv_dtype);
