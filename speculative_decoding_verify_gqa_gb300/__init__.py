@@ -326,6 +326,13 @@ class Plan:
                     head_dim_v=int(np.frombuffer(h[168:176].tobytes(), dtype=np.int64)[0]),
                     max_nsplit=int(np.frombuffer(h[176:184].tobytes(), dtype=np.int64)[0]))
 
+    def value_width(self) -> int:
+        """Elements of an output row (read from the plan once)."""
+        dv = self.__dict__.get("_dv")
+        if dv is None:
+            dv = self._dv = int(self.host[168:176].view(np.int64)[0])
+        return dv
+
     def launches(self) -> int:
         n = ctypes.c_int(0)
         _check("verify_attn_plan_launches",
@@ -549,10 +556,10 @@ def _run_args(q, k_cache, v_cache, kv_indptr, kv_indices, last_page_len, qo_indp
 
 def _alloc_out(q, plan, out, lse, want_lse):
     if out is None:
-        dv = plan.header()["head_dim_v"]
-        out = q.new_empty(q.shape[0], q.shape[1], dv)
+        dv = plan.value_width()
+        out = torch.empty_like(q) if dv == q.shape[2] else q.new_empty(q.shape[0], q.shape[1], dv)
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[0], q.shape[1], dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     return out, lse
 
 
@@ -855,32 +862,53 @@ def verify_accept_greedy(logits, qo_indptr, draft_tokens, parents, workspace=Non
 
 
 _CODES = {torch.bfloat16: 0, torch.float32: 2}
+_CACHE_CODES = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_FP8_E4M3}
 
 
-def _current(t, name):
-    """Raise unless `t` lives on the current CUDA device (kernels are launched there)."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+_device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _current(t, name) -> int:
+    """Index of the current CUDA device, where kernels are launched; raises
+    unless `t` lives there."""
+    dev = t.get_device() if t.is_cuda else -1
+    if dev < 0 or dev != _device_index():
         raise ValueError("%s must be on the current CUDA device" % name)
+    return dev
 
 
-def _arg(t, name, dtype, shape, device):
-    """Device address of a contiguous tensor of this dtype, shape and device (None stays None)."""
+def _arg(t, name, dtype, numel, dev):
+    """Device address of a contiguous tensor of this dtype, number of elements
+    and device index (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
-                         % (name, dtype, tuple(shape), device))
+    if t.dtype is not dtype or t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of %d elements on cuda:%d"
+                         % (name, dtype, numel, dev))
     return t.data_ptr()
 
 
-def _rows(t, name, rows, vocab, device):
+def _rows(t, name, rows, vocab, dev):
     """(address, row stride) of a [rows, vocab] matrix with unit column stride; rows may be padded."""
-    if t.shape != (rows, vocab) or t.device != device or (rows and vocab > 1 and t.stride(1) != 1):
-        raise ValueError("%s must be [%d, %d] on %s with unit column stride" % (name, rows, vocab, device))
-    stride = t.stride(0) if rows > 1 else vocab
+    if t.shape != (rows, vocab) or t.get_device() != dev:
+        raise ValueError("%s must be [%d, %d] on cuda:%d" % (name, rows, vocab, dev))
+    if t.is_contiguous():
+        return t.data_ptr(), vocab
+    stride, col = t.stride()
+    if col != 1 and vocab > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    if rows <= 1:
+        stride = vocab
     if stride < vocab:
         raise ValueError("%s has overlapping rows" % name)
     return t.data_ptr(), stride
+
+
+def _device_stream(stream, dev) -> int:
+    """The cudaStream_t of `stream`, or of torch's current stream of device `dev`."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def verify_accept_sample(logits, qo_indptr, draft_tokens, parents, uniforms, noise,
@@ -894,11 +922,11 @@ def verify_accept_sample(logits, qo_indptr, draft_tokens, parents, uniforms, noi
     not sampled.  All on the current device.  Returns (accept_len [B],
     accepted_nodes [total], bonus_token [B], logprobs [total] or None), int32
     and fp32, written into `out` (such a tuple) when given."""
-    _current(logits, "logits")
+    dev = _current(logits, "logits")
     if logits.dim() != 2 or logits.dtype not in _CODES:
         raise ValueError("logits must be [total, vocab], bfloat16 or float32")
     total, vocab = logits.shape
-    dev, batch = logits.device, qo_indptr.shape[0] - 1
+    batch = qo_indptr.shape[0] - 1
     lp, ls = _rows(logits, "logits", total, vocab, dev)
     np_, ns = _rows(noise, "noise", batch, vocab, dev)
     if noise.dtype != torch.float32:
@@ -909,19 +937,21 @@ def verify_accept_sample(logits, qo_indptr, draft_tokens, parents, uniforms, noi
             raise ValueError("draft_probs must be bfloat16 or float32")
         dp, ds = _rows(draft_probs, "draft_probs", total, vocab, dev)
         dc = _CODES[draft_probs.dtype]
-    i32, f32, n, b = torch.int32, torch.float32, (total,), (batch,)
+    i32, f32 = torch.int32, torch.float32
     if out is None:
-        out = (torch.empty(b, dtype=i32, device=dev), torch.empty(n, dtype=i32, device=dev),
-               torch.empty(b, dtype=i32, device=dev),
-               torch.empty(n, dtype=f32, device=dev) if want_logprobs else None)
+        where = logits.device
+        out = (torch.empty(batch, dtype=i32, device=where), torch.empty(total, dtype=i32, device=where),
+               torch.empty(batch, dtype=i32, device=where),
+               torch.empty(total, dtype=f32, device=where) if want_logprobs else None)
     acc, path, bonus, logprobs = out
     rc = lib().verify_accept_sample(
-        lp, _CODES[logits.dtype], total, vocab, ls, _arg(qo_indptr, "qo_indptr", i32, (batch + 1,), dev),
-        batch, _arg(draft_tokens, "draft_tokens", i32, n, dev), _arg(parents, "parents", i32, n, dev),
-        _arg(uniforms, "uniforms", f32, n, dev), np_, ns, _arg(temperature, "temperature", f32, b, dev),
-        dp, dc, ds, _arg(acc, "accept_len", i32, b, dev), _arg(path, "accepted_nodes", i32, n, dev),
-        _arg(bonus, "bonus_token", i32, b, dev), _arg(logprobs, "logprobs", f32, n, dev),
-        _arg(status, "status", i32, (1,), dev), 0, _stream(stream))
+        lp, _CODES[logits.dtype], total, vocab, ls, _arg(qo_indptr, "qo_indptr", i32, batch + 1, dev), batch,
+        _arg(draft_tokens, "draft_tokens", i32, total, dev), _arg(parents, "parents", i32, total, dev),
+        _arg(uniforms, "uniforms", f32, total, dev), np_, ns,
+        _arg(temperature, "temperature", f32, batch, dev), dp, dc, ds,
+        _arg(acc, "accept_len", i32, batch, dev), _arg(path, "accepted_nodes", i32, total, dev),
+        _arg(bonus, "bonus_token", i32, batch, dev), _arg(logprobs, "logprobs", f32, total, dev),
+        _arg(status, "status", i32, 1, dev), 0, _device_stream(stream, dev))
     _check("verify_accept_sample", rc)
     return out
 
@@ -934,30 +964,31 @@ def paged_kv_compact(accept_len, accepted_nodes, qo_indptr, kv_indptr, kv_indice
     drafts); k_cache / v_cache are one layer's pool, or [layers, ...] pools of
     several layers moved in one call.  kv_len_out [B] int32 receives prefix +
     accept_len, the next step's kv lengths.  All on the current device."""
-    _current(k_cache, "k_cache")
-    if k_cache.dim() not in (4, 5) or v_cache.shape[:-1] != k_cache.shape[:-1]:
+    dev = _current(k_cache, "k_cache")
+    k_shape, v_shape = k_cache.shape, v_cache.shape
+    if len(k_shape) not in (4, 5) or v_shape[:-1] != k_shape[:-1]:
         raise ValueError("k_cache / v_cache must be [pages, ...] or [layers, pages, ...] pools of like shape")
-    if k_cache.dtype != v_cache.dtype or k_cache.dtype not in _DTYPES:
-        raise ValueError("k_cache / v_cache must both be bfloat16 or float8_e4m3fn")
-    layers = k_cache.shape[0] if k_cache.dim() == 5 else 1
+    if k_cache.dtype not in _CACHE_CODES:
+        raise ValueError("k_cache / v_cache must be bfloat16 or float8_e4m3fn")
+    layers = k_shape[0] if len(k_shape) == 5 else 1
     layout = _LAYOUTS[kv_layout]
-    num_pages, a, c, d = k_cache.shape[-4:]
+    num_pages, a, c, d = k_shape[-4:]
     page_size, h_kv = (a, c) if layout == LAYOUT_NHD else (c, a)
-    dev, i32, batch = k_cache.device, torch.int32, qo_indptr.shape[0] - 1
-    total, b = accepted_nodes.shape[0], (batch,)
+    i32, batch, total = torch.int32, qo_indptr.shape[0] - 1, accepted_nodes.shape[0]
     if kv_indices.dim() != 1:
         raise ValueError("kv_indices must be one-dimensional")
     rc = lib().paged_kv_compact(
-        _arg(accept_len, "accept_len", i32, b, dev), _arg(accepted_nodes, "accepted_nodes", i32, (total,), dev),
-        _arg(qo_indptr, "qo_indptr", i32, (batch + 1,), dev), total,
-        _arg(kv_indptr, "kv_indptr", i32, (batch + 1,), dev),
-        _arg(kv_indices, "kv_indices", i32, kv_indices.shape, dev),
-        _arg(last_page_len, "last_page_len", i32, b, dev),
-        _arg(k_cache, "k_cache", k_cache.dtype, k_cache.shape, dev),
-        _arg(v_cache, "v_cache", v_cache.dtype, v_cache.shape, dev), layers, batch, h_kv, d,
-        v_cache.shape[-1], page_size, num_pages, _DTYPES[k_cache.dtype], layout,
-        _arg(kv_len_out, "kv_len_out", i32, b, dev), _arg(status, "status", i32, (1,), dev),
-        _stream(stream))
+        _arg(accept_len, "accept_len", i32, batch, dev),
+        _arg(accepted_nodes, "accepted_nodes", i32, total, dev),
+        _arg(qo_indptr, "qo_indptr", i32, batch + 1, dev), total,
+        _arg(kv_indptr, "kv_indptr", i32, batch + 1, dev),
+        _arg(kv_indices, "kv_indices", i32, kv_indices.shape[0], dev),
+        _arg(last_page_len, "last_page_len", i32, batch, dev),
+        _arg(k_cache, "k_cache", k_cache.dtype, k_cache.numel(), dev),
+        _arg(v_cache, "v_cache", k_cache.dtype, v_cache.numel(), dev), layers, batch, h_kv, d,
+        v_shape[-1], page_size, num_pages, _CACHE_CODES[k_cache.dtype], layout,
+        _arg(kv_len_out, "kv_len_out", i32, batch, dev), _arg(status, "status", i32, 1, dev),
+        _device_stream(stream, dev))
     _check("paged_kv_compact", rc)
 
 

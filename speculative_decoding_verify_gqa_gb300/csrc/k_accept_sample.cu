@@ -79,8 +79,10 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t cta, uint6
 __device__ __forceinline__ void prefetch_l2(const void* p, int64_t bytes) {
   const uintptr_t a = (reinterpret_cast<uintptr_t>(p) + 15) & ~(uintptr_t)15,
                   z = (reinterpret_cast<uintptr_t>(p) + (uintptr_t)bytes) & ~(uintptr_t)15;
-  if (z > a)
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"((uint32_t)(z - a)) : "memory");
+  if (z > a)   // (at most 1 GB, far more than L2 holds)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a),
+                 "r"((uint32_t)(z - a < (1u << 30) ? z - a : (1u << 30)))
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -198,6 +200,19 @@ __global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const Sample
     prefetch_row(0);
     if (!greedy) prefetch_l2(noise + c0, (int64_t)(c1 - c0) * 4);
   }
+  // log2(e) / T as a float pair: a rounded factor alone would tilt the whole
+  // distribution by |logit difference| * 2^-25.  Rounded down, so that both
+  // parts are positive and a logit of -inf stays -inf (log2(e) itself is
+  // 1.4426950216 + 1.926e-8).
+  const float c_hi = greedy ? 1.f : __fdiv_rd(1.4426950216293335f, temp);
+  const float c_lo =
+      greedy ? 1.f
+             : fminf(fmaxf((fmaf(-c_hi, temp, 1.4426950216293335f) + 1.925963033500e-8f) / temp, 1e-45f), 3e38f);
+  if (tid == 0) {
+    sh.c_hi = c_hi;
+    sh.c_lo = c_lo;
+    sh.temp = temp;
+  }
   int bad = 0;
   if (tid < kNodes) {
     sh.first[tid] = kNodes;
@@ -233,20 +248,6 @@ __global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const Sample
   if (L <= kNodes && tid > 0 && tid < L) {
     atomicMin(&sh.first[sh.par[tid]], tid);
     atomicAdd(&sh.kids[sh.par[tid]], 1);
-  }
-
-  // log2(e) / T as a float pair: a rounded factor alone would tilt the whole
-  // distribution by |logit difference| * 2^-25.  Rounded down, so that both
-  // parts are positive and a logit of -inf stays -inf (log2(e) itself is
-  // 1.4426950216 + 1.926e-8).
-  const float c_hi = greedy ? 1.f : __fdiv_rd(1.4426950216293335f, temp);
-  const float c_lo =
-      greedy ? 1.f
-             : fminf(fmaxf((fmaf(-c_hi, temp, 1.4426950216293335f) + 1.925963033500e-8f) / temp, 1e-45f), 3e38f);
-  if (tid == 0) {
-    sh.c_hi = c_hi;
-    sh.c_lo = c_lo;
-    sh.temp = temp;
   }
   __syncthreads();
   const uint64_t ch2 = f32x2(c_hi, c_hi), cl2 = f32x2(c_lo, c_lo);

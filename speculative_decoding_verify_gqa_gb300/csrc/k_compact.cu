@@ -11,9 +11,11 @@
 // head), so no two threads touch the same bytes and nothing waits.  The work
 // is a copy of a few rows: bound by the chain of dependent reads (tables,
 // path, page ids, rows), so a CTA resolves its request's rows once in shared
-// memory and then keeps eight row loads in flight per thread.
+// memory and then keeps a few row loads in flight per thread.
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "../../include/verify_attn.h"
 #include "va_device.cuh"
@@ -23,9 +25,10 @@ namespace va {
 namespace {
 
 constexpr int kRows = 128;  // path entries resolved at a time
-constexpr int kBatch = 8;   // rows in flight per thread
+constexpr int kCtas = 4;    // CTAs an SM holds
+constexpr int kBatch = 4;   // rows in flight per thread
 
-__global__ void __launch_bounds__(256) paged_kv_compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(256, kCtas) paged_kv_compact_kernel(const CompactParams p) {
   __shared__ long long src_row[kRows], dst_row[kRows];  // cache row (of head 0), or -1: nothing to do
   const int b = blockIdx.y, tid = threadIdx.x;
   grid_dependency_wait();
@@ -52,19 +55,9 @@ __global__ void __launch_bounds__(256) paged_kv_compact_kernel(const CompactPara
   }
   if (bad) return;
 
-  // this thread's (layer, cache, head, chunk): layers outermost
-  const int per_head = p.k_chunks + p.v_chunks, per_layer = p.h_kv * per_head;
-  const long long idx = (long long)blockIdx.x * blockDim.x + tid;
-  const bool active = idx < (long long)p.layers * per_layer;
-  const int layer = active ? (int)(idx / per_layer) : 0;
-  const int rem = active ? (int)(idx - (long long)layer * per_layer) : 0;
-  const bool is_v = rem >= p.h_kv * p.k_chunks;
-  const int r2 = is_v ? rem - p.h_kv * p.k_chunks : rem, nch = is_v ? p.v_chunks : p.k_chunks;
-  const int head = r2 / nch, ch = r2 - head * nch;
+  const int per_layer = p.h_kv * (p.k_chunks + p.v_chunks), total = p.layers * per_layer;
   // rows of one page and layer: HND [head][slot], NHD [slot][head]
   const size_t layer_rows = (size_t)p.num_pages * p.h_kv * p.page_size;
-  uint4* base = static_cast<uint4*>(is_v ? p.v_cache : p.k_cache) +
-                ((size_t)layer * layer_rows + (p.nhd ? (size_t)head : (size_t)head * p.page_size)) * nch + ch;
   int bad_page = 0;
   for (int k0 = 0; k0 < n; k0 += kRows) {
     const int m = min(kRows, n - k0);
@@ -83,15 +76,23 @@ __global__ void __launch_bounds__(256) paged_kv_compact_kernel(const CompactPara
       src_row[k] = ps * page_rows + (s & (p.page_size - 1)) * slot_rows;
     }
     __syncthreads();
-    if (!active) continue;
-    for (int k = 0; k < m; k += kBatch) {
-      uint4 w[kBatch];
+    // this thread's (layer, cache, head, chunk)s: layers outermost
+    for (int idx = blockIdx.x * blockDim.x + tid; idx < total; idx += gridDim.x * blockDim.x) {
+      const int layer = idx / per_layer, rem = idx - layer * per_layer;
+      const bool is_v = rem >= p.h_kv * p.k_chunks;
+      const int r2 = is_v ? rem - p.h_kv * p.k_chunks : rem, nch = is_v ? p.v_chunks : p.k_chunks;
+      const int head = r2 / nch, ch = r2 - head * nch;
+      uint4* base = static_cast<uint4*>(is_v ? p.v_cache : p.k_cache) +
+                    ((size_t)layer * layer_rows + (p.nhd ? (size_t)head : (size_t)head * p.page_size)) * nch + ch;
+      for (int k = 0; k < m; k += kBatch) {
+        uint4 w[kBatch];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (k + j < m && src_row[k + j] >= 0) w[j] = base[src_row[k + j] * nch];
+        for (int j = 0; j < kBatch; ++j)
+          if (k + j < m && src_row[k + j] >= 0) w[j] = base[src_row[k + j] * nch];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (k + j < m && src_row[k + j] >= 0) base[dst_row[k + j] * nch] = w[j];
+        for (int j = 0; j < kBatch; ++j)
+          if (k + j < m && src_row[k + j] >= 0) base[dst_row[k + j] * nch] = w[j];
+      }
     }
   }
   if (bad_page && blockIdx.x == 0 && p.status) atomicOr(p.status, VA_DEV_BAD_PAGE);
@@ -100,9 +101,13 @@ __global__ void __launch_bounds__(256) paged_kv_compact_kernel(const CompactPara
 }  // namespace
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
+  if (p.batch > 65535) return cudaErrorInvalidValue;
+  // At most the CTAs that are resident together (kCtas on each of 152 SMs): every
+  // CTA of a request walks the same tables first, and a second wave would
+  // do so after the first.
   const long long threads = (long long)p.layers * p.h_kv * (p.k_chunks + p.v_chunks);
-  const long long blocks = (threads + 255) / 256;
-  if (blocks > 0x7fffffffLL || p.batch > 65535) return cudaErrorInvalidValue;
+  const long long most = std::max(1, kCtas * 152 / p.batch);
+  const long long blocks = std::min<long long>((threads + 255) / 256, most);
   void* args[] = {const_cast<CompactParams*>(&p)};
   return launch_kernel(reinterpret_cast<const void*>(paged_kv_compact_kernel),
                        dim3((unsigned)blocks, (unsigned)p.batch), dim3(256), 0, stream, args, /*pdl=*/true);

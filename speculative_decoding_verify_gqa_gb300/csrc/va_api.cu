@@ -1075,7 +1075,7 @@ int paged_kv_compact(const int32_t* accept_len, const int32_t* accepted_nodes,
   p.k_chunks = head_dim * es / 16;
   p.v_chunks = head_dim_v * es / 16;
   p.nhd = kv_layout == VA_LAYOUT_NHD;
-  if ((int64_t)num_layers * num_kv_heads * (p.k_chunks + p.v_chunks) > 0x7fffffffLL) return VA_ERR_UNSUPPORTED;
+  if ((int64_t)num_layers * num_kv_heads * (p.k_chunks + p.v_chunks) > (1 << 30)) return VA_ERR_UNSUPPORTED;
   cudaError_t e = launch_compact(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }

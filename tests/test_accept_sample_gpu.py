@@ -42,7 +42,7 @@ def _parents(lens, kind, rng):
 
 
 def _inputs(seed, lens, vocab, kind="tree", ldt=torch.bfloat16, qdt=None, temps=None, masked=0.0, spread=2.0,
-            pad=0, u_min=0.0):
+            pad=0, u_min=0.0, u_max=1.0, near=0.5, greedy_drafts=False):
     """Peaked logits (a few hot tokens a row), drafts sampled from the draft
     distribution, or, without one, the likeliest tokens (repeats among them)."""
     rng = np.random.default_rng(seed)
@@ -61,7 +61,7 @@ def _inputs(seed, lens, vocab, kind="tree", ldt=torch.bfloat16, qdt=None, temps=
     par = _parents(lens, kind, rng)
     req = np.repeat(np.arange(B), lens)
     t = None if temps is None else np.array([temps[b % len(temps)] for b in range(B)], np.float32)
-    x = host / np.maximum(np.ones(total) if t is None else t[req], 0.3)[:, None] + rng.standard_normal((total, vocab)) * 0.5
+    x = host / np.maximum(np.ones(total) if t is None else t[req], 0.3)[:, None] + rng.standard_normal((total, vocab)) * near
     x = np.exp(x - x.max(1, keepdims=True))
     q = x / x.sum(1, keepdims=True)
     rows = np.array([indptr[req[i]] + max(int(par[i]), 0) for i in range(total)], np.int64)
@@ -73,7 +73,9 @@ def _inputs(seed, lens, vocab, kind="tree", ldt=torch.bfloat16, qdt=None, temps=
         toks = (q[rows] / rng.exponential(size=(total, vocab))).argmax(1).astype(np.int32) if total else np.zeros(0, np.int32)
         dp = torch.from_numpy(np.concatenate([q, np.full((total, pad), np.nan)], 1)).to(qdt)
         dp_host = dp.double().numpy()[:, :vocab]
-    u = (u_min + (1 - u_min) * rng.random(total)).astype(np.float32)
+    if greedy_drafts:
+        toks = host[rows].argmax(1).astype(np.int32)
+    u = (u_min + (u_max - u_min) * rng.random(total)).astype(np.float32)
     u = np.minimum(u, np.float32(1 - 2.0 ** -24))
     noise = rng.exponential(size=(B, vocab + pad)).astype(np.float32)
     return dict(lg=lg, host=host, indptr=indptr, par=par, toks=toks, u=u, noise=noise, t=t, dp=dp, dp_host=dp_host,
@@ -139,6 +141,9 @@ CASES = {
     "star_no_q_late": dict(lens=[150, 90], vocab=300, kind="star", u_min=0.97),
     "star_q_late": dict(lens=[70, 40], vocab=500, kind="star", qdt=F, temps=[1.5], u_min=0.9),
     "star_bf16_q_late": dict(lens=[12, 20], vocab=8192, kind="star", qdt=H, u_min=0.95),
+    "big_tree_q": dict(lens=[300, 2], vocab=600, qdt=F),                     # past what shared memory keeps of a tree
+    "long_chain": dict(lens=[400, 140], vocab=40, kind="chain", qdt=F, near=0.0, u_max=0.4),   # hundreds accepted
+    "long_chain_greedy": dict(lens=[200], vocab=300, kind="chain", temps=[0.0], greedy_drafts=True),
     "star_q": dict(lens=[70, 40], vocab=1000, kind="star", qdt=F, temps=[1.5]),
     "many_requests": dict(lens=[3] * 330, vocab=64, kind="chain", qdt=F),    # one CTA each
     "two_ctas": dict(lens=[2] * 120, vocab=9000, kind="chain", qdt=H),
@@ -331,6 +336,20 @@ def test_graph_replay_and_side_stream(va):
         g.replay()
         torch.cuda.synchronize()
         _same(c, out)
+
+
+def test_rows_far_apart(va):
+    """Row and noise offsets past 2^32 bytes."""
+    c = _case(31, lens=[2, 1], vocab=4096, kind="chain", qdt=F)
+    a = _dev(c)
+    far = 1 << 30
+    big = torch.empty(2 * far + 4096, dtype=H, device="cuda")
+    lg = big.as_strided((3, 4096), (far, 1))
+    lg.copy_(a[0])
+    nbig = torch.empty(far + 4096 + 4, dtype=F, device="cuda")
+    noise = nbig[4:].as_strided((2, 4096), (far, 1))
+    noise.copy_(a[5])
+    _same(c, va.verify_accept_sample(lg, *a[1:5], noise, draft_probs=a[7], want_logprobs=True))
 
 
 def test_refusals(va):

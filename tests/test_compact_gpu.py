@@ -159,6 +159,24 @@ def test_graph_replay_and_side_stream(va):
         assert np.array_equal(kv_len.cpu().numpy(), new)
 
 
+def test_offsets_past_32_bits(va):
+    """Rows beyond 4 GB of a pool (the slots are compared, not the pool)."""
+    pages, h, P, d = 140000, 8, 16, 128
+    pool = [torch.empty((pages, h, P, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    assert pool[0].numel() * 2 > 1 << 32
+    i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    last = pages - 1
+    for x in pool:
+        x[last].normal_()
+        x[2].normal_()
+    want = [(x[last, :, 3].clone(), x[2, :, 1].clone()) for x in pool]
+    # prefix 13: drafts 0 .. 2 on the last page's slots 13 .. 15, 3 .. 5 on page 2's 0 .. 2
+    keep = [x[last, :, 13].clone() for x in pool]
+    va.paged_kv_compact(i(2), i(0, 4, -1, -1, -1, -1), i(0, 6), i(0, 2), i(last, 2), i(3), *pool)
+    for x, (a, b), k in zip(pool, want, keep):
+        assert torch.equal(x[last, :, 13], k) and torch.equal(x[last, :, 14], b) and torch.equal(x[last, :, 3], a)
+
+
 def test_refusals(va):
     c = _case(4, lens=[3], pre=[1], acc=[2], page=16, h_kv=2, d=64)
     t = _dev(c)
