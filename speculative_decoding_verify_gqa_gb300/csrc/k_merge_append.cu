@@ -285,6 +285,8 @@ static cudaError_t launch_merge_d(const MergeParams& p, int n_merge, int block_r
   void* args[] = {const_cast<MergeParams*>(&p)};
   const void* k = max_nsplit <= 4   ? reinterpret_cast<const void*>(verify_merge_kernel<D, 4, SHARED>)
                   : max_nsplit <= 8 ? reinterpret_cast<const void*>(verify_merge_kernel<D, 8, SHARED>)
+                  : SHARED && max_nsplit <= 12
+                      ? reinterpret_cast<const void*>(verify_merge_kernel<D, 12, true>)
                                     : reinterpret_cast<const void*>(verify_merge_kernel<D, 24, SHARED>);
   return launch_kernel(k, grid, dim3(128), 0, stream, args, /*pdl=*/true);
 }
