@@ -41,7 +41,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kRows = 4;        // rows of a pass at most
+constexpr int kRows = 8;        // rows of a pass at most
 constexpr int kChildList = 64;  // children's tokens kept in shared memory (further ones are searched)
 constexpr int kMarks = 32;
 constexpr int kNodes = 128;     // a tree of at most so many nodes is kept in shared memory
@@ -126,6 +126,7 @@ struct RowState {
   int am, dead;             // first argmax (T = 0); nothing of the row is possible
   int next, more;           // the accepted child, or -1; a residual's sum is wanted first
   int n_child;
+  int kid[32];              // the children now in the lanes of the row's warp
   uint32_t marks[kMarks];   // bit (x >> 3) mod 32 kMarks for every child's token x
   int child_tok[kChildList];
 };
@@ -168,7 +169,7 @@ __device__ __forceinline__ uint64_t scale64(uint64_t a, float w) {
 
 // LB: logits bf16 (else fp32).  QT: draft distributions: 0 none, 1 bf16, 2 fp32.
 template <bool LB, int QT>
-__global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const SampleParams p) {
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = p.cluster;
@@ -297,92 +298,93 @@ __global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const Sample
   if (tid == 0 && rank == 0) p.path[o] = 0;
   for (;;) {
     // ---- the rows of this pass: the first child's always, those below it
-    // while no node has a choice.  Four rows of a chain at once took 11.6 us
-    // against 13.4 with two and 17.3 with one (4 drafts, 32,016 tokens); in
-    // a wide tree two are best (16.4 us against 18.7 with one and with four).
-    int node[kRows], n = 1;
-    node[0] = v;
-    bool alone = true;
-#pragma unroll
-    for (int r = 1; r < kRows; ++r) {
-      node[r] = -1;
-      if (n != r || L > kNodes) continue;
-      const int kids = sh.kids[node[r - 1]];
-      alone = alone && kids == 1;
-      if (kids > 0 && (r == 1 || alone)) {
-        node[r] = sh.first[node[r - 1]];
-        ++n;
+    // while no node has a choice.  A chain of 4 drafts (32,016 tokens) took
+    // 10.1 us with up to eight rows, 11.5 with four, 13.4 with two and 17.3 with one;
+    // in a wide tree two are best (16.4 us against 18.7 with one and with four).
+    // The host asks for eight rows where the batch leaves SMs idle, else for
+    // four: 64 ragged chains took 47.8 us with four and 52.1 with eight, whose
+    // rows past the accepted ones are read from HBM for nothing.
+    int n = 1, mine = warp == 0 ? v : -1;   // rows; the node that this warp decides about
+    if (L <= kNodes) {
+      bool alone = true;
+      for (int at = v; n < p.rows; ++n) {
+        const int kids = sh.kids[at];
+        alone = alone && kids == 1;
+        if (kids == 0 || (n > 1 && !alone)) break;
+        at = sh.first[at];
+        if (warp == n) mine = at;
       }
     }
-    int mine = -1;   // the node that this warp decides about
-#pragma unroll
-    for (int r = 0; r < kRows; ++r)
-      if (warp == r) mine = node[r];
     if (mine >= 0 && lane == 0) prefetch_row(mine);
 
-    // ---- its children, 32 nodes at a time: what each lane's node needs is
+    // ---- its children, up to 32 at a time, one a lane: what they need is
     // asked for before the pass over the rows, so it arrives meanwhile
     RowState& rs = sh.row[warp & (kRows - 1)];
     const void* const row = row_of(max(mine, 0));
     const void* const qrow = qrow_of(max(mine, 0));
-    int base = mine + 1 - 32;
-    uint32_t win = 0;   // children in the window base .. base + 31 not yet tried
-    int ctok = -1;
+    int scan = mine + 1;   // the next node to look at
+    uint32_t win = 0;      // lanes whose child has not been tried
+    int kid = -1, ctok = -1;
     float cx = -INFINITY, cq = 0.f, cu = 0.f;   // token's logit and draft probability, the child's number
-    auto load_window = [&]() {
-      for (base += 32; base < L && win == 0; base += 32) {
-        const int i = base + lane;
-        win = __ballot_sync(0xffffffffu, i < L && par[i] == mine);
-        if (win == 0) continue;
-        ctok = -1;
-        cx = -INFINITY;
-        cq = cu = 0.f;
-        if ((win >> lane) & 1u) {
-          ctok = tok[i];
-          cu = uni[i];
-          if (ctok >= 0 && ctok < V) {
-            cx = load_elem<LB>(row, ctok);
-            if (QT) cq = load_elem<QT == 1>(qrow, ctok);
-          }
-        }
-        if (!QT) {
-          // q one-hot: an earlier sibling's equal token was rejected before
-          // this one, so nothing of it is left
-          const uint32_t before = win & ((1u << lane) - 1u);
-          bool dup = (__match_any_sync(0xffffffffu, ctok) & before) != 0;
-          const int n0 = rs.n_child, at = n0 + __popc(before);
-          for (int j = 0; j < min(n0, kChildList); ++j) dup |= rs.child_tok[j] == ctok;
-          if (n0 > kChildList)
-            for (int j = mine + 1; j < base; ++j) dup |= par[j] == mine && tok[j] == ctok;
-          if (dup) cx = -INFINITY;
-          if ((win >> lane) & 1u) {
-            if (at < kChildList) rs.child_tok[at] = ctok;
-            atomicOr(&rs.marks[(ctok >> 8) & (kMarks - 1)], 1u << ((ctok >> 3) & 31));
-          }
-          __syncwarp();
-          if (lane == 0) rs.n_child = n0 + __popc(win);
-          __syncwarp();
-        }
-        break;
+    auto load_children = [&]() {
+      int cnt = 0;
+      while (scan < L && cnt < 32) {
+        const int i = scan + lane;
+        const bool is = i < L && par[i] == mine;
+        const uint32_t m = __ballot_sync(0xffffffffu, is);
+        const int pos = cnt + __popc(m & ((1u << lane) - 1u));
+        if (is && pos < 32) rs.kid[pos] = i;
+        const uint32_t full = __ballot_sync(0xffffffffu, is && pos == 31);
+        cnt = min(32, cnt + __popc(m));
+        scan += full ? __ffs(full) : 32;   // go on behind the 32nd
       }
+      __syncwarp();
+      win = cnt < 32 ? (1u << cnt) - 1u : 0xffffffffu;
+      kid = ctok = -1;
+      cx = -INFINITY;
+      cq = cu = 0.f;
+      if (lane < cnt) {
+        kid = rs.kid[lane];
+        ctok = tok[kid];
+        cu = uni[kid];
+        if (ctok >= 0 && ctok < V) {
+          cx = load_elem<LB>(row, ctok);
+          if (QT) cq = load_elem<QT == 1>(qrow, ctok);
+        }
+      }
+      if (!QT && cnt > 0) {
+        // q one-hot: an earlier sibling's equal token was rejected before
+        // this one, so nothing of it is left
+        bool dup = (__match_any_sync(0xffffffffu, ctok) & ((1u << lane) - 1u)) != 0;
+        const int n0 = rs.n_child, at = n0 + lane;
+        for (int j = 0; j < min(n0, kChildList); ++j) dup |= rs.child_tok[j] == ctok;
+        if (n0 > kChildList)
+          for (int j = mine + 1; j < kid; ++j) dup |= par[j] == mine && tok[j] == ctok;
+        if (dup) cx = -INFINITY;
+        if (lane < cnt) {
+          if (at < kChildList) rs.child_tok[at] = ctok;
+          atomicOr(&rs.marks[(ctok >> 8) & (kMarks - 1)], 1u << ((ctok >> 3) & 31));
+        }
+        __syncwarp();
+        if (lane == 0) rs.n_child = n0 + cnt;
+      }
+      __syncwarp();
     };
     if (mine >= 0) {
       rs.marks[lane] = 0;
       if (lane == 0) rs.n_child = 0;
       __syncwarp();
-      load_window();
+      load_children();
     }
 
     // ---- each row's maximum and sum over the slice (T = 0: its first argmax).
     // The warps are shared out among the rows, so that every row's loads are in
     // flight at once and each warp reduces once.
-    const int row_warps = kWarps / (n > 2 ? 4 : n);
+    const int row_warps = kWarps / (n > 4 ? 8 : n > 2 ? 4 : n);
     const int r_mine = warp / row_warps, w_mine = warp - r_mine * row_warps;
     if (r_mine < n) {
-      int i_row = node[0];
-#pragma unroll
-      for (int j = 1; j < kRows; ++j)
-        if (r_mine == j) i_row = node[j];
+      int i_row = v;
+      for (int j = 0; j < r_mine; ++j) i_row = sh.first[i_row];
       const void* x_row = row_of(i_row);
       const int t0 = w_mine * 32 + lane, step = row_warps * 32;
       // 16-byte loads over the aligned middle of the slice, single elements at the ends
@@ -508,12 +510,17 @@ __global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const Sample
     float cw = 0.f, sf = 0.f;             // weight of the child's token: sum times its probability
     double A = 0.0, B = 1.0;
     auto child_w = [&]() { return greedy ? (ctok == am && cx > -INFINITY ? 1.f : 0.f) : weight(cx, m); };
+    // u q B < p - A q, times the sum, in fp64: where fp32 is too close to tell
+    auto precisely = [&](float x, float q, float u, double b) {
+      const double w = exp(((double)x - (double)m) / (double)sh.temp);
+      return (double)u * b * (double)q * sum < w - (QT ? A * (double)q * sum : 0.0);
+    };
     auto decide = [&]() {
       int next = -1, more = 0;
       float nx = 0.f;
       while (!dead) {
         if (win == 0) {
-          load_window();
+          load_children();
           if (win == 0) break;
           cw = child_w();
         }
@@ -521,34 +528,61 @@ __global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const Sample
           more = 1;
           break;
         }
-        const int j = __ffs(win) - 1;
-        win &= win - 1;
-        const float wj = __shfl_sync(0xffffffffu, cw, j), xj = __shfl_sync(0xffffffffu, cx, j);
-        const float qj = QT ? __shfl_sync(0xffffffffu, cq, j) : 1.f, uj = __shfl_sync(0xffffffffu, cu, j);
-        bool ok;
-        if (greedy) {
-          ok = wj > 0.f;
-        } else {
-          // u q B < p - A q, times the sum.  In fp32, and once more in fp64
-          // where that is too close to tell.
-          const float lhs = uj * (float)B * qj * sf, aq = QT ? (float)A * qj * sf : 0.f;
-          ok = lhs < wj - aq;
-          if (fabsf(wj - aq - lhs) <= 4e-6f * (wj + aq + lhs) && xj > -INFINITY) {
-            const double w = exp(((double)xj - (double)m) / (double)sh.temp);
-            ok = (double)uj * B * (double)qj * sum < w - (QT ? A * (double)qj * sum : 0.0);
+        if constexpr (QT == 0) {
+          // every lane its own child: B is what the children before it leave
+          float before = cw;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= d) before += y;
           }
-        }
-        if (ok) {
-          next = base + j;
-          nx = xj;
-          break;
-        }
-        if (greedy) continue;
-        if (QT) {
+          const float all = __shfl_sync(0xffffffffu, before, 31);
+          before -= cw;
+          const float lhs = greedy ? 0.f : cu * ((float)B * sf - before);
+          const bool near = !greedy && fabsf(cw - lhs) <= 4e-6f * (cw + sf) && cx > -INFINITY;
+          const bool ok = greedy ? cw > 0.f : lhs < cw;
+          uint32_t may = __ballot_sync(0xffffffffu, (ok || near) && ((win >> lane) & 1u));
+          const uint32_t close = __ballot_sync(0xffffffffu, near);
+          while (may) {
+            const int j = __ffs(may) - 1;
+            const float xj = __shfl_sync(0xffffffffu, cx, j), uj = __shfl_sync(0xffffffffu, cu, j);
+            bool yes = true;
+            if ((close >> j) & 1u) {
+              double b = B;
+              for (int i = 0; i < j; ++i) b -= (double)__shfl_sync(0xffffffffu, cw, i) / sum;
+              yes = precisely(xj, 1.f, uj, b);
+            }
+            if (yes) {
+              next = __shfl_sync(0xffffffffu, kid, j);
+              nx = xj;
+              break;
+            }
+            may &= may - 1;
+          }
+          win = 0;
+          if (next >= 0) break;
+          if (!greedy) B -= (double)(all / sf);
+        } else {
+          const int j = __ffs(win) - 1;
+          win &= win - 1;
+          const float wj = __shfl_sync(0xffffffffu, cw, j), xj = __shfl_sync(0xffffffffu, cx, j);
+          const float qj = __shfl_sync(0xffffffffu, cq, j), uj = __shfl_sync(0xffffffffu, cu, j);
+          bool ok;
+          if (greedy) {
+            ok = wj > 0.f;
+          } else {
+            const float lhs = uj * (float)B * qj * sf, aq = (float)A * qj * sf;
+            ok = lhs < wj - aq;
+            if (fabsf(wj - aq - lhs) <= 4e-6f * (wj + aq + lhs) && xj > -INFINITY) ok = precisely(xj, qj, uj, B);
+          }
+          if (ok) {
+            next = __shfl_sync(0xffffffffu, kid, j);
+            nx = xj;
+            break;
+          }
+          if (greedy) continue;
           A += B;
           pending = true;
-        } else {
-          B -= (double)(wj / sf);
         }
       }
       pending = false;
@@ -635,12 +669,10 @@ __global__ void __launch_bounds__(kThreads, 2) accept_sample_kernel(const Sample
         }
       }
       ++k;
+      // the pass's next row is the first child's
+      const bool ahead = r + 1 < n && to == sh.first[at];
       at = to;
-      int ahead = -1;   // the node of the pass's next row
-#pragma unroll
-      for (int j = 1; j < kRows; ++j)
-        if (j == r + 1) ahead = node[j];
-      if (to != ahead) break;
+      if (!ahead) break;
       ++r;
     }
     if (to >= 0) {

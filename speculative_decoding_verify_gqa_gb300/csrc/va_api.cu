@@ -963,9 +963,11 @@ int verify_accept_greedy(const void* logits, va_dtype logits_dtype, int64_t tota
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }
 
-// CTAs per request of the sampled acceptance: enough that the batch fills the
-// GPU twice over (two CTAs fit an SM), each with at least 4096 vocabulary
-// entries.  A power of two up to the portable cluster size.
+// CTAs per request of the sampled acceptance: a power of two up to the
+// portable cluster size, at most two CTAs an SM over the batch -- 64 ragged
+// chains over 128,256 tokens took 49 us with four CTAs each, 55 with two and
+// 66 with eight -- and at least 4096 entries a CTA (a chain of 4 drafts over
+// 32,016 tokens: 9.3 us with eight CTAs, 10.7 with four).
 static int sample_cluster(int batch, int vocab, int num_sms) {
   int c = 1;
   while (c < 8 && (int64_t)batch * c * 2 <= 2LL * num_sms && vocab > 4096 * c) c *= 2;
@@ -1025,6 +1027,7 @@ int verify_accept_sample(const void* logits, va_dtype logits_dtype, int64_t tota
   p.vocab = vocab;
   p.batch = batch;
   p.cluster = sample_cluster(batch, vocab, num_sms);
+  p.rows = p.batch * p.cluster <= num_sms ? 8 : 4;
   p.slice = ((vocab + p.cluster - 1) / p.cluster + 7) / 8 * 8;
   p.vec = vocab % 8 == 0 && la % 16 == 0 && row_stride * les % 16 == 0 && na % 16 == 0 &&
           noise_stride % 4 == 0 && (!draft_probs || (qa % 16 == 0 && draft_stride * qes % 16 == 0));

@@ -135,6 +135,7 @@ struct SampleParams {
   int64_t row_stride, draft_stride, noise_stride;  // elements
   int total, vocab, batch;
   int cluster;                // CTAs per request
+  int rows;                   // rows of a pass (see the kernel), at most 8
   int slice;                  // vocabulary entries per CTA (a multiple of 8)
   int vec;                    // every row starts on 16 bytes and holds a multiple of 8 entries
 };
