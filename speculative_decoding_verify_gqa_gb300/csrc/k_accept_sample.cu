@@ -73,6 +73,11 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t cta, uint6
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(cta));
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
 }
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t cta, uint32_t v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(cta));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 
 // Ask for [p, p + bytes) to be brought into L2, rounded inwards to 16 bytes:
 // one instruction, by one thread.
@@ -133,6 +138,8 @@ struct RowState {
 struct Shared {
   uint64_t part_a[kRows][kWarps], part_b[kRows][kWarps];
   uint64_t ex_a[2][kRows][kMaxCluster], ex_b[2][kRows][kMaxCluster];  // the cluster's exchange, two phases
+  uint32_t ex_tag[2][kMaxCluster];                                    // where each CTA's walk stands
+  int o, L;                                                           // the request's first row, its nodes
   RowState row[kRows];
   int par[kNodes], tok[kNodes], first[kNodes], kids[kNodes];  // parents, tokens, first children, their number
   float u[kNodes];
@@ -140,7 +147,7 @@ struct Shared {
   double lsum[kNodes];
   // read again where fp64 needs them: kept in registers, their conversions
   // would be hoisted and done by every thread, on a pipe of two lanes a cycle
-  volatile float c_hi, c_lo, temp;
+  volatile float c_hi, c_lo, temp;   // (temp: the request's temperature)
 };
 
 // Sums of weights and residuals cross threads as fixed-point integers: adding
@@ -177,9 +184,21 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   cluster_arrive();  // waited for before the first store to another CTA's shared memory
   grid_dependency_wait();
   grid_dependents_launch();
-  const int o = p.qo_indptr[b];
-  const int L = p.qo_indptr[b + 1] - o;
-  const float temp = p.temperature ? p.temperature[b] : 1.f;
+  // read once, for every thread: what steers the barriers below is the same
+  // throughout the CTA even if the caller's tables change under it
+  if (tid == 0) {
+    const int o = p.qo_indptr[b];
+    sh.o = o;
+    sh.L = p.qo_indptr[b + 1] - o;
+    sh.temp = p.temperature ? p.temperature[b] : 1.f;
+  }
+  if (tid < kNodes) {
+    sh.first[tid] = kNodes;
+    sh.kids[tid] = 0;
+  }
+  __syncthreads();
+  const int o = sh.o, L = sh.L;
+  const float temp = sh.temp;
   const bool table_ok = o >= 0 && L >= 0 && (int64_t)o + L <= p.total;
   const int V = p.vocab;
   const int c0 = (int)min((int64_t)V, (int64_t)rank * p.slice), c1 = (int)min((int64_t)V, (int64_t)c0 + p.slice);
@@ -218,13 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   if (tid == 0) {
     sh.c_hi = c_hi;
     sh.c_lo = c_lo;
-    sh.temp = temp;
   }
   int bad = 0;
-  if (tid < kNodes) {
-    sh.first[tid] = kNodes;
-    sh.kids[tid] = 0;
-  }
   if (table_ok)
     for (int i = tid; i < L; i += kThreads) {
       const int par = p.parents[o + i];
@@ -237,19 +251,48 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     }
   bad = __syncthreads_or(bad) || !table_ok || !(temp >= 0.f && temp < INFINITY);
   cluster_wait();
-  if (bad || L == 0) {  // the same in every CTA of the cluster
-    if (rank == 0) {
-      if (tid == 0) {
-        p.accept_len[b] = 0;
-        p.bonus[b] = -1;
-        if (bad && p.status) atomicOr(p.status, VA_DEV_BAD_TABLE);
-      }
-      if (table_ok)
-        for (int i = tid; i < L; i += kThreads) {
-          p.path[o + i] = -1;
-          if (p.logprobs) p.logprobs[o + i] = 0.f;
-        }
+
+  // The exchange: lane k of a warp that has a row's words sends them to CTA k,
+  // and after the barrier every CTA has all of them in sh.ex_a / ex_b
+  // [phase][row][0 .. C).  The two phases alternate, so a CTA that runs ahead
+  // never writes what a slower one still reads.  With them goes a tag of where
+  // the sender's walk stands.  Every CTA computes the same walk from the same
+  // inputs; should they differ -- inputs written while they are read -- all of
+  // them see it at the same barrier and end there, before one waits for, or
+  // writes to, another that has left.
+  int phase = 0;
+  auto send = [&](int r, uint64_t x, uint64_t y) {
+    if (lane < C) {
+      cluster_store(smem_u32(&sh.ex_a[phase][r][rank]), lane, x);
+      cluster_store(smem_u32(&sh.ex_b[phase][r][rank]), lane, y);
     }
+    __syncwarp();
+  };
+  auto agree = [&](uint32_t tag) -> bool {  // every thread; after the senders' send()
+    if (warp == kWarps - 1 && lane < C) cluster_store(smem_u32(&sh.ex_tag[phase][rank]), lane, tag);
+    __syncwarp();
+    cluster_sync();
+    return __all_sync(0xffffffffu, lane >= C || sh.ex_tag[phase][lane] == sh.ex_tag[phase][0]);
+  };
+  enum : uint32_t { kStats = 1u << 28, kResidual = 2u << 28, kBonus = 3u << 28, kEnd = 4u << 28, kNone = 5u << 28 };
+  // no answer: the request's outputs say so
+  auto give_up = [&](bool flag) {
+    if (rank != 0) return;
+    if (tid == 0) {
+      p.accept_len[b] = 0;
+      p.bonus[b] = -1;
+      if (flag && p.status) atomicOr(p.status, VA_DEV_BAD_TABLE);
+    }
+    if (table_ok)
+      for (int i = tid; i < L; i += kThreads) {
+        p.path[o + i] = -1;
+        if (p.logprobs) p.logprobs[o + i] = 0.f;
+      }
+  };
+  if (bad || L == 0) {
+    phase ^= 1;   // as the first exchange of a walk
+    const bool same = agree(kNone);
+    give_up(bad || !same);
     return;
   }
   if (L <= kNodes && tid > 0 && tid < L) {
@@ -269,19 +312,6 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   auto weight = [&](float x, float m) {
     const float d = x - m;
     return ex2(fmaf(d, c_hi, d * c_lo));
-  };
-
-  // The exchange: lane k of a warp that has a row's words sends them to CTA k,
-  // and after the barrier every CTA has all of them in sh.ex_a / ex_b
-  // [phase][row][0 .. C).  The two phases alternate, so a CTA that runs ahead
-  // never writes what a slower one still reads.
-  int phase = 0;
-  auto send = [&](int r, uint64_t x, uint64_t y) {
-    if (lane < C) {
-      cluster_store(smem_u32(&sh.ex_a[phase][r][rank]), lane, x);
-      cluster_store(smem_u32(&sh.ex_b[phase][r][rank]), lane, y);
-    }
-    __syncwarp();
   };
 
   const int32_t* par = L <= kNodes ? sh.par : p.parents + o;
@@ -423,68 +453,68 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         best = warp_max64(best);
         if (lane == 0) sh.part_a[r_mine][w_mine] = best;
       } else {
-      // running maximum and sum, eight vectors at a time
-      float m = -INFINITY, s = 0.f;
-      constexpr int NV = 8;
-      for (int i0 = t0; i0 < nvec; i0 += NV * step) {
-        uint4 w[NV];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int i = i0 + j * step;
-          const uint32_t ninf = LB ? 0xff80ff80u : 0xff800000u;
-          w[j] = i < nvec ? __ldg(vp + i) : make_uint4(ninf, ninf, ninf, ninf);
-        }
-        float mx;
-        if constexpr (LB) {   // the maximum in bf16 pairs
-          uint32_t v2 = w[0].x;
-#pragma unroll
-          for (int j = 0; j < NV; ++j)
-            v2 = max_bf16x2(max_bf16x2(v2, w[j].x), max_bf16x2(w[j].y, max_bf16x2(w[j].z, w[j].w)));
-          mx = fmaxf(__uint_as_float(v2 << 16), __uint_as_float(v2 & 0xffff0000u));
-        } else {
-          mx = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < NV; ++j)
-            mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(w[j].x), __uint_as_float(w[j].y))),
-                       fmaxf(__uint_as_float(w[j].z), __uint_as_float(w[j].w)));
-        }
-        if (mx > m) {
-          s = m == -INFINITY ? 0.f : s * weight(m, mx);
-          m = mx;
-        }
-        if (m == -INFINITY) continue;
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          if (i0 + j * step >= nvec) break;
-          const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-          for (int q = 0; q < (LB ? 4 : 2); ++q) {
-            float w0, w1;
-            if (LB) weight2(__uint_as_float(u[q] << 16), __uint_as_float(u[q] & 0xffff0000u), m, &w0, &w1);
-            else weight2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]), m, &w0, &w1);
-            s0 += w0;
-            s1 += w1;
+        // running maximum and sum, eight vectors at a time
+        float m = -INFINITY, s = 0.f;
+        constexpr int NV = 8;
+        for (int i0 = t0; i0 < nvec; i0 += NV * step) {
+          uint4 w[NV];
+  #pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            const int i = i0 + j * step;
+            const uint32_t ninf = LB ? 0xff80ff80u : 0xff800000u;
+            w[j] = i < nvec ? __ldg(vp + i) : make_uint4(ninf, ninf, ninf, ninf);
           }
+          float mx;
+          if constexpr (LB) {   // the maximum in bf16 pairs
+            uint32_t v2 = w[0].x;
+  #pragma unroll
+            for (int j = 0; j < NV; ++j)
+              v2 = max_bf16x2(max_bf16x2(v2, w[j].x), max_bf16x2(w[j].y, max_bf16x2(w[j].z, w[j].w)));
+            mx = fmaxf(__uint_as_float(v2 << 16), __uint_as_float(v2 & 0xffff0000u));
+          } else {
+            mx = -INFINITY;
+  #pragma unroll
+            for (int j = 0; j < NV; ++j)
+              mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(w[j].x), __uint_as_float(w[j].y))),
+                         fmaxf(__uint_as_float(w[j].z), __uint_as_float(w[j].w)));
+          }
+          if (mx > m) {
+            s = m == -INFINITY ? 0.f : s * weight(m, mx);
+            m = mx;
+          }
+          if (m == -INFINITY) continue;
+          float s0 = 0.f, s1 = 0.f;
+  #pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            if (i0 + j * step >= nvec) break;
+            const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+  #pragma unroll
+            for (int q = 0; q < (LB ? 4 : 2); ++q) {
+              float w0, w1;
+              if (LB) weight2(__uint_as_float(u[q] << 16), __uint_as_float(u[q] & 0xffff0000u), m, &w0, &w1);
+              else weight2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]), m, &w0, &w1);
+              s0 += w0;
+              s1 += w1;
+            }
+          }
+          s += s0 + s1;
         }
-        s += s0 + s1;
-      }
-      for (int i = t0; i < n_end; i += step) {
-        const float x = load_elem<LB>(x_row, end_at(i));
-        if (x > m) {
-          s = m == -INFINITY ? 0.f : s * weight(m, x);
-          m = x;
+        for (int i = t0; i < n_end; i += step) {
+          const float x = load_elem<LB>(x_row, end_at(i));
+          if (x > m) {
+            s = m == -INFINITY ? 0.f : s * weight(m, x);
+            m = x;
+          }
+          if (m > -INFINITY) s += weight(x, m);
         }
-        if (m > -INFINITY) s += weight(x, m);
-      }
-      // thread -> warp -> CTA -> cluster: each part against its own maximum,
-      // joined against the common one
-      const float wm = warp_max(m);
-      const uint64_t wsum = warp_add64(__float2ull_rn(m == -INFINITY ? 0.f : s * weight(m, wm) * sum_unit));
-      if (lane == 0) {
-        sh.part_a[r_mine][w_mine] = __float_as_uint(wm);
-        sh.part_b[r_mine][w_mine] = wsum;
-      }
+        // thread -> warp -> CTA -> cluster: each part against its own maximum,
+        // joined against the common one
+        const float wm = warp_max(m);
+        const uint64_t wsum = warp_add64(__float2ull_rn(m == -INFINITY ? 0.f : s * weight(m, wm) * sum_unit));
+        if (lane == 0) {
+          sh.part_a[r_mine][w_mine] = __float_as_uint(wm);
+          sh.part_b[r_mine][w_mine] = wsum;
+        }
       }
     }
     __syncthreads();
@@ -508,7 +538,10 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         send(warp, __float_as_uint(m), f);
       }
     }
-    cluster_sync();
+    if (!agree(kStats | ((uint32_t)v & 0xffffffu) << 4 | (uint32_t)n)) {
+      give_up(true);
+      return;
+    }
 
     // ---- each row's warp tries its children in index order.  The row's warp
     // of every CTA comes to the same decisions: the same numbers, read and
@@ -654,7 +687,10 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         __syncthreads();
         phase ^= 1;
         if (warp == 0) send(0, warp_add64(lane < kWarps ? sh.part_a[0][lane] : 0), 0);
-        cluster_sync();
+        if (!agree(kResidual | ((uint32_t)at & 0xffffffu) << 4 | (uint32_t)r)) {
+          give_up(true);
+          return;
+        }
         if (warp == r) {
           f = 0;
           for (int j = 0; j < C; ++j) f += sh.ex_a[phase][0][j];
@@ -694,9 +730,14 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     // all of its slice asked for at once: the loads below run behind it
     if (QT && tid == 0 && !last.dead && !greedy)
       prefetch_l2(static_cast<const uint8_t*>(q_row) + (size_t)c0 * QES, (int64_t)(c1 - c0) * QES);
-    if (!last.dead && greedy) {
-      bonus = last.am;
-    } else if (!last.dead) {
+    if (last.dead || greedy) {
+      phase ^= 1;
+      if (!agree(kEnd | ((uint32_t)at & 0xffffffu) << 4)) {
+        give_up(true);
+        return;
+      }
+      if (!last.dead) bonus = last.am;
+    } else {
       const float rm = last.m, as = last.as;
       const int n_child = QT ? 0 : last.n_child;
       bool plain = n_child == 0 && !QT;   // draw from p_v itself: nothing rejected, or nothing left of the residual
@@ -759,7 +800,10 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         __syncthreads();
         phase ^= 1;
         if (warp == 0) send(0, warp_max64(lane < kWarps ? sh.part_a[0][lane] : 0), 0);
-        cluster_sync();
+        if (!agree(kBonus | ((uint32_t)at & 0xffffffu) << 4 | (plain ? 1u : 0u))) {
+          give_up(true);
+          return;
+        }
         key = 0;
         for (int j = 0; j < C; ++j) key = max64(key, sh.ex_a[phase][0][j]);
         if (key != 0) {

@@ -30,13 +30,19 @@ constexpr int kBatch = 4;   // rows in flight per thread
 
 __global__ void __launch_bounds__(256, kCtas) paged_kv_compact_kernel(const CompactParams p) {
   __shared__ long long src_row[kRows], dst_row[kRows];  // cache row (of head 0), or -1: nothing to do
+  __shared__ int geo[6];
   const int b = blockIdx.y, tid = threadIdx.x;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int o = p.qo_indptr[b], L = p.qo_indptr[b + 1] - o;
-  const int pg0 = p.kv_indptr[b], npg = p.kv_indptr[b + 1] - pg0;
-  const int lpl = npg > 0 ? p.last_page_len[b] : 1;
-  const int n = p.accept_len[b];
+  // (read once for the CTA: the barriers below go by them)
+  if (tid < 6) {
+    const int32_t* const src[6] = {p.qo_indptr + b, p.qo_indptr + b + 1, p.kv_indptr + b, p.kv_indptr + b + 1,
+                                   p.last_page_len + b, p.accept_len + b};
+    geo[tid] = *src[tid];
+  }
+  __syncthreads();
+  const int o = geo[0], L = geo[1] - o, pg0 = geo[2], npg = geo[3] - pg0;
+  const int lpl = npg > 0 ? geo[4] : 1, n = geo[5];
   const long long kv_len = npg > 0 ? (long long)(npg - 1) * p.page_size + lpl : 0;
   const long long pre = kv_len - L;
   const bool table_ok = o >= 0 && L >= 0 && (long long)o + L <= p.total_qo && npg >= 0 && pg0 >= 0 && lpl >= 1 &&
