@@ -433,8 +433,12 @@ int verify_attn_shared_groups(const int32_t* kv_indptr_h, const int32_t* kv_indi
                               const int32_t* qo_indptr_h, const int32_t* last_page_len_h, int batch,
                               int page_size, int min_pages, int32_t* group_indptr_h,
                               int32_t* shared_pages_h, int* num_groups) {
-  return shared_groups(kv_indptr_h, kv_indices_h, qo_indptr_h, last_page_len_h, batch, page_size, min_pages,
-                       group_indptr_h, shared_pages_h, num_groups);
+  try {
+    return shared_groups(kv_indptr_h, kv_indices_h, qo_indptr_h, last_page_len_h, batch, page_size, min_pages,
+                         group_indptr_h, shared_pages_h, num_groups);
+  } catch (...) {   // no host memory for the lists
+    return VA_ERR_UNSUPPORTED;
+  }
 }
 
 int verify_attn_plan_shared_bounds(int batch, int num_groups, int64_t total_qo, int num_qo_heads,
@@ -460,9 +464,13 @@ int verify_attn_plan_shared_host(const int32_t* kv_indptr_h, const int32_t* qo_i
     int rc = query_sms(&num_sms);
     if (rc) return rc;
   }
-  return plan_shared_host(kv_indptr_h, qo_indptr_h, last_page_len_h, mask_indptr_h, batch, group_indptr_h,
-                          shared_pages_h, num_groups, num_qo_heads, num_kv_heads, head_dim, page_size, q_dtype,
-                          kv_dtype, has_mask, num_sms, options, plan_h, plan_bytes, workspace_bytes);
+  try {
+    return plan_shared_host(kv_indptr_h, qo_indptr_h, last_page_len_h, mask_indptr_h, batch, group_indptr_h,
+                            shared_pages_h, num_groups, num_qo_heads, num_kv_heads, head_dim, page_size, q_dtype,
+                            kv_dtype, has_mask, num_sms, options, plan_h, plan_bytes, workspace_bytes);
+  } catch (...) {   // no host memory for the work list
+    return VA_ERR_UNSUPPORTED;
+  }
 }
 
 int verify_attn_plan_upload(const void* plan_h, void* workspace_d, size_t workspace_bytes,
