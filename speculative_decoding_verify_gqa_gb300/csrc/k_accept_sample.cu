@@ -44,6 +44,8 @@ constexpr int kMaxCluster = 8;
 constexpr int kRows = 8;        // rows of a pass at most
 constexpr int kChildList = 64;  // children's tokens kept in shared memory (further ones are searched)
 constexpr int kMarks = 32;
+constexpr int kVectors = 8;     // 16-byte loads of a thread in flight
+static_assert(kWarps == 2 * kRows, "a warp that decides and one that prefetches for each row");
 constexpr int kNodes = 128;     // a tree of at most so many nodes is kept in shared memory
 
 __device__ __forceinline__ uint64_t race_key(float v, uint32_t idx) {  // v >= 0
@@ -96,12 +98,22 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// An element as it lies in memory, and its value: apart, since whatever is
+// done to a loaded word waits for it.
+template <bool BF16>
+__device__ __forceinline__ uint32_t load_bits(const void* row, int64_t i) {
+  if constexpr (BF16)
+    return __ldg(static_cast<const uint16_t*>(row) + i);
+  else
+    return __ldg(static_cast<const uint32_t*>(row) + i);
+}
+template <bool BF16>
+__device__ __forceinline__ float bits_value(uint32_t w) {
+  return __uint_as_float(BF16 ? w << 16 : w);
+}
 template <bool BF16>
 __device__ __forceinline__ float load_elem(const void* row, int64_t i) {
-  if constexpr (BF16)
-    return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(row) + i) << 16);
-  else
-    return __ldg(static_cast<const float*>(row) + i);
+  return bits_value<BF16>(load_bits<BF16>(row, i));
 }
 
 // Eight consecutive elements from element i (16-byte aligned there).
@@ -125,11 +137,10 @@ __device__ __forceinline__ void load8(const void* row, int64_t i, float* x) {
 
 // What is known of one row of a pass.
 struct RowState {
-  double sum;               // of its weights 2^((x - m) log2(e) / T)
-  float m, inv, as;         // maximum; 1 / sum; A after the children tried so far, times the sum
+  uint64_t sum;             // of its weights 2^((x - m) log2(e) / T), in units of 2^(2 - sum_bits)
+  float m, sf, as;          // maximum; the sum in fp32; A after the children tried so far, times the sum
   float x;                  // logit of the accepted child's token
   int am, dead;             // first argmax (T = 0); nothing of the row is possible
-  int next, more;           // the accepted child, or -1; a residual's sum is wanted first
   int n_child;
   int kid[32];              // the children now in the lanes of the row's warp
   uint32_t marks[kMarks];   // bit (x >> 3) mod 32 kMarks for every child's token x
@@ -141,37 +152,62 @@ struct Shared {
   uint32_t ex_tag[2][kMaxCluster];                                    // where each CTA's walk stands
   int o, L;                                                           // the request's first row, its nodes
   RowState row[kRows];
+  int node[kRows], next[kRows], more[kRows];   // each row's node; the accepted child, or -1; a residual's sum is wanted first
   int par[kNodes], tok[kNodes], first[kNodes], kids[kNodes];  // parents, tokens, first children, their number
   float u[kNodes];
   float lx[kNodes], lm[kNodes];                 // emitted tokens' logits and their rows' maxima and sums
-  double lsum[kNodes];
-  // read again where fp64 needs them: kept in registers, their conversions
-  // would be hoisted and done by every thread, on a pipe of two lanes a cycle
-  volatile float c_hi, c_lo, temp;   // (temp: the request's temperature)
+  uint64_t lsum[kNodes];
+  float c_hi, c_lo;
+  // the request's temperature, read again where fp64 needs it: kept in a
+  // register, its conversion would be hoisted and done by every thread, on a
+  // pipe of two lanes a cycle
+  volatile float temp;
 };
 
 // Sums of weights and residuals cross threads as fixed-point integers: adding
 // them is exact, takes the integer pipe (fp64 adds run at a 64th of its rate
-// here) and needs no order.
+// here) and needs no order.  A warp reduces with redux, whose 32-bit words a
+// 64-bit sum is cut into: 27 bits of 32 lanes stay below 2^32.  (A step of a
+// walk is a dozen short dependent pieces of one warp; with five rounds of
+// shuffles for each of its reductions a chain of 4 drafts took 1.5 us longer.)
 __device__ __forceinline__ uint64_t warp_add64(uint64_t v) {
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-  return v;
+  constexpr uint32_t kLimb = (1u << 27) - 1;
+  const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)v & kLimb),
+                 b = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 27) & kLimb),
+                 c = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 54));
+  return (uint64_t)a + ((uint64_t)b << 27) + ((uint64_t)c << 54);
 }
 __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) v = max64(v, __shfl_xor_sync(0xffffffffu, v, k));
-  return v;
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return (uint64_t)hi << 32 | lo;
 }
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, k));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // a * w for a weight w in [0, 1], in half of a's units (the product's upper bits).
 __device__ __forceinline__ uint64_t scale64(uint64_t a, float w) {
-  return __umul64hi(a, __float2ull_rn(w * 4294967296.f) << 31);
+  return __umul64hi(a, (uint64_t)__float2uint_rn(w * 2147483648.f) << 32);
+}
+
+// (x - m) c - log2(sum), times ln 2, in fp32 pairs (fp64 took 1.2 us of a
+// request's end): c = c_hi + c_lo is log2(e) / T and the sum is f 2^unit.
+__device__ __forceinline__ float log_prob(float x, float m, float c_hi, float c_lo, uint64_t f, int unit) {
+  const float s = __ull2float_rn(f);   // within 2^-24, as its terms are
+  const int e = (__float_as_int(s) >> 23) - 127;
+  const float l = log2f(__int_as_float((__float_as_int(s) & 0x7fffff) | 0x3f800000));
+  const float d = x - m, dv = d - x, d_lo = (x - (d - dv)) - (m + dv);   // x - m = d + d_lo
+  const float y = d * c_hi;
+  if (!(y > -3e38f)) return -INFINITY;
+  const float y_lo = fmaf(d, c_hi, -y) + fmaf(d, c_lo, d_lo * c_hi);
+  const float n = (float)-(e + unit);
+  const float t = y + n, tv = t - y, t_lo = (y - (t - tv)) + (n - tv) + y_lo - l;   // log2 p = t + t_lo
+  const float r = t * 0.693147182464599609f;
+  // ln 2 less its rounding to fp32: -1.9046543e-9
+  return r + (fmaf(t, 0.693147182464599609f, -r) + fmaf(t, -1.9046543e-9f, t_lo * 0.693147182464599609f));
 }
 
 // LB: logits bf16 (else fp32).  QT: draft distributions: 0 none, 1 bf16, 2 fp32.
@@ -222,34 +258,43 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   auto prefetch_noise = [&]() {
     if (!greedy) prefetch_l2(noise + c0, (int64_t)(c1 - c0) * 4);
   };
-  if (tid == 0 && table_ok && L > 0) {
+  // (by warps that have nothing of the tables to read)
+  if (tid == kThreads - 32 && table_ok && L > 0) {
     prefetch_row(0);
     if (noise_first) prefetch_noise();
   }
-  // log2(e) / T as a float pair: a rounded factor alone would tilt the whole
-  // distribution by |logit difference| * 2^-25.  Rounded down, so that both
-  // parts are positive and a logit of -inf stays -inf (log2(e) itself is
-  // 1.4426950216 + 1.926e-8).
-  const float c_hi = greedy ? 1.f : __fdiv_rd(1.4426950216293335f, temp);
-  const float c_lo =
-      greedy ? 1.f
-             : fminf(fmaxf((fmaf(-c_hi, temp, 1.4426950216293335f) + 1.925963033500e-8f) / temp, 1e-45f), 3e38f);
-  if (tid == 0) {
-    sh.c_hi = c_hi;
-    sh.c_lo = c_lo;
+  if (warp == kWarps - 2) {
+    // log2(e) / T as a float pair: a rounded factor alone would tilt the whole
+    // distribution by |logit difference| * 2^-25.  Rounded down, so that both
+    // parts are positive and a logit of -inf stays -inf (log2(e) itself is
+    // 1.4426950216 + 1.926e-8).
+    const float hi = greedy ? 1.f : __fdiv_rd(1.4426950216293335f, temp);
+    const float lo =
+        greedy ? 1.f
+               : fminf(fmaxf((fmaf(-hi, temp, 1.4426950216293335f) + 1.925963033500e-8f) / temp, 1e-45f), 3e38f);
+    if (lane == 0) {
+      sh.c_hi = hi;
+      sh.c_lo = lo;
+    }
   }
   int bad = 0;
   if (table_ok)
     for (int i = tid; i < L; i += kThreads) {
       const int par = p.parents[o + i];
-      bad |= i == 0 ? par >= 0 : (par < 0 || par >= i);
+      const bool wrong = i == 0 ? par >= 0 : (par < 0 || par >= i);
+      bad |= wrong;
       if (L <= kNodes) {
         sh.par[i] = par;
         sh.tok[i] = p.tokens[o + i];
         sh.u[i] = p.uniforms[o + i];
+        if (i > 0 && !wrong) {
+          atomicMin(&sh.first[par], i);
+          atomicAdd(&sh.kids[par], 1);
+        }
       }
     }
   bad = __syncthreads_or(bad) || !table_ok || !(temp >= 0.f && temp < INFINITY);
+  const float c_hi = sh.c_hi, c_lo = sh.c_lo;
   cluster_wait();
 
   // The exchange: lane k of a warp that has a row's words sends them to CTA k,
@@ -295,11 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     give_up(bad || !same);
     return;
   }
-  if (L <= kNodes && tid > 0 && tid < L) {
-    atomicMin(&sh.first[sh.par[tid]], tid);
-    atomicAdd(&sh.kids[sh.par[tid]], 1);
-  }
-  __syncthreads();
   const uint64_t ch2 = f32x2(c_hi, c_hi), cl2 = f32x2(c_lo, c_lo);
   // 2^((x - m) log2(e) / T) of a pair: the difference first (exact for bf16
   // logits of like size), then the two-term product
@@ -320,15 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   // weights of at most 1 in units of 2^-sum_bits: V of them stay below 2^63
   const int sum_bits = V <= (1 << 22) ? 40 : 31;
   const float sum_unit = __int_as_float((127 + sum_bits) << 23);
-
-  // (x - m) / T - ln(sum): the logarithm of the sum's fraction in fp32, the
-  // rest in fp64, a handful of operations
-  auto log_p = [&](float x, float rm, double t) -> float {
-    const int e = (int)(__double_as_longlong(t) >> 52) - 1023;
-    const float f = (float)(t * __longlong_as_double((long long)(1023 - e) << 52));
-    const double d = ((double)x - (double)rm) * ((double)sh.c_hi + (double)sh.c_lo) - (double)e;
-    return (float)(d * 0.6931471805599453 - (double)logf(f));
-  };
+  // a row's joined sum (two joins halved the unit twice)
+  auto sum_value = [&](uint64_t f) { return (double)f * __longlong_as_double((long long)(1025 - sum_bits) << 52); };
 
   int v = 0, k = 0;
   if (tid == 0 && rank == 0) p.path[o] = 0;
@@ -340,18 +373,28 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     // The host asks for eight rows where the batch leaves SMs idle, else for
     // four: 64 ragged chains took 47.8 us with four and 52.1 with eight, whose
     // rows past the accepted ones are read from HBM for nothing.
-    int n = 1, mine = warp == 0 ? v : -1;   // rows; the node that this warp decides about
+    int n = 1, mine = (warp & (kRows - 1)) == 0 ? v : -1;   // rows; the node that this warp decides about
+    int n_kids = L;                                         // how many children it has at most
     if (L <= kNodes) {
       bool alone = true;
-      for (int at = v; n < p.rows; ++n) {
-        const int kids = sh.kids[at];
+      int kids = sh.kids[v], at = sh.first[v];
+      if (mine == v) n_kids = kids;
+      for (; n < p.rows; ++n) {
         alone = alone && kids == 1;
         if (kids == 0 || (n > 1 && !alone)) break;
+        if ((warp & (kRows - 1)) == n) mine = at;
+        kids = sh.kids[at];
         at = sh.first[at];
-        if (warp == n) mine = at;
+        if ((warp & (kRows - 1)) == n) n_kids = kids;
       }
     }
-    if (mine >= 0 && lane == 0) prefetch_row(mine);
+    const int row_warps = kWarps / (n > 4 ? 8 : n > 2 ? 4 : n);   // warps of a row in the pass over them
+    // slices that take more than one round of loads are asked for in one go,
+    // by the warps that decide about no row
+    if (warp >= kRows) {
+      if (mine > 0 && lane == 0 && (int64_t)(c1 - c0) * LES > row_warps * 32 * 16 * kVectors) prefetch_row(mine);
+      mine = -1;
+    }
 
     // ---- its children, up to 32 at a time, one a lane: what they need is
     // asked for before the pass over the rows, so it arrives meanwhile
@@ -361,9 +404,17 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     int scan = mine + 1;   // the next node to look at
     uint32_t win = 0;      // lanes whose child has not been tried
     int kid = -1, ctok = -1;
-    float cx = -INFINITY, cq = 0.f, cu = 0.f;   // token's logit and draft probability, the child's number
+    uint32_t cxb = 0, cqb = 0;                  // token's logit and draft probability as loaded,
+    bool has = false;                           // if it is a token and nothing of it was rejected,
+    float cx = -INFINITY, cq = 0.f, cu = 0.f;   // and as numbers; the child's number
     auto load_children = [&]() {
       int cnt = 0;
+      if (n_kids == 1 && scan == mine + 1 && L <= kNodes) {   // a chain's only child
+        if (lane == 0) rs.kid[0] = sh.first[mine];
+        cnt = 1;
+        scan = L;
+      }
+      if (n_kids == 0) scan = L;
       while (scan < L && cnt < 32) {
         const int i = scan + lane;
         const bool is = i < L && par[i] == mine;
@@ -377,17 +428,15 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
       __syncwarp();
       win = cnt < 32 ? (1u << cnt) - 1u : 0xffffffffu;
       kid = ctok = -1;
-      cx = -INFINITY;
-      cq = cu = 0.f;
+      cu = 0.f;
       if (lane < cnt) {
         kid = rs.kid[lane];
         ctok = tok[kid];
         cu = uni[kid];
-        if (ctok >= 0 && ctok < V) {
-          cx = load_elem<LB>(row, ctok);
-          if (QT) cq = load_elem<QT == 1>(qrow, ctok);
-        }
       }
+      has = ctok >= 0 && ctok < V;
+      cxb = load_bits<LB>(row, has ? ctok : 0);   // (not waited for here: see child_values)
+      if (QT) cqb = load_bits<QT == 1>(qrow, has ? ctok : 0);
       if (!QT && cnt > 0) {
         // q one-hot: an earlier sibling's equal token was rejected before
         // this one, so nothing of it is left
@@ -396,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         for (int j = 0; j < min(n0, kChildList); ++j) dup |= rs.child_tok[j] == ctok;
         if (n0 > kChildList)
           for (int j = mine + 1; j < kid; ++j) dup |= par[j] == mine && tok[j] == ctok;
-        if (dup) cx = -INFINITY;
+        if (dup) has = false;
         if (lane < cnt) {
           if (at < kChildList) rs.child_tok[at] = ctok;
           atomicOr(&rs.marks[(ctok >> 8) & (kMarks - 1)], 1u << ((ctok >> 3) & 31));
@@ -405,6 +454,10 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         if (lane == 0) rs.n_child = n0 + cnt;
       }
       __syncwarp();
+    };
+    auto child_values = [&]() {
+      cx = has ? bits_value<LB>(cxb) : -INFINITY;
+      cq = QT && has ? bits_value<QT == 1>(cqb) : 0.f;
     };
     if (mine >= 0) {
       rs.marks[lane] = 0;
@@ -416,7 +469,6 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     // ---- each row's maximum and sum over the slice (T = 0: its first argmax).
     // The warps are shared out among the rows, so that every row's loads are in
     // flight at once and each warp reduces once.
-    const int row_warps = kWarps / (n > 4 ? 8 : n > 2 ? 4 : n);
     const int r_mine = warp / row_warps, w_mine = warp - r_mine * row_warps;
     if (r_mine < n) {
       int i_row = v;
@@ -431,74 +483,86 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
       const uint4* vp = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x_row) + (size_t)v0 * LES);
       const int n_end = head + (c1 - v1);
       auto end_at = [&](int i) { return i < head ? c0 + i : v1 + (i - head); };
-      if (greedy) {
-        uint64_t best = 0;
-        for (int i = t0; i < n_end; i += step)
-          best = max64(best, logit_key(load_elem<LB>(x_row, end_at(i)), (uint32_t)end_at(i)));
-#pragma unroll 4
-        for (int i = t0; i < nvec; i += step) {
-          const uint4 w = __ldg(vp + i);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-          const uint32_t e = (uint32_t)(v0 + i * EPV);
+      // running maximum and sum, eight vectors at a time (T = 0: the maximum
+      // and the eight vectors it was first met in)
+      float m = -INFINITY, s = 0.f;
+      int i_max = 0;
+      constexpr int NV = kVectors;
+      for (int i0 = t0; i0 < nvec; i0 += NV * step) {
+        uint4 w[NV];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (LB) {
-              best = max64(best, logit_key(__uint_as_float(u[q] << 16), e + 2 * q));
-              best = max64(best, logit_key(__uint_as_float(u[q] & 0xffff0000u), e + 2 * q + 1));
-            } else {
-              best = max64(best, logit_key(__uint_as_float(u[q]), e + q));
+        for (int j = 0; j < NV; ++j) {
+          const int i = i0 + j * step;
+          const uint32_t ninf = LB ? 0xff80ff80u : 0xff800000u;
+          w[j] = i < nvec ? __ldg(vp + i) : make_uint4(ninf, ninf, ninf, ninf);
+        }
+        float mx;
+        if constexpr (LB) {   // the maximum in bf16 pairs
+          uint32_t v2 = w[0].x;
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+            v2 = max_bf16x2(max_bf16x2(v2, w[j].x), max_bf16x2(w[j].y, max_bf16x2(w[j].z, w[j].w)));
+          mx = fmaxf(__uint_as_float(v2 << 16), __uint_as_float(v2 & 0xffff0000u));
+        } else {
+          mx = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+            mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(w[j].x), __uint_as_float(w[j].y))),
+                       fmaxf(__uint_as_float(w[j].z), __uint_as_float(w[j].w)));
+        }
+        if (mx > m) {
+          s = m == -INFINITY ? 0.f : s * weight(m, mx);
+          m = mx;
+          i_max = i0;
+        }
+        if (greedy || m == -INFINITY) continue;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (i0 + j * step >= nvec) break;
+          const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+          for (int q = 0; q < (LB ? 4 : 2); ++q) {
+            float w0, w1;
+            if (LB) weight2(__uint_as_float(u[q] << 16), __uint_as_float(u[q] & 0xffff0000u), m, &w0, &w1);
+            else weight2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]), m, &w0, &w1);
+            s0 += w0;
+            s1 += w1;
+          }
+        }
+        s += s0 + s1;
+      }
+      if (greedy) {
+        // the lanes that hold the warp's maximum look it up where they met it
+        // (10.3 us of a 4-row pass over 128,256 tokens came down to 5.5
+        // against a key of value and index kept for every entry)
+        uint64_t best = 0;
+        for (int i = t0; i < n_end; i += step) {
+          const float x = load_elem<LB>(x_row, end_at(i));
+          if (x >= -INFINITY) best = max64(best, logit_key(x + 0.f, (uint32_t)end_at(i)));
+        }
+        const float wm = warp_max(m);
+        if (m > -INFINITY && m == wm) {
+          int at_max = -1;
+#pragma unroll
+          for (int j = NV - 1; j >= 0; --j) {
+            const int i = i_max + j * step;
+            if (i >= nvec) continue;
+            const uint4 w = __ldg(vp + i);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int q = EPV - 1; q >= 0; --q) {
+              const float x = !LB     ? __uint_as_float(u[q % 4])
+                              : q & 1 ? __uint_as_float(u[q / 2] & 0xffff0000u)
+                                      : __uint_as_float(u[q / 2] << 16);
+              if (x == m) at_max = v0 + i * EPV + q;
             }
           }
+          if (at_max >= 0) best = max64(best, logit_key(m + 0.f, (uint32_t)at_max));
         }
         best = warp_max64(best);
         if (lane == 0) sh.part_a[r_mine][w_mine] = best;
       } else {
-        // running maximum and sum, eight vectors at a time
-        float m = -INFINITY, s = 0.f;
-        constexpr int NV = 8;
-        for (int i0 = t0; i0 < nvec; i0 += NV * step) {
-          uint4 w[NV];
-  #pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            const int i = i0 + j * step;
-            const uint32_t ninf = LB ? 0xff80ff80u : 0xff800000u;
-            w[j] = i < nvec ? __ldg(vp + i) : make_uint4(ninf, ninf, ninf, ninf);
-          }
-          float mx;
-          if constexpr (LB) {   // the maximum in bf16 pairs
-            uint32_t v2 = w[0].x;
-  #pragma unroll
-            for (int j = 0; j < NV; ++j)
-              v2 = max_bf16x2(max_bf16x2(v2, w[j].x), max_bf16x2(w[j].y, max_bf16x2(w[j].z, w[j].w)));
-            mx = fmaxf(__uint_as_float(v2 << 16), __uint_as_float(v2 & 0xffff0000u));
-          } else {
-            mx = -INFINITY;
-  #pragma unroll
-            for (int j = 0; j < NV; ++j)
-              mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(w[j].x), __uint_as_float(w[j].y))),
-                         fmaxf(__uint_as_float(w[j].z), __uint_as_float(w[j].w)));
-          }
-          if (mx > m) {
-            s = m == -INFINITY ? 0.f : s * weight(m, mx);
-            m = mx;
-          }
-          if (m == -INFINITY) continue;
-          float s0 = 0.f, s1 = 0.f;
-  #pragma unroll
-          for (int j = 0; j < NV; ++j) {
-            if (i0 + j * step >= nvec) break;
-            const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-  #pragma unroll
-            for (int q = 0; q < (LB ? 4 : 2); ++q) {
-              float w0, w1;
-              if (LB) weight2(__uint_as_float(u[q] << 16), __uint_as_float(u[q] & 0xffff0000u), m, &w0, &w1);
-              else weight2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]), m, &w0, &w1);
-              s0 += w0;
-              s1 += w1;
-            }
-          }
-          s += s0 + s1;
-        }
         for (int i = t0; i < n_end; i += step) {
           const float x = load_elem<LB>(x_row, end_at(i));
           if (x > m) {
@@ -528,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
       return warp_add64(pm > -INFINITY ? scale64(pb[lane], weight(pm, jm)) : 0);
     };
     float m = -INFINITY;
-    double sum = 0.0;
+    uint64_t f_sum = 0;
     int am = -1;
     if (mine >= 0) {
       if (greedy) {
@@ -549,10 +613,12 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     bool dead = false, pending = false;   // pending (QT): a child was rejected and its B not yet summed
     float cw = 0.f, sf = 0.f;             // weight of the child's token: sum times its probability
     double A = 0.0, B = 1.0;
+    float Af = 0.f, Bf = 1.f;             // (their fp32 values: conversions take the fp64 pipe)
     auto child_w = [&]() { return greedy ? (ctok == am && cx > -INFINITY ? 1.f : 0.f) : weight(cx, m); };
     // u q B < p - A q, times the sum, in fp64: where fp32 is too close to tell
     auto precisely = [&](float x, float q, float u, double b) {
       const double w = exp(((double)x - (double)m) / (double)sh.temp);
+      const double sum = sum_value(f_sum);
       return (double)u * b * (double)q * sum < w - (QT ? A * (double)q * sum : 0.0);
     };
     auto decide = [&]() {
@@ -562,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         if (win == 0) {
           load_children();
           if (win == 0) break;
+          child_values();
           cw = child_w();
         }
         if (pending) {
@@ -578,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
           }
           const float all = __shfl_sync(0xffffffffu, before, 31);
           before -= cw;
-          const float lhs = greedy ? 0.f : cu * ((float)B * sf - before);
+          const float lhs = greedy ? 0.f : cu * (Bf * sf - before);
           const bool near = !greedy && fabsf(cw - lhs) <= 4e-6f * (cw + sf) && cx > -INFINITY;
           const bool ok = greedy ? cw > 0.f : lhs < cw;
           uint32_t may = __ballot_sync(0xffffffffu, (ok || near) && ((win >> lane) & 1u));
@@ -589,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
             bool yes = true;
             if ((close >> j) & 1u) {
               double b = B;
-              for (int i = 0; i < j; ++i) b -= (double)__shfl_sync(0xffffffffu, cw, i) / sum;
+              for (int i = 0; i < j; ++i) b -= (double)__shfl_sync(0xffffffffu, cw, i) / sum_value(f_sum);
               yes = precisely(xj, 1.f, uj, b);
             }
             if (yes) {
@@ -601,7 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
           }
           win = 0;
           if (next >= 0) break;
-          if (!greedy) B -= (double)(all / sf);
+          if (!greedy && scan < L) {
+            B -= (double)(all / sf);
+            Bf = (float)B;
+          }
         } else {
           const int j = __ffs(win) - 1;
           win &= win - 1;
@@ -611,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
           if (greedy) {
             ok = wj > 0.f;
           } else {
-            const float lhs = uj * (float)B * qj * sf, aq = (float)A * qj * sf;
+            const float lhs = uj * Bf * qj * sf, aq = Af * qj * sf;
             ok = lhs < wj - aq;
             if (fabsf(wj - aq - lhs) <= 4e-6f * (wj + aq + lhs) && xj > -INFINITY) ok = precisely(xj, qj, uj, B);
           }
@@ -622,33 +692,35 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
           }
           if (greedy) continue;
           A += B;
+          Af = (float)A;
           pending = true;
         }
       }
       pending = false;
       if (lane == 0) {
-        rs.next = next;
-        rs.more = more;
-        rs.as = (float)A * sf;
+        sh.next[warp] = next;
+        sh.more[warp] = more;
+        rs.as = Af * sf;
         rs.x = nx;
       }
     };
     if (mine >= 0) {
       if (greedy) {
-        am = (int)(0xffffffffu - (uint32_t)warp_max64(lane < C ? sh.ex_a[phase][warp][lane] : 0));
-        dead = !(load_elem<LB>(row, am) > -INFINITY);
+        const uint64_t key = warp_max64(lane < C ? sh.ex_a[phase][warp][lane] : 0);
+        dead = key <= logit_key(-INFINITY, 0);
+        am = dead ? 0 : (int)(0xffffffffu - (uint32_t)key);
       } else {
-        const uint64_t f = join(sh.ex_a[phase][warp], sh.ex_b[phase][warp], C, &m);
-        dead = f == 0;
-        // (two joins halved the unit twice)
-        sum = (double)f * __longlong_as_double((long long)(1025 - sum_bits) << 52);
-        sf = (float)sum;
+        f_sum = join(sh.ex_a[phase][warp], sh.ex_b[phase][warp], C, &m);
+        dead = f_sum == 0;
+        sf = __ull2float_rn(f_sum) * __int_as_float((129 - sum_bits) << 23);
       }
+      child_values();
       if (!dead) cw = child_w();
       if (lane == 0) {
+        sh.node[warp] = mine;
         rs.m = m;
-        rs.sum = sum;
-        rs.inv = 1.f / sf;
+        rs.sum = f_sum;
+        rs.sf = sf;
         rs.am = am;
         rs.dead = dead;
       }
@@ -656,69 +728,76 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     }
     __syncthreads();
 
-    // ---- follow the decisions along the rows of the pass
-    int r = 0, at = v, to;
-    for (;;) {
-      while (QT && sh.row[r].more) {
-        // B = sum_x (p(x) - A q(x))+ of this row, in units of 2^-50
-        const void *x_row = row_of(at), *q_row = qrow_of(at);
-        const float rm = sh.row[r].m, inv = sh.row[r].inv, as = sh.row[r].as;
-        float t = 0.f;
-        if (p.vec) {
-#pragma unroll 2
-          for (int i = c0 + 8 * tid; i < c1; i += 8 * kThreads) {
-            float x[8], q[8];
-            load8<LB>(x_row, i, x);
-            load8<QT == 1>(q_row, i, q);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              float w0, w1;
-              weight2(x[e], x[e + 1], rm, &w0, &w1);
-              t += fmaxf(fmaf(-as, q[e], w0), 0.f) + fmaxf(fmaf(-as, q[e + 1], w1), 0.f);
-            }
-          }
-        } else {
-#pragma unroll 4
-          for (int i = c0 + tid; i < c1; i += kThreads)
-            t += fmaxf(fmaf(-as, load_elem<QT == 1>(q_row, i), weight(load_elem<LB>(x_row, i), rm)), 0.f);
-        }
-        uint64_t f = warp_add64(__float2ull_rn(t * inv * 0x1p50f));
-        if (lane == 0) sh.part_a[0][warp] = f;
-        __syncthreads();
-        phase ^= 1;
-        if (warp == 0) send(0, warp_add64(lane < kWarps ? sh.part_a[0][lane] : 0), 0);
-        if (!agree(kResidual | ((uint32_t)at & 0xffffffu) << 4 | (uint32_t)r)) {
-          give_up(true);
-          return;
-        }
-        if (warp == r) {
-          f = 0;
-          for (int j = 0; j < C; ++j) f += sh.ex_a[phase][0][j];
-          B = (double)f * 0x1p-50;
-          decide();
-        }
-        __syncthreads();
-      }
-      to = sh.row[r].next;
-      if (to < 0) break;
-      if (tid == 0 && rank == 0) {
-        p.path[o + k + 1] = to;
-        if (k < kNodes) {
-          sh.lx[k] = sh.row[r].x;
-          sh.lm[k] = sh.row[r].m;
-          sh.lsum[k] = sh.row[r].sum;
+    // ---- follow the decisions along the rows of the pass: a row whose accepted
+    // child is the next row's node leads on to it, and all such are taken at once
+    auto emit = [&](int r0, int count) {   // rows r0 .. accept their children: nodes k + 1 ..
+      if (rank == 0 && tid < count) {
+        const RowState& e = sh.row[r0 + tid];
+        const int i = k + tid;
+        p.path[o + i + 1] = sh.next[r0 + tid];
+        if (i < kNodes) {
+          sh.lx[i] = e.x;
+          sh.lm[i] = e.m;
+          sh.lsum[i] = e.sum;
         } else if (p.logprobs) {
-          p.logprobs[o + k] = greedy ? 0.f : log_p(sh.row[r].x, sh.row[r].m, sh.row[r].sum);
+          p.logprobs[o + i] = greedy ? 0.f : log_prob(e.x, e.m, c_hi, c_lo, e.sum, 2 - sum_bits);
         }
       }
-      ++k;
-      // the pass's next row is the first child's
-      const bool ahead = r + 1 < n && to == sh.first[at];
-      at = to;
-      if (!ahead) break;
-      ++r;
+      k += count;
+    };
+    int r = 0, at, to;
+    for (;;) {
+      const int slot = lane & (kRows - 1);
+      const int r_node = sh.node[slot], r_next = sh.next[slot], r_more = QT ? sh.more[slot] : 0;
+      const int after = __shfl_down_sync(0xffffffffu, r_node, 1);
+      const uint32_t leads = __ballot_sync(0xffffffffu, lane + 1 < n && !r_more && r_next == after);
+      const int run = __ffs(~(leads >> r)) - 1;
+      if (run) emit(r, run);
+      r += run;
+      at = __shfl_sync(0xffffffffu, r_node, r);
+      to = __shfl_sync(0xffffffffu, r_next, r);
+      if (!QT || !__shfl_sync(0xffffffffu, r_more, r)) break;
+      // B = sum_x (p(x) - A q(x))+ of this row, in units of 2^-50
+      const void *x_row = row_of(at), *q_row = qrow_of(at);
+      const float rm = sh.row[r].m, inv = 1.f / sh.row[r].sf, as = sh.row[r].as;
+      float t = 0.f;
+      if (p.vec) {
+#pragma unroll 2
+        for (int i = c0 + 8 * tid; i < c1; i += 8 * kThreads) {
+          float x[8], q[8];
+          load8<LB>(x_row, i, x);
+          load8<QT == 1>(q_row, i, q);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            float w0, w1;
+            weight2(x[e], x[e + 1], rm, &w0, &w1);
+            t += fmaxf(fmaf(-as, q[e], w0), 0.f) + fmaxf(fmaf(-as, q[e + 1], w1), 0.f);
+          }
+        }
+      } else {
+#pragma unroll 4
+        for (int i = c0 + tid; i < c1; i += kThreads)
+          t += fmaxf(fmaf(-as, load_elem<QT == 1>(q_row, i), weight(load_elem<LB>(x_row, i), rm)), 0.f);
+      }
+      uint64_t f = warp_add64(__float2ull_rn(t * inv * 0x1p50f));
+      if (lane == 0) sh.part_a[0][warp] = f;
+      __syncthreads();
+      phase ^= 1;
+      if (warp == 0) send(0, warp_add64(lane < kWarps ? sh.part_a[0][lane] : 0), 0);
+      if (!agree(kResidual | ((uint32_t)at & 0xffffffu) << 4 | (uint32_t)r)) {
+        give_up(true);
+        return;
+      }
+      if (warp == r) {
+        f = warp_add64(lane < C ? sh.ex_a[phase][0][lane] : 0);
+        B = (double)f * 0x1p-50;
+        Bf = (float)B;
+        decide();
+      }
+      __syncthreads();
     }
     if (to >= 0) {
+      emit(r, 1);
       v = to;
       continue;
     }
@@ -804,8 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
           give_up(true);
           return;
         }
-        key = 0;
-        for (int j = 0; j < C; ++j) key = max64(key, sh.ex_a[phase][0][j]);
+        key = warp_max64(lane < C ? sh.ex_a[phase][0][lane] : 0);
         if (key != 0) {
           bonus = (int)(0xffffffffu - (uint32_t)key);
           break;
@@ -823,10 +901,11 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         // every emitted token's, a lane each
         __syncwarp();
         for (int i = lane; i <= k; i += 32) {
-          if (i == k)
-            p.logprobs[o + k] = greedy || bonus < 0 ? 0.f : log_p(load_elem<LB>(x_row, bonus), last.m, last.sum);
-          else if (i < kNodes)
-            p.logprobs[o + i] = greedy ? 0.f : log_p(sh.lx[i], sh.lm[i], sh.lsum[i]);
+          if (i < k && i >= kNodes) continue;   // (written on the way)
+          const bool end = i == k;
+          const float x = !end ? sh.lx[i] : bonus >= 0 ? load_elem<LB>(x_row, bonus) : 0.f;
+          const float lp = greedy ? 0.f : log_prob(x, end ? last.m : sh.lm[i], c_hi, c_lo, end ? last.sum : sh.lsum[i], 2 - sum_bits);
+          p.logprobs[o + i] = end && bonus < 0 ? 0.f : lp;
         }
       }
       for (int i = k + 1 + tid; i < L; i += kThreads) {

@@ -314,6 +314,27 @@ def test_agrees_with_greedy_acceptance_at_temperature_zero(va):
     assert int(g[0].max()) > 2 and am.numel()
 
 
+@pytest.mark.parametrize("V", [1, 7, 1001, 40000])
+@pytest.mark.parametrize("ldt", [H, F], ids=["bf16", "fp32"])
+def test_greedy_bonus_is_the_first_of_equal_maxima(va, ldt, V):
+    """T = 0 on rows with one to several equal maxima, +0 and -0 among them: the first index."""
+    rng = np.random.default_rng(V)
+    B = 24
+    lg = np.full((B, V), -3.0, np.float32)
+    for b in range(B):
+        at = rng.integers(0, V, 1 + b % 5)
+        lg[b, at] = [5.0, -0.0, 0.0][b % 3]
+        if b % 3:
+            lg[b, rng.choice(at)] *= -1
+    x = torch.from_numpy(lg).to(ldt).cuda()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    acc, path, bonus, _ = va.verify_accept_sample(x, i32(range(B + 1)), i32([0] * B), i32([-1] * B),
+                                                  torch.zeros(B, device="cuda"), torch.ones(B, V, device="cuda"),
+                                                  temperature=torch.zeros(B, device="cuda"))
+    assert acc.tolist() == [1] * B and path.tolist() == [0] * B
+    assert bonus.tolist() == lg.argmax(1).tolist()
+
+
 def test_graph_replay_and_side_stream(va):
     """Captured once, replayed over new inputs in the same buffers, on a stream of its own."""
     cs = [_case(s, lens=[5, 5, 5], vocab=4096, kind="chain", qdt=F, temps=[0.9]) for s in (21, 22)]
