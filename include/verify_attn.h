@@ -620,9 +620,10 @@ int verify_accept_greedy(const void* logits, va_dtype logits_dtype, int64_t tota
  * parents, tables or temperature (negative, infinite, NaN) are invalid gives
  * the same, its path -1, and raises VA_DEV_BAD_TABLE in status_d (nullable).
  * Rows may start at any element (16-byte aligned rows of a vocabulary that is
- * a multiple of 8 are read fastest).  Probabilities, sums and residuals are
- * computed in fp32 with sums and decisions in fp64.  Rows of nodes that are
- * not reached are not read.  No workspace.
+ * a multiple of 8 are read fastest).  Weights and residuals are computed in
+ * fp32 and summed in 64-bit fixed point; decisions too close for fp32 are made
+ * in fp64.  Rows of nodes that are not reached are not read.  The outputs may
+ * not overlap the inputs.  No workspace.
  * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED (dtypes, sizes past 32
  * bits), VA_ERR_CUDA.
  */
@@ -649,7 +650,7 @@ int verify_accept_sample(const void* logits, va_dtype logits_dtype, int64_t tota
  *
  * k_cache / v_cache: num_layers caches of the same page table one after the
  * other, each in the layout kv_layout ([num_layers, num_pages, ...],
- * contiguous).  head_dim_v 0 means head_dim.  A row whose page id lies outside
+ * contiguous; the two pools do not overlap).  head_dim_v 0 means head_dim.  A row whose page id lies outside
  * the pool is skipped with VA_DEV_BAD_PAGE.  Requests whose draft slots share
  * a page slot are not supported (their order is not defined).
  * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED, VA_ERR_CUDA.

@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -297,6 +298,9 @@ def _make_options(max_splits=0, min_chunk=0, target_ctas=0, kernel=0, mask_layou
     return o
 
 
+_PLAN_DV = struct.Struct("=q")
+
+
 @dataclass
 class Plan:
     """A plan: the host buffer (numpy) and the device workspace (torch) it was
@@ -327,11 +331,8 @@ class Plan:
                     max_nsplit=int(np.frombuffer(h[176:184].tobytes(), dtype=np.int64)[0]))
 
     def value_width(self) -> int:
-        """Elements of an output row (read from the plan once)."""
-        dv = self.__dict__.get("_dv")
-        if dv is None:
-            dv = self._dv = int(self.host[168:176].view(np.int64)[0])
-        return dv
+        """Elements of an output row."""
+        return _PLAN_DV.unpack_from(self.host, 168)[0]
 
     def launches(self) -> int:
         n = ctypes.c_int(0)

@@ -69,9 +69,10 @@ __global__ void __launch_bounds__(256, kCtas) paged_kv_compact_kernel(const Comp
     const int m = min(kRows, n - k0);
     __syncthreads();
     for (int k = tid; k < m; k += blockDim.x) {
-      const long long s = pre + p.path[o + k0 + k], d = pre + k0 + k;
+      const int node = p.path[o + k0 + k];
+      const long long s = pre + node, d = pre + k0 + k;
       src_row[k] = -1;
-      if (s == d) continue;
+      if (s == d || node < 0 || node >= L) continue;   // (checked above, should the path change meanwhile)
       const int ps = p.kv_indices[pg0 + (int)(s >> p.log2_page)], pd = p.kv_indices[pg0 + (int)(d >> p.log2_page)];
       if ((unsigned)ps >= (unsigned)p.num_pages || (unsigned)pd >= (unsigned)p.num_pages) {
         bad_page = 1;

@@ -138,6 +138,21 @@ def test_compact_validation_without_device(va):
         assert call(**bad) == -2, bad
 
 
+def test_compact_refuses_pools_that_overlap(va):
+    """The same pool twice, or one that begins inside the other, either way round."""
+    at = ctypes.c_void_p
+
+    def call(k, v, d=128, dv=64):
+        t = at(4096)
+        return va.lib().paged_kv_compact(t, t, t, 4, t, t, t, at(k), at(v), 3, 1, 2, d, dv, 16, 10, 0, 0, None, None,
+                                         None)
+
+    k_bytes, v_bytes = 3 * 10 * 2 * 16 * 128 * 2, 3 * 10 * 2 * 16 * 64 * 2
+    base = 1 << 20
+    for k, v in ((base, base), (base, base + k_bytes - 16), (base + v_bytes - 16, base), (base, base + 16)):
+        assert call(k, v) == -1
+
+
 def test_binding_refuses_host_tensors(va):
     z = torch.zeros
     with pytest.raises(ValueError, match="current CUDA device"):

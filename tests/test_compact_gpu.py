@@ -95,6 +95,18 @@ def test_matches_host_copy(va, name):
     assert np.array_equal(got[0], k) and np.array_equal(got[1], v) and np.array_equal(got[2], new)
 
 
+def test_pools_side_by_side_in_one_tensor(va):
+    c = _case(3, **CASES["layers"])
+    k, v, new, _ = _expect(c)
+    t = _dev(c)
+    t["k"], t["v"] = torch.stack([t["k"], t["v"]])
+    got = _run(va, c, t)
+    assert got[3] == 0
+    assert np.array_equal(got[0], k) and np.array_equal(got[1], v) and np.array_equal(got[2], new)
+    with pytest.raises(RuntimeError):
+        va.paged_kv_compact(t["acc"], t["path"], t["qo"], t["kvp"], t["ids"], t["last"], t["k"], t["k"])
+
+
 def test_bad_paths_move_nothing(va):
     """A path that does not ascend, leaves the request or is longer than it:
     its request keeps its slots and length, the others are compacted."""
