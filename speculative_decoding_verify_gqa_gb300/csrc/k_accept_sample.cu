@@ -34,6 +34,7 @@
 #include "../../include/verify_attn.h"
 #include "va_device.cuh"
 #include "va_kernels.h"
+#include "va_tc.cuh"
 
 namespace va {
 namespace {
@@ -68,17 +69,25 @@ __device__ __forceinline__ void cluster_sync() {
   cluster_arrive();
   cluster_wait();
 }
-// Store 8 bytes at shared address `addr` (of this CTA) in the shared memory
-// of CTA `cta` of the cluster.
-__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t cta, uint64_t v) {
-  uint32_t a;
+// Store 16 bytes at shared address `addr` (of this CTA) in the shared memory
+// of CTA `cta` of the cluster, counted there by the mbarrier at `bar`.
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t bar, uint32_t cta, uint64_t x, uint64_t y) {
+  uint32_t a, m;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(cta));
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(m) : "r"(bar), "r"(cta));
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(a),
+               "l"(x), "l"(y), "r"(m)
+               : "memory");
 }
-__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t cta, uint32_t v) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(cta));
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+__device__ __forceinline__ bool cluster_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Ask for [p, p + bytes) to be brought into L2, rounded inwards to 16 bytes:
@@ -146,10 +155,15 @@ struct RowState {
   uint32_t marks[kMarks];   // bit (x >> 3) mod 32 kMarks for every child's token x
   int child_tok[kChildList];
 };
+// What a CTA tells the others of the cluster about a row: a sum or key; a
+// maximum (low half) and where its walk stands (high half).
+struct alignas(16) Message {
+  uint64_t a, b;
+};
 struct Shared {
   uint64_t part_a[kRows][kWarps], part_b[kRows][kWarps];
-  uint64_t ex_a[2][kRows][kMaxCluster], ex_b[2][kRows][kMaxCluster];  // the cluster's exchange, two phases
-  uint32_t ex_tag[2][kMaxCluster];                                    // where each CTA's walk stands
+  Message ex[2][kRows][kMaxCluster];   // the cluster's exchange, two phases
+  uint64_t ex_bar[2];
   int o, L;                                                           // the request's first row, its nodes
   RowState row[kRows];
   int node[kRows], next[kRows], more[kRows];   // each row's node; the accepted child, or -1; a residual's sum is wanted first
@@ -217,6 +231,11 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = p.cluster;
   const int rank = (int)cluster_rank(), b = blockIdx.x / C;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.ex_bar[i]), 1);
+    mbar_fence_init();
+    for (int i = 0; i < 2; ++i) mbar_expect_tx(smem_u32(&sh.ex_bar[i]), C * kRows * (int)sizeof(Message));
+  }
   cluster_arrive();  // waited for before the first store to another CTA's shared memory
   grid_dependency_wait();
   grid_dependents_launch();
@@ -253,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   };
   // the noise (read last, but always) too: at once where SMs idle, else while
   // the first pass's exchange and decisions leave HBM idle -- asked for at the
-  // start it would delay the rows (64 chains: 49.8 us, 48.5 behind them)
+  // start it would delay the rows (64 chains: 46.3 us, 44.5 behind them)
   const bool noise_first = p.rows == kRows;
   auto prefetch_noise = [&]() {
     if (!greedy) prefetch_l2(noise + c0, (int64_t)(c1 - c0) * 4);
@@ -297,31 +316,40 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   const float c_hi = sh.c_hi, c_lo = sh.c_lo;
   cluster_wait();
 
-  // The exchange: lane k of a warp that has a row's words sends them to CTA k,
-  // and after the barrier every CTA has all of them in sh.ex_a / ex_b
-  // [phase][row][0 .. C).  The two phases alternate, so a CTA that runs ahead
-  // never writes what a slower one still reads.  With them goes a tag of where
-  // the sender's walk stands.  Every CTA computes the same walk from the same
-  // inputs; should they differ -- inputs written while they are read -- all of
-  // them see it at the same barrier and end there, before one waits for, or
-  // writes to, another that has left.
+  // The exchange: lane k of the r-th warp sends its message of row r to CTA k,
+  // and an mbarrier here counts the messages of all CTAs into sh.ex[phase][row]
+  // [0 .. C): one way through the cluster's network, where a cluster barrier
+  // behind plain stores takes two (a chain of 4 drafts: 7.5 us, 7.9 with it).  All kRows
+  // messages are always sent, so every count is the same.  The two phases
+  // alternate, so a CTA that runs ahead never writes what a slower one still
+  // reads.  With them goes a tag of where the sender's walk stands.  Every CTA
+  // computes the same walk from the same inputs; should they differ -- inputs
+  // written while they are read -- all of them see it at the same exchange and
+  // end there, before one waits for, or writes to, another that has left.
   int phase = 0;
-  auto send = [&](int r, uint64_t x, uint64_t y) {
-    if (lane < C) {
-      cluster_store(smem_u32(&sh.ex_a[phase][r][rank]), lane, x);
-      cluster_store(smem_u32(&sh.ex_b[phase][r][rank]), lane, y);
-    }
-    __syncwarp();
-  };
-  auto agree = [&](uint32_t tag) -> bool {  // every thread; after the senders' send()
-    if (warp == kWarps - 1 && lane < C) cluster_store(smem_u32(&sh.ex_tag[phase][rank]), lane, tag);
-    __syncwarp();
-    cluster_sync();
-    return __all_sync(0xffffffffu, lane >= C || sh.ex_tag[phase][lane] == sh.ex_tag[phase][0]);
+  uint32_t parities = 0;
+  bool late = false;
+  // every thread, all lanes of a warp with the same words; false: the CTAs' walks differ
+  auto exchange = [&](uint32_t tag, uint64_t a, uint32_t m) -> bool {
+    phase ^= 1;
+    if (warp < kRows && lane < C)
+      cluster_store(smem_u32(&sh.ex[phase][warp][rank]), smem_u32(&sh.ex_bar[phase]), lane, a, (uint64_t)tag << 32 | m);
+    bool here = false;
+    for (uint32_t i = 0; i < kSpinLimit && !here; ++i)
+      here = cluster_try_wait(smem_u32(&sh.ex_bar[phase]), (parities >> phase) & 1u);
+    late = !__syncthreads_and(here);
+    parities ^= 1u << phase;
+    if (tid == 0) mbar_expect_tx(smem_u32(&sh.ex_bar[phase]), C * kRows * (int)sizeof(Message));   // its next use
+    const uint32_t other = (uint32_t)(sh.ex[phase][0][lane < C ? lane : 0].b >> 32);
+    return __all_sync(0xffffffffu, other == tag) && !late;
   };
   enum : uint32_t { kStats = 1u << 28, kResidual = 2u << 28, kBonus = 3u << 28, kEnd = 4u << 28, kNone = 5u << 28 };
   // no answer: the request's outputs say so
   auto give_up = [&](bool flag) {
+    if (late) {   // nothing may arrive here after this CTA has ended: wait for the others to end too
+      if (tid == 0 && p.status) atomicOr(p.status, VA_DEV_TIMEOUT);
+      cluster_sync();
+    }
     if (rank != 0) return;
     if (tid == 0) {
       p.accept_len[b] = 0;
@@ -335,8 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
       }
   };
   if (bad || L == 0) {
-    phase ^= 1;   // as the first exchange of a walk
-    const bool same = agree(kNone);
+    const bool same = exchange(kNone, 0, 0);
     give_up(bad || !same);
     return;
   }
@@ -368,10 +395,10 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   for (;;) {
     // ---- the rows of this pass: the first child's always, those below it
     // while no node has a choice.  A chain of 4 drafts (32,016 tokens) took
-    // 10.1 us with up to eight rows, 11.5 with four, 13.4 with two and 17.3 with one;
-    // in a wide tree two are best (16.4 us against 18.7 with one and with four).
+    // 7.9 us with up to eight rows, 9.4 with four, 11.0 with two and 14.3 with one;
+    // a wide tree 13.6 us with the first child's row and 16.8 without.
     // The host asks for eight rows where the batch leaves SMs idle, else for
-    // four: 64 ragged chains took 47.8 us with four and 52.1 with eight, whose
+    // four: 64 ragged chains took 44.6 us with four and 47.0 with eight, whose
     // rows past the accepted ones are read from HBM for nothing.
     int n = 1, mine = (warp & (kRows - 1)) == 0 ? v : -1;   // rows; the node that this warp decides about
     int n_kids = L;                                         // how many children it has at most
@@ -415,6 +442,22 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         scan = L;
       }
       if (n_kids == 0) scan = L;
+      if (L <= kNodes && n_kids <= 32 && scan < L) {   // the whole tree at once
+        bool is[kNodes / 32];
+        uint32_t who[kNodes / 32];
+#pragma unroll
+        for (int c = 0; c < kNodes / 32; ++c) {
+          const int i = 32 * c + lane;
+          is[c] = i > mine && i < L && sh.par[i] == mine;
+          who[c] = __ballot_sync(0xffffffffu, is[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < kNodes / 32; ++c) {
+          if (is[c]) rs.kid[cnt + __popc(who[c] & ((1u << lane) - 1u))] = 32 * c + lane;
+          cnt += __popc(who[c]);
+        }
+        scan = L;
+      }
       while (scan < L && cnt < 32) {
         const int i = scan + lane;
         const bool is = i < L && par[i] == mine;
@@ -534,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
       }
       if (greedy) {
         // the lanes that hold the warp's maximum look it up where they met it
-        // (10.3 us of a 4-row pass over 128,256 tokens came down to 5.5
+        // (10.3 us of a 4-row pass over 128,256 tokens came down to 3.9
         // against a key of value and index kept for every entry)
         uint64_t best = 0;
         for (int i = t0; i < n_end; i += step) {
@@ -583,26 +626,24 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     }
     __syncthreads();
     if (!noise_first && v == 0 && tid == kThreads - 1) prefetch_noise();
-    phase ^= 1;
-    // `count` parts, one a lane, joined in every lane
-    auto join = [&](const uint64_t* pa, const uint64_t* pb, int count, float* mo) -> uint64_t {
-      const float pm = lane < count ? __uint_as_float((uint32_t)pa[lane]) : -INFINITY;
+    // the lanes' maxima and sums, joined in every lane
+    auto join = [&](float pm, uint64_t pf, float* mo) -> uint64_t {
       const float jm = warp_max(pm);
       *mo = jm;
-      return warp_add64(pm > -INFINITY ? scale64(pb[lane], weight(pm, jm)) : 0);
+      return warp_add64(pm > -INFINITY ? scale64(pf, weight(pm, jm)) : 0);
     };
     float m = -INFINITY;
     uint64_t f_sum = 0;
     int am = -1;
+    uint64_t mine_a = 0;
     if (mine >= 0) {
-      if (greedy) {
-        send(warp, warp_max64(lane < row_warps ? sh.part_a[warp][lane] : 0), 0);
-      } else {
-        const uint64_t f = join(sh.part_a[warp], sh.part_b[warp], row_warps, &m);
-        send(warp, __float_as_uint(m), f);
-      }
+      const bool in = lane < row_warps;
+      if (greedy) mine_a = warp_max64(in ? sh.part_a[warp][lane] : 0);
+      else
+        mine_a = join(in ? __uint_as_float((uint32_t)sh.part_a[warp][lane]) : -INFINITY,
+                      in ? sh.part_b[warp][lane] : 0, &m);
     }
-    if (!agree(kStats | ((uint32_t)v & 0xffffffu) << 4 | (uint32_t)n)) {
+    if (!exchange(kStats | ((uint32_t)v & 0xffffffu) << 4 | (uint32_t)n, mine_a, __float_as_uint(m))) {
       give_up(true);
       return;
     }
@@ -706,11 +747,12 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     };
     if (mine >= 0) {
       if (greedy) {
-        const uint64_t key = warp_max64(lane < C ? sh.ex_a[phase][warp][lane] : 0);
+        const uint64_t key = warp_max64(lane < C ? sh.ex[phase][warp][lane].a : 0);
         dead = key <= logit_key(-INFINITY, 0);
         am = dead ? 0 : (int)(0xffffffffu - (uint32_t)key);
       } else {
-        f_sum = join(sh.ex_a[phase][warp], sh.ex_b[phase][warp], C, &m);
+        const Message in = sh.ex[phase][warp][lane < C ? lane : 0];
+        f_sum = join(lane < C ? __uint_as_float((uint32_t)in.b) : -INFINITY, in.a, &m);
         dead = f_sum == 0;
         sf = __ull2float_rn(f_sum) * __int_as_float((129 - sum_bits) << 23);
       }
@@ -782,14 +824,13 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
       uint64_t f = warp_add64(__float2ull_rn(t * inv * 0x1p50f));
       if (lane == 0) sh.part_a[0][warp] = f;
       __syncthreads();
-      phase ^= 1;
-      if (warp == 0) send(0, warp_add64(lane < kWarps ? sh.part_a[0][lane] : 0), 0);
-      if (!agree(kResidual | ((uint32_t)at & 0xffffffu) << 4 | (uint32_t)r)) {
+      if (warp == 0) f = warp_add64(lane < kWarps ? sh.part_a[0][lane] : 0);
+      if (!exchange(kResidual | ((uint32_t)at & 0xffffffu) << 4 | (uint32_t)r, f, 0)) {
         give_up(true);
         return;
       }
       if (warp == r) {
-        f = warp_add64(lane < C ? sh.ex_a[phase][0][lane] : 0);
+        f = warp_add64(lane < C ? sh.ex[phase][0][lane].a : 0);
         B = (double)f * 0x1p-50;
         Bf = (float)B;
         decide();
@@ -810,8 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     if (QT && tid == 0 && !last.dead && !greedy)
       prefetch_l2(static_cast<const uint8_t*>(q_row) + (size_t)c0 * QES, (int64_t)(c1 - c0) * QES);
     if (last.dead || greedy) {
-      phase ^= 1;
-      if (!agree(kEnd | ((uint32_t)at & 0xffffffu) << 4)) {
+      if (!exchange(kEnd | ((uint32_t)at & 0xffffffu) << 4, 0, 0)) {
         give_up(true);
         return;
       }
@@ -877,13 +917,12 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         uint64_t key = warp_max64(best_i >= 0 ? race_key(__fdiv_rn(best_w, best_e), (uint32_t)best_i) : 0);
         if (lane == 0) sh.part_a[0][warp] = key;
         __syncthreads();
-        phase ^= 1;
-        if (warp == 0) send(0, warp_max64(lane < kWarps ? sh.part_a[0][lane] : 0), 0);
-        if (!agree(kBonus | ((uint32_t)at & 0xffffffu) << 4 | (plain ? 1u : 0u))) {
+        if (warp == 0) key = warp_max64(lane < kWarps ? sh.part_a[0][lane] : 0);
+        if (!exchange(kBonus | ((uint32_t)at & 0xffffffu) << 4 | (plain ? 1u : 0u), key, 0)) {
           give_up(true);
           return;
         }
-        key = warp_max64(lane < C ? sh.ex_a[phase][0][lane] : 0);
+        key = warp_max64(lane < C ? sh.ex[phase][0][lane].a : 0);
         if (key != 0) {
           bonus = (int)(0xffffffffu - (uint32_t)key);
           break;

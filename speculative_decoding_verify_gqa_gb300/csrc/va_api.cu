@@ -973,9 +973,9 @@ int verify_accept_greedy(const void* logits, va_dtype logits_dtype, int64_t tota
 
 // CTAs per request of the sampled acceptance: a power of two up to the
 // portable cluster size, at most two CTAs an SM over the batch -- 64 ragged
-// chains over 128,256 tokens took 49 us with four CTAs each, 55 with two and
-// 66 with eight -- and at least 4096 entries a CTA (a chain of 4 drafts over
-// 32,016 tokens: 9.3 us with eight CTAs, 10.7 with four).
+// chains over 128,256 tokens took 45 us with four CTAs each, 48 with two and
+// 60 with eight -- and at least 4096 entries a CTA (a chain of 4 drafts over
+// 32,016 tokens: 7.9 us with eight CTAs, 9.4 with four).
 static int sample_cluster(int batch, int vocab, int num_sms) {
   int c = 1;
   while (c < 8 && (int64_t)batch * c * 2 <= 2LL * num_sms && vocab > 4096 * c) c *= 2;
