@@ -164,7 +164,8 @@ struct Shared {
   uint64_t part_a[kRows][kWarps], part_b[kRows][kWarps];
   Message ex[2][kRows][kMaxCluster];   // the cluster's exchange, two phases
   uint64_t ex_bar[2];
-  int o, L;                                                           // the request's first row, its nodes
+  alignas(16) int keys[kThreads];   // the batch, in the order it is taken
+  int b, o, L;                                                        // the request's first row, its nodes
   RowState row[kRows];
   int node[kRows], next[kRows], more[kRows];   // each row's node; the accepted child, or -1; a residual's sum is wanted first
   int par[kNodes], tok[kNodes], first[kNodes], kids[kNodes];  // parents, tokens, first children, their number
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = p.cluster;
-  const int rank = (int)cluster_rank(), b = blockIdx.x / C;
+  const int rank = (int)cluster_rank(), place = blockIdx.x / C;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.ex_bar[i]), 1);
     mbar_fence_init();
@@ -241,18 +242,47 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   grid_dependents_launch();
   // read once, for every thread: what steers the barriers below is the same
   // throughout the CTA even if the caller's tables change under it
-  if (tid == 0) {
-    const int o = p.qo_indptr[b];
+  // Where not all CTAs fit the GPU at once, the clusters -- which start in the
+  // order of their numbers -- take the requests with the most nodes first (T = 0
+  // after others: they end without the race).  64 ragged chains:
+  // 39.2 us, 43.4 in the order given.
+  if (p.rows < kRows && p.batch <= kThreads) {
+    int o_t = 0, L_t = 0, key = -1;
+    float temp_t = 1.f;
+    if (tid < p.batch) {
+      o_t = p.qo_indptr[tid];
+      L_t = p.qo_indptr[tid + 1] - o_t;
+      if (p.temperature) temp_t = p.temperature[tid];
+      key = (2 * min(max(L_t, 0), 1 << 16) + (temp_t == 0.f ? 0 : 8)) * kThreads + (kThreads - 1 - tid);
+    }
+    sh.keys[tid] = key;
+    __syncthreads();
+    if (tid < p.batch) {
+      int before = 0;
+      for (int i = 0; i < p.batch; i += 4) {   // (behind the batch: -1)
+        const int4 other = *reinterpret_cast<const int4*>(&sh.keys[i]);
+        before += (other.x > key) + (other.y > key) + (other.z > key) + (other.w > key);
+      }
+      if (before == place) {
+        sh.b = tid;
+        sh.o = o_t;
+        sh.L = L_t;
+        sh.temp = temp_t;
+      }
+    }
+  } else if (tid == 0) {
+    const int o = p.qo_indptr[place];
+    sh.b = place;
     sh.o = o;
-    sh.L = p.qo_indptr[b + 1] - o;
-    sh.temp = p.temperature ? p.temperature[b] : 1.f;
+    sh.L = p.qo_indptr[place + 1] - o;
+    sh.temp = p.temperature ? p.temperature[place] : 1.f;
   }
   if (tid < kNodes) {
     sh.first[tid] = kNodes;
     sh.kids[tid] = 0;
   }
   __syncthreads();
-  const int o = sh.o, L = sh.L;
+  const int b = sh.b, o = sh.o, L = sh.L;
   const float temp = sh.temp;
   const bool table_ok = o >= 0 && L >= 0 && (int64_t)o + L <= p.total;
   const int V = p.vocab;
