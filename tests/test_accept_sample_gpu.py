@@ -314,6 +314,42 @@ def test_agrees_with_greedy_acceptance_at_temperature_zero(va):
     assert int(g[0].max()) > 2 and am.numel()
 
 
+LONG = {   # 154 requests, a CTA each: long slices of the vocabulary, most drafts rejected
+    "f32_q": dict(lens=[2] * 154, vocab=32768, kind="chain", qdt=F, u_min=0.8),
+    "bf16_q_siblings": dict(lens=[3, 2] * 77, vocab=20000, kind="star", qdt=H, u_min=0.9, temps=[0.8, 0.0, 1.3]),
+    "q_close_to_p": dict(lens=[2] * 154, vocab=16408, kind="chain", qdt=F, u_min=0.95, near=0.02),
+    "f32_logits_masked": dict(lens=[2] * 154, vocab=24576, ldt=F, qdt=F, u_min=0.8, masked=0.98),
+    "longest": dict(lens=[2] * 153, vocab=66000, kind="chain", qdt=H, u_min=0.8),
+}
+
+
+@pytest.mark.parametrize("name", LONG)
+def test_long_slices_match_oracle(va, name):
+    c = _case(21, **LONG[name])
+    _same(c, _run(va, c))
+
+
+def test_long_slices_noise_of_zero_and_residuals_without_mass(va):
+    """p uniform, q twice p on the first half of the tokens: the residual lies on the second half alone."""
+    B, V = 154, 32768
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    lg = torch.zeros(2 * B, V, dtype=H, device="cuda")
+    q = torch.zeros(2 * B, V, device="cuda")
+    q[:, :V // 2] = 2.0 / V
+    noise = torch.ones(B, V, device="cuda")
+    noise[:, 100] = 0.0                       # rejected with its half
+    noise[1::3, 20000] = 0.0                  # the first possible one
+    noise[2::3, [31000, 25001]] = 0.5
+    args = (i32(range(0, 2 * B + 1, 2)), i32([0, 5] * B), i32([-1, 0] * B), torch.full((2 * B,), 0.9, device="cuda"))
+    acc, path, bonus, logp = va.verify_accept_sample(lg, *args, noise, draft_probs=q, want_logprobs=True)
+    assert acc.tolist() == [1] * B
+    assert bonus.tolist() == [[V // 2, 20000, 25001][b % 3] for b in range(B)]
+    assert (logp[::2] + np.log(V)).abs().max() < LOGP_TOL and (logp[1::2] == 0).all()
+    # q above p everywhere: the bonus token comes from p
+    acc, path, bonus, _ = va.verify_accept_sample(lg, *args, noise, draft_probs=torch.full_like(q, 1.5 / V))
+    assert acc.tolist() == [1] * B and bonus.tolist() == [100] * B
+
+
 @pytest.mark.parametrize("V", [1, 7, 1001, 40000])
 @pytest.mark.parametrize("ldt", [H, F], ids=["bf16", "fp32"])
 def test_greedy_bonus_is_the_first_of_equal_maxima(va, ldt, V):
