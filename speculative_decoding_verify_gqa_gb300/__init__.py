@@ -944,14 +944,16 @@ def verify_accept_sample(logits, qo_indptr, draft_tokens, parents, uniforms, noi
         out = (torch.empty(batch, dtype=i32, device=where), torch.empty(total, dtype=i32, device=where),
                torch.empty(batch, dtype=i32, device=where),
                torch.empty(total, dtype=f32, device=where) if want_logprobs else None)
-    acc, path, bonus, logprobs = out
+        into = [None if t is None else t.data_ptr() for t in out]
+    else:
+        acc, path, bonus, logprobs = out
+        into = (_arg(acc, "accept_len", i32, batch, dev), _arg(path, "accepted_nodes", i32, total, dev),
+                _arg(bonus, "bonus_token", i32, batch, dev), _arg(logprobs, "logprobs", f32, total, dev))
     rc = lib().verify_accept_sample(
         lp, _CODES[logits.dtype], total, vocab, ls, _arg(qo_indptr, "qo_indptr", i32, batch + 1, dev), batch,
         _arg(draft_tokens, "draft_tokens", i32, total, dev), _arg(parents, "parents", i32, total, dev),
         _arg(uniforms, "uniforms", f32, total, dev), np_, ns,
-        _arg(temperature, "temperature", f32, batch, dev), dp, dc, ds,
-        _arg(acc, "accept_len", i32, batch, dev), _arg(path, "accepted_nodes", i32, total, dev),
-        _arg(bonus, "bonus_token", i32, batch, dev), _arg(logprobs, "logprobs", f32, total, dev),
+        _arg(temperature, "temperature", f32, batch, dev), dp, dc, ds, *into,
         _arg(status, "status", i32, 1, dev), 0, _device_stream(stream, dev))
     _check("verify_accept_sample", rc)
     return out
