@@ -289,6 +289,29 @@ def test_malformed_requests_are_flagged_and_the_others_answered(va):
     assert acc[:3].tolist() == c["ref"][0][:3].tolist()
 
 
+@pytest.mark.parametrize("qdt", [None, F], ids=["no_q", "q"])
+def test_a_batch_larger_than_the_gpu_is_answered_in_any_order(va, qdt):
+    """200 ragged requests (more CTAs than SMs), empty, malformed and T = 0 ones among them: each as by itself."""
+    rng = np.random.default_rng(11)
+    lens = [int(n) for n in rng.integers(0, 10, 200)]
+    lens[7] = lens[150] = 6
+    c = _case(31, lens=lens, vocab=600, qdt=qdt, temps=[0.9, 0.0, 1.2])
+    _same(c, _run(va, c))
+    a = _dev(c)
+    a[3][int(c["indptr"][7]) + 3] = 5          # a parent that comes later
+    a[6][150] = -1.0                           # no temperature
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    acc, path, bonus, logp = va.verify_accept_sample(*a[:6], temperature=a[6], draft_probs=a[7], want_logprobs=True,
+                                                     status=status)
+    assert int(status) == 2
+    want_acc, want_bonus = np.array(c["ref"][0]), np.array(c["ref"][2])
+    want_acc[[7, 150]], want_bonus[[7, 150]] = 0, -1
+    assert np.array_equal(acc.cpu().numpy(), want_acc) and np.array_equal(bonus.cpu().numpy(), want_bonus)
+    for b in (7, 150):
+        o, e = int(c["indptr"][b]), int(c["indptr"][b + 1])
+        assert (path[o:e] == -1).all() and (logp[o:e] == 0).all()
+
+
 def test_agrees_with_greedy_acceptance_at_temperature_zero(va):
     """Distinct siblings, T = 0: verify_accept_greedy's path and bonus token."""
     rng = np.random.default_rng(2)
