@@ -28,9 +28,11 @@ namespace {
 template <int D, int CH, bool SHARED>
 __global__ void __launch_bounds__(128) verify_merge_kernel(const MergeParams p) {
   constexpr int V = D / 32;
-  // After this library's split kernel in an append-and-run call, the merge
-  // list (uploaded with the plan) and qo_indptr are read before the wait for
-  // it: no kernel of the step writes them.  A call of its own waits first.
+  // After this library's split kernel in the same call, the merge list
+  // (uploaded with the plan) and qo_indptr are read before the wait for it: it
+  // does not write them, and it lets this kernel start only when what came
+  // before it is done (or, with early reads, promised not to write them).  A
+  // call of its own waits first.
   grid_dependents_launch();  // the next kernel may be scheduled; it waits for our completion
   if (!p.early_inputs) grid_dependency_wait();
   const MergeItem it = p.items[blockIdx.x];

@@ -295,13 +295,15 @@ __global__ void __launch_bounds__(TcCfg<FP8, NQ, F8MMA>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // Every CTA of this persistent grid is resident, so the next kernel (the
-  // merge) may be scheduled now: it waits for our completion before reading
-  // anything.  The wait for the grid before this one in the stream (which
+  // merge) may be scheduled early: it waits for our completion before reading
+  // what we write.  It reads its list and qo_indptr before that, so a call of
+  // its own lets it start only when the producer has seen the previous grid,
+  // which may write them, complete.  The wait for the grid before this one in the stream (which
   // may still be writing the drafts' pages) is the producer's alone: it is
   // taken before the first load of a key tile holding draft keys, and every
   // role that writes memory does so after consuming such loads or q, so its
   // writes follow the previous grid's completion.
-  grid_dependents_launch();
+  if (p.early_inputs) grid_dependents_launch();
 
   // Operand u = 2 j (K_j) or 2 j + 1 (V_j) of the CTA's running tile count j
   // sits in ring slot u % NSLOT, on its (u / NSLOT)-th use of that slot.
@@ -328,6 +330,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, NQ, F8MMA>::THREADS, 1)
       if (!p.early_inputs) {
         // a call of its own: nothing is read before the previous grid is done
         grid_dependency_wait();
+        grid_dependents_launch();
         waited = true;
       }
       const bool nhd = p.nhd != 0;

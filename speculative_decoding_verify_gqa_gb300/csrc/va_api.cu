@@ -547,8 +547,7 @@ int verify_attn_run_ex(const void* q, const void* k_cache, const void* v_cache,
                                   stream);
   if (rc) return rc;
   return verify_attn_merge_impl(qo_indptr, num_qo_heads, num_kv_heads, head_dim, out, lse, plan_h,
-                                workspace_d, workspace_bytes,
-                                options && options->early_reads ? 1 : 0, stream);
+                                workspace_d, workspace_bytes, 1, stream);
 }
 
 int verify_attn_run(const void* q, const void* k_cache, const void* v_cache,
