@@ -240,6 +240,33 @@ def test_partial_and_merge_apart(va):
     assert torch.equal(out, got) and torch.equal(lse, got_lse)
 
 
+@pytest.mark.parametrize("kernel", [2, 3, 4])
+def test_plans_taking_turns_in_one_workspace(va, kernel):
+    """Upload, append, run, upload the other plan, append, run, ... without a wait between: each run reads its own lists."""
+    sets = [make_shared(groups=[7], shared=[1024], own=[31, 3, 0, 77, 16, 300, 9], qo=[5, 9, 3, 2, 17, 1, 4], h_q=16, h_kv=4,
+                        d=128, mask="tree", seed=20),
+            make_shared(groups=[3, 2], shared=[512, 2048], own=[100, 0, 5, 44, 700], qo=[1, 2, 30, 4, 6], h_q=16, h_kv=4,
+                        d=128, mask="tree", seed=21)]
+    dws, want = [], []
+    for wl, gi, sp in sets:
+        dw, plan, out, lse = _run(va, wl, gi, sp, kernel=kernel)
+        dws.append(dw)
+        want.append((out.clone(), lse.clone(), plan))
+    ws = torch.empty(max(w[2].workspace_bytes for w in want), dtype=torch.uint8, device="cuda")
+    got = []
+    for turn in range(12):
+        dw, (wl, gi, sp) = dws[turn % 2], sets[turn % 2]
+        plan = shared_plan(va, dw, gi, sp, kernel=kernel, workspace=ws)
+        va.paged_kv_append(dw.k_new, dw.v_new, dw.qo_indptr, dw.kv_indptr, dw.kv_indices, dw.last_page_len, dw.k_cache,
+                           dw.v_cache)
+        out, lse, _ = dw.run(plan=plan)
+        got.append((out, lse))
+    torch.cuda.synchronize()
+    assert va.verify_attn_device_status(plan) == 0
+    for turn, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[turn % 2][0]) and torch.equal(lse, want[turn % 2][1])
+
+
 def test_workspace_of_the_bounds_serves_later_plans(va):
     wl, gi, sp = make_shared(groups=[5], shared=[512], own=[31, 3, 0, 77, 16], qo=[2] * 5, h_q=8, h_kv=2, d=128, seed=15)
     dw = DeviceWorkload(wl)
