@@ -440,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     // while no node has a choice.  A chain of 4 drafts (32,016 tokens) took
     // 7.9 us with up to eight rows, 9.4 with four, 11.0 with two and 14.3 with one;
     // a wide tree 13.6 us with the first child's row and 16.8 without.
-    // The host asks for eight rows where the batch leaves SMs idle, else for
-    // four: 64 ragged chains took 44.6 us with four and 47.0 with eight, whose
+    // The host asks for eight rows where the whole batch fits the GPU, else for
+    // four: 64 ragged chains took 39.6 us with four and 43.2 with eight, whose
     // rows past the accepted ones are read from HBM for nothing.
     int n = 1, mine = (warp & (kRows - 1)) == 0 ? v : -1;   // rows; the node that this warp decides about
     int n_kids = L;                                         // how many children it has at most

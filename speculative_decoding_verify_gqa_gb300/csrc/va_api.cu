@@ -970,15 +970,34 @@ int verify_accept_greedy(const void* logits, va_dtype logits_dtype, int64_t tota
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }
 
-// CTAs per request of the sampled acceptance: a power of two up to the
-// portable cluster size, at most two CTAs an SM over the batch -- 64 ragged
-// chains over 128,256 tokens took 45 us with four CTAs each, 48 with two and
-// 60 with eight -- and at least 4096 entries a CTA (a chain of 4 drafts over
-// 32,016 tokens: 7.9 us with eight CTAs, 9.4 with four).
+// Clusters of the sampled acceptance that the GPU holds at a time, a CTA an SM:
+// clusters of 4 and 8 leave SMs of a GPC over (36 and 15 on the 152 SMs of a
+// GB300, by the occupancy query).
+static int sample_resident(int cluster, int num_sms) {
+  return std::max(1, cluster <= 2 ? num_sms / cluster : cluster == 4 ? num_sms * 9 / 38 : num_sms * 15 / 152);
+}
+
+// CTAs per request: of 1, 2, 4 and 8 with more than 512 entries a CTA the one
+// that this estimate finds fastest, in us.  A request by itself takes 7 us and
+// 0.3 us per 1000 entries of a CTA's slice; clusters that do not fit at once
+// take turns, the longest first; and all requests share HBM.  Measured with 1
+// to 600 ragged chains of up to 8 drafts and trees of up to 32, 8,192 to
+// 128,256 tokens: the choice is at most 14 % over the best of the four (30 trees
+// over 32,000 tokens took 20.0, 13.8, 15.2 and 19.2 us with 8, 4, 2 and 1; 20
+// chains over 128,256 tokens 20.1, 23.0, 35.0 and 60.1).
 static int sample_cluster(int batch, int vocab, int num_sms) {
-  int c = 1;
-  while (c < 8 && (int64_t)batch * c * 2 <= 2LL * num_sms && vocab > 4096 * c) c *= 2;
-  return c;
+  int best = 1;
+  double best_us = 0.0;
+  for (int c = 1; c <= 8; c *= 2) {
+    if (c > 1 && vocab <= 512 * c) break;
+    const double alone = 7.0 + 0.3e-3 * vocab / c, turns = (double)batch / sample_resident(c, num_sms);
+    const double us = std::max(turns <= 1.0 ? alone : alone * (0.7 + 0.8 * turns), alone + 1.9e-6 * batch * vocab);
+    if (c == 1 || us < best_us) {
+      best = c;
+      best_us = us;
+    }
+  }
+  return best;
 }
 
 int verify_accept_sample(const void* logits, va_dtype logits_dtype, int64_t total_qo, int vocab,
@@ -1034,7 +1053,7 @@ int verify_accept_sample(const void* logits, va_dtype logits_dtype, int64_t tota
   p.vocab = vocab;
   p.batch = batch;
   p.cluster = sample_cluster(batch, vocab, num_sms);
-  p.rows = p.batch * p.cluster <= num_sms ? 8 : 4;
+  p.rows = batch <= sample_resident(p.cluster, num_sms) ? 8 : 4;
   p.slice = ((vocab + p.cluster - 1) / p.cluster + 7) / 8 * 8;
   p.vec = vocab % 8 == 0 && la % 16 == 0 && row_stride * les % 16 == 0 && na % 16 == 0 &&
           noise_stride % 4 == 0 && (!draft_probs || (qa % 16 == 0 && draft_stride * qes % 16 == 0));

@@ -337,7 +337,7 @@ def test_agrees_with_greedy_acceptance_at_temperature_zero(va):
     assert int(g[0].max()) > 2 and am.numel()
 
 
-LONG = {   # 154 requests, a CTA each: long slices of the vocabulary, most drafts rejected
+LONG = {   # 154 requests, a CTA or two each: long slices of the vocabulary, most drafts rejected
     "f32_q": dict(lens=[2] * 154, vocab=32768, kind="chain", qdt=F, u_min=0.8),
     "bf16_q_siblings": dict(lens=[3, 2] * 77, vocab=20000, kind="star", qdt=H, u_min=0.9, temps=[0.8, 0.0, 1.3]),
     "q_close_to_p": dict(lens=[2] * 154, vocab=16408, kind="chain", qdt=F, u_min=0.95, near=0.02),
