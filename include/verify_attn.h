@@ -618,7 +618,9 @@ int verify_accept_greedy(const void* logits, va_dtype logits_dtype, int64_t tota
  * draft_probs bf16 or fp32, >= 0.  A draft token outside [0, vocab) is
  * rejected.  An empty request gives accept_len 0 and bonus -1; one whose
  * parents, tables or temperature (negative, infinite, NaN) are invalid gives
- * the same, its path -1, and raises VA_DEV_BAD_TABLE in status_d (nullable).
+ * the same, its path -1, and raises VA_DEV_BAD_TABLE in status_d (nullable); so
+ * does one whose inputs are overwritten during the call (and VA_DEV_TIMEOUT if
+ * a wait among its CTAs ran out).
  * Rows may start at any element (16-byte aligned rows of a vocabulary that is
  * a multiple of 8 are read fastest).  Weights and residuals are computed in
  * fp32 and summed in 64-bit fixed point; decisions too close for fp32 are made
