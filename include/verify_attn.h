@@ -255,7 +255,12 @@ int verify_attn_plan(const int32_t* kv_indptr_h, const int32_t* qo_indptr_h,
  * mask_indptr are NULL iff the plan was made with has_mask = 0.
  * sm_scale <= 0 selects head_dim^-1/2.  k_scale / v_scale multiply the
  * stored keys / values (1 for bf16 caches); both must be finite and > 0.
- * lse may be NULL.  num_pages bounds every page id (a page id outside the
+ * lse may be NULL.  A row (token, query head) that sees no key gives out 0 and
+ * lse -inf.  A NaN in its q, or in a key that it sees, makes the row NaN in out
+ * and lse; keys that its mask hides may hold anything.  A NaN or infinity in an
+ * element of a value row makes that element of out NaN or infinite in the rows
+ * that see the key, and may make it NaN in other rows of the same request (0
+ * times it is added there).  num_pages bounds every page id (a page id outside the
  * pool is read as zeros and raises VA_DEV_BAD_PAGE).  plan_h is the host plan
  * buffer; it is read on the host during the call only.
  * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_PLAN_MISMATCH,

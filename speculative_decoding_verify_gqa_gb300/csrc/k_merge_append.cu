@@ -95,7 +95,6 @@ __global__ void __launch_bounds__(128) verify_merge_kernel(const MergeParams p) 
     float cm = -INFINITY;
 #pragma unroll
     for (int c = 0; c < CH; ++c) cm = fmaxf(cm, ls[c]);
-    if (cm == -INFINITY) continue;  // no split of this chunk carries mass
     if (cm > m) {
       const float sc = ex2((m - cm) * kLog2e);  // 0 while m = -inf
       den *= sc;
@@ -105,14 +104,14 @@ __global__ void __launch_bounds__(128) verify_merge_kernel(const MergeParams p) 
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (ls[c] == -INFINITY) continue;  // an empty split carries no mass
+      if (ls[c] == -INFINITY) continue;  // an empty split carries no mass (one with a NaN does)
       const float w = ex2((ls[c] - m) * kLog2e);
       den += w;
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] += w * x[c][i];
     }
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = den == 0.f ? 0.f : 1.f / den;
   const int rr = it.row0 + r;
   const int t = rr / p.group, g = rr - t * p.group;
   const size_t orow = (size_t)(qo0 + t) * p.h_q + (size_t)it.h * p.group + g;
@@ -125,7 +124,7 @@ __global__ void __launch_bounds__(128) verify_merge_kernel(const MergeParams p) 
   } else {
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
   }
-  if (p.lse && lane == 0) p.lse[orow] = den > 0.f ? m + logf(den) : -INFINITY;
+  if (p.lse && lane == 0) p.lse[orow] = den == 0.f ? -INFINITY : m + logf(den);
 }
 
 // Paged append (vLLM PR #1679: every draft's K/V is cached before attention;

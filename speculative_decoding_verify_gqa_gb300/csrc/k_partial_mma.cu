@@ -428,8 +428,10 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
     if (rl >= nrows) continue;
     const float m = half ? m_hi : m_lo;
     const float l = half ? l_hi : l_lo;
-    const float lse = l > 0.f ? m * p.scale_nat + logf(l) : -INFINITY;
-    const float inv = l > 0.f ? p.v_scale / l : 0.f;
+    // no mass is l = 0, and nothing else: a NaN among the scores reached l
+    // and stays in the row (the merge passes it on)
+    const float lse = l == 0.f ? -INFINITY : m * p.scale_nat + logf(l);
+    const float inv = l == 0.f ? 0.f : p.v_scale / l;
     if (it.part_row < 0) {
       const int rr = row0 + rl;
       const int t = rr / G, g = rr - t * G;

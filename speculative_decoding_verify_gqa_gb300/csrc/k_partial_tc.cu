@@ -1170,8 +1170,10 @@ __global__ void __launch_bounds__(TcCfg<FP8, NQ, F8MMA>::THREADS, 1)
       // epilogue
       if (!__all_sync(0xffffffffu, mbar_wait(bar(B_O_DONE + qt), no & 1, abort_flag))) { live = false; break; }
       tc_fence_after();
-      const float lse = l > 0.f ? (m_used + __log2f(l)) * kLn2 : -INFINITY;
-      const float inv = l > 0.f ? p.v_scale / l : 0.f;
+      // no mass is l = 0, and nothing else: a NaN among the scores reached l
+      // and stays in the row (the merge passes it on)
+      const float lse = l == 0.f ? -INFINITY : (m_used + __log2f(l)) * kLn2;
+      const float inv = l == 0.f ? 0.f : p.v_scale / l;
       // The first write of this thread waits for the previous grid: an item
       // whose tiles all went out before the producer's wait could otherwise
       // finish before it, and that grid may still read the workspace (a
