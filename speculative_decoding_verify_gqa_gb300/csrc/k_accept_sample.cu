@@ -729,9 +729,11 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
           }
           const float all = __shfl_sync(0xffffffffu, before, 31);
           before -= cw;
-          const float lhs = greedy ? 0.f : cu * (Bf * sf - before);
+          // (rounding may put the weights before this child above all there is:
+          // nothing is left then, and not less)
+          const float lhs = greedy ? 0.f : cu * fmaxf(Bf * sf - before, 0.f);
           const bool near = !greedy && fabsf(cw - lhs) <= 4e-6f * (cw + sf) && cx > -INFINITY;
-          const bool ok = greedy ? cw > 0.f : lhs < cw;
+          const bool ok = cw > 0.f && lhs < cw;   // a weight of 0 is never accepted
           uint32_t may = __ballot_sync(0xffffffffu, (ok || near) && ((win >> lane) & 1u));
           const uint32_t close = __ballot_sync(0xffffffffu, near);
           while (may) {
@@ -741,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
             if ((close >> j) & 1u) {
               double b = B;
               for (int i = 0; i < j; ++i) b -= (double)__shfl_sync(0xffffffffu, cw, i) / sum_value(f_sum);
-              yes = precisely(xj, 1.f, uj, b);
+              yes = precisely(xj, 1.f, uj, fmax(b, 0.0));
             }
             if (yes) {
               next = __shfl_sync(0xffffffffu, kid, j);
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
           win = 0;
           if (next >= 0) break;
           if (!greedy && scan < L) {
-            B -= (double)(all / sf);
+            B = fmax(B - (double)(all / sf), 0.0);
             Bf = (float)B;
           }
         } else {
