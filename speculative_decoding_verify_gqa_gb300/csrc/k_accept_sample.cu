@@ -28,10 +28,10 @@
 // they lead along those rows.  Rows further off are read only when the walk
 // gets there, so a 64-node tree whose path is two nodes long reads four rows.
 //
-// On one GB300 in a CUDA graph: a chain of 4 drafts over 32,016 tokens 7.4 us,
-// 8 trees of 64 nodes over 128,256 tokens 12.8 us (latency both), 64 ragged
-// chains of up to 8 nodes over 128,256 tokens, fp32 drafts, 37.8 us (103 MB of
-// HBM: 40 % of its rate; 1.7 waves of CTAs of some 15 us, a pass bound by HBM and
+// On one GB300 in a CUDA graph: a chain of 4 drafts over 32,016 tokens 7.7 us,
+// 8 trees of 64 nodes over 128,256 tokens 13.4 us (latency both), 64 ragged
+// chains of up to 8 nodes over 128,256 tokens, fp32 drafts, 39.9 us (103 MB of
+// HBM: 38 % of its rate; 1.7 waves of CTAs of some 15 us, a pass bound by HBM and
 // by the exponentials, 16 a cycle and SM, the steps between by latency).
 #include <cuda_runtime.h>
 #include <math.h>
@@ -157,8 +157,9 @@ __device__ __forceinline__ void load8(const void* row, int64_t i, float* x) {
 
 // What is known of one row of a pass.
 struct RowState {
-  uint64_t sum;             // of its weights 2^((x - m) log2(e) / T), in units of 2^(2 - sum_bits)
-  float m, sf, as;          // maximum; the sum in fp32; A after the children tried so far, times the sum
+  // Maximum; its weights 2^((x - m) log2(e) / T) but the maximum's own 1; their
+  // sum, 1 + tail; A after the children tried so far, times the sum.
+  float m, tail, sf, as;
   float x;                  // logit of the accepted child's token
   int am, dead;             // first argmax (T = 0); nothing of the row is possible
   int n_child;
@@ -166,13 +167,14 @@ struct RowState {
   uint32_t marks[kMarks];   // bit (x >> 3) mod 32 kMarks for every child's token x
   int child_tok[kChildList];
 };
-// What a CTA tells the others of the cluster about a row: a sum or key; a
-// maximum (low half) and where its walk stands (high half).
+// What a CTA tells the others of the cluster about a row: a tail, a residual's
+// sum or a key; a maximum (low half) and where its walk stands (high half).
 struct alignas(16) Message {
   uint64_t a, b;
 };
 struct Shared {
-  uint64_t part_a[kRows][kWarps], part_b[kRows][kWarps];
+  uint64_t part[kRows][kWarps];        // the warps' parts of a row: tail and maximum, or a key or sum
+  float beat[kWarps];
   Message ex[2][kRows][kMaxCluster];   // the cluster's exchange, two phases
   uint64_t ex_bar[2];
   alignas(16) int keys[kThreads];   // of every request: the larger, the sooner it is taken
@@ -182,8 +184,7 @@ struct Shared {
   int node[kRows], next[kRows], more[kRows];
   int par[kNodes], tok[kNodes], first[kNodes], kids[kNodes];  // parents, tokens, first children, their number
   float u[kNodes];
-  float lx[kNodes], lm[kNodes];                 // emitted tokens' logits and their rows' maxima and sums
-  uint64_t lsum[kNodes];
+  float lx[kNodes], lm[kNodes], lt[kNodes];     // emitted tokens' logits and their rows' maxima and tails
   float c_hi, c_lo;
   // the request's temperature, read again where fp64 needs it: kept in a
   // register, its conversion would be hoisted and done by every thread, on a
@@ -191,12 +192,13 @@ struct Shared {
   volatile float temp;
 };
 
-// Sums of weights and residuals cross threads as fixed-point integers: adding
-// them is exact, takes the integer pipe (fp64 adds run at a 64th of its rate
-// here) and needs no order.  A warp reduces with redux, whose 32-bit words a
-// 64-bit sum is cut into: 27 bits of 32 lanes stay below 2^32.  (A step of a
-// walk is a dozen short dependent pieces of one warp; with five rounds of
-// shuffles for each of its reductions a chain of 4 drafts took 1.5 us longer.)
+// Sums cross threads as integers: adding them is exact, takes the integer pipe
+// (fp64 adds run at a 64th of its rate here) and needs no order.  A warp reduces
+// with redux, whose 32-bit words a 64-bit sum is cut into: 27 bits of 32 lanes
+// stay below 2^32.  (A step of a walk is a dozen short dependent pieces of one
+// warp; with five rounds of shuffles for each of its reductions a chain of 4
+// drafts took 1.5 us longer.)  Residuals are in units of 2^-50; terms of a tail,
+// which may be as small as they like, in the unit that gives the largest of them 27 bits.
 __device__ __forceinline__ uint64_t warp_add64(uint64_t v) {
   constexpr uint32_t kLimb = (1u << 27) - 1;
   const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)v & kLimb),
@@ -215,26 +217,27 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-// a * w for a weight w in [0, 1], in half of a's units (the product's upper bits).
-__device__ __forceinline__ uint64_t scale64(uint64_t a, float w) {
-  return __umul64hi(a, (uint64_t)__float2uint_rn(w * 2147483648.f) << 32);
+// The lanes' terms >= 0 added, each rounded to 2^-27 of the largest or less.
+__device__ __forceinline__ float warp_add(float v) {
+  const int e = max(__float_as_int(warp_max(v)) >> 23, 27);   // (below 2^-100 the unit stays)
+  const uint32_t sum = __reduce_add_sync(0xffffffffu, __float2uint_rn(v * __int_as_float((280 - e) << 23)));
+  return __uint2float_rn(sum) * __int_as_float((e - 26) << 23);
 }
 
-// (x - m) c - log2(sum), times ln 2, in fp32 pairs (fp64 took 1.2 us of a
-// request's end): c = c_hi + c_lo is log2(e) / T and the sum is f 2^unit.
-__device__ __forceinline__ float log_prob(float x, float m, float c_hi, float c_lo, uint64_t f, int unit) {
-  const float s = __ull2float_rn(f);   // within 2^-24, as its terms are
-  const int e = (__float_as_int(s) >> 23) - 127;
-  const float l = log2f(__int_as_float((__float_as_int(s) & 0x7fffff) | 0x3f800000));
+// (x - m) c ln 2 - log(1 + tail) in fp32 pairs (fp64 took 1.2 us of a request's
+// end): c = c_hi + c_lo is log2(e) / T.  Of the likeliest token the first term
+// is 0 and the second keeps the tail's digits, however small it is.
+__device__ __forceinline__ float log_prob(float x, float m, float c_hi, float c_lo, float tail) {
   const float d = x - m, dv = d - x, d_lo = (x - (d - dv)) - (m + dv);   // x - m = d + d_lo
   const float y = d * c_hi;
   if (!(y > -3e38f)) return -INFINITY;
   const float y_lo = fmaf(d, c_hi, -y) + fmaf(d, c_lo, d_lo * c_hi);
-  const float n = (float)-(e + unit);
-  const float t = y + n, tv = t - y, t_lo = (y - (t - tv)) + (n - tv) + y_lo - l;   // log2 p = t + t_lo
-  const float r = t * 0.693147182464599609f;
+  const float r = y * 0.693147182464599609f;
   // ln 2 less its rounding to fp32: -1.9046543e-9
-  return r + (fmaf(t, 0.693147182464599609f, -r) + fmaf(t, -1.9046543e-9f, t_lo * 0.693147182464599609f));
+  const float r_lo = fmaf(y, 0.693147182464599609f, -r) + fmaf(y, -1.9046543e-9f, y_lo * 0.693147182464599609f);
+  const float l = log1pf(tail);
+  const float t = r - l, tv = t - r;
+  return t + ((r - (t - tv)) - (l + tv) + r_lo);
 }
 
 // LB: logits bf16 (else fp32).  QT: draft distributions: 0 none, 1 bf16, 2 fp32.
@@ -419,6 +422,13 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     *w0 = ex2(f32x2_lo(y));
     *w1 = ex2(f32x2_hi(y));
   };
+  // twice that, which is 2 at the maximum and below 2 elsewhere
+  auto twice2 = [&](float x0, float x1, float m, float* w0, float* w1) {
+    const uint64_t d = add_f32x2(f32x2(x0, x1), f32x2(-m, -m));
+    const uint64_t y = fma_f32x2(d, ch2, fma_f32x2(d, cl2, f32x2(1.f, 1.f)));
+    *w0 = ex2(f32x2_lo(y));
+    *w1 = ex2(f32x2_hi(y));
+  };
   auto weight = [&](float x, float m) {
     const float d = x - m;
     return ex2(fmaf(d, c_hi, d * c_lo));
@@ -427,12 +437,6 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
   const int32_t* par = L <= kNodes ? sh.par : p.parents + o;
   const int32_t* tok = L <= kNodes ? sh.tok : p.tokens + o;
   const float* uni = L <= kNodes ? sh.u : p.uniforms + o;
-  // weights of at most 1 in units of 2^-sum_bits: V of them stay below 2^63
-  const int sum_bits = V <= (1 << 22) ? 40 : 31;
-  const float sum_unit = __int_as_float((127 + sum_bits) << 23);
-  // a row's joined sum (two joins halved the unit twice)
-  auto sum_value = [&](uint64_t f) { return (double)f * __longlong_as_double((long long)(1025 - sum_bits) << 52); };
-
   int v = 0, k = 0;
   if (tid == 0 && rank == 0) p.path[o] = 0;
   for (;;) {
@@ -569,9 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
       const uint4* vp = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x_row) + (size_t)v0 * LES);
       const int n_end = head + (c1 - v1);
       auto end_at = [&](int i) { return i < head ? c0 + i : v1 + (i - head); };
-      // running maximum and sum, eight vectors at a time (T = 0: the maximum
-      // and the eight vectors it was first met in)
-      float m = -INFINITY, s = 0.f;
+      // Running maximum and sum, eight vectors at a time (T = 0: the maximum
+      // and the eight vectors it was first met in).  Weights of 1, the maximum's
+      // own, are counted apart: a small weight added to them would lose its
+      // digits, which are all there is of log p where the model is sure (log p
+      // near -1e-6 was off by a tenth of itself, now by 3e-7; it costs 2.0 of
+      // 39.9 us of 64 chains, 0.3 of 7.7 us of a chain of 4 drafts).
+      float m = -INFINITY, s = 0.f, ones = 0.f;
       int i_max = 0;
       constexpr int NV = kVectors;
       for (int i0 = t0; i0 < nvec; i0 += NV * step) {
@@ -597,12 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
                        fmaxf(__uint_as_float(w[j].z), __uint_as_float(w[j].w)));
         }
         if (mx > m) {
-          s = m == -INFINITY ? 0.f : s * weight(m, mx);
+          s = m == -INFINITY ? 0.f : (ones + s) * weight(m, mx);
+          ones = 0.f;
           m = mx;
           i_max = i0;
         }
         if (greedy || m == -INFINITY) continue;
         float s0 = 0.f, s1 = 0.f;
+        uint32_t at_max = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           if (i0 + j * step >= nvec) break;
@@ -610,13 +620,17 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
 #pragma unroll
           for (int q = 0; q < (LB ? 4 : 2); ++q) {
             float w0, w1;
-            if (LB) weight2(__uint_as_float(u[q] << 16), __uint_as_float(u[q] & 0xffff0000u), m, &w0, &w1);
-            else weight2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]), m, &w0, &w1);
-            s0 += w0;
-            s1 += w1;
+            if (LB) twice2(__uint_as_float(u[q] << 16), __uint_as_float(u[q] & 0xffff0000u), m, &w0, &w1);
+            else twice2(__uint_as_float(u[2 * q]), __uint_as_float(u[2 * q + 1]), m, &w0, &w1);
+            // of numbers up to 2, 2 alone has bit 30, and no other bit
+            at_max += __float_as_uint(w0) >> 30;
+            at_max += __float_as_uint(w1) >> 30;
+            s0 += __uint_as_float(__float_as_uint(w0) & 0xbfffffffu);
+            s1 += __uint_as_float(__float_as_uint(w1) & 0xbfffffffu);
           }
         }
-        s += s0 + s1;
+        ones += (float)at_max;
+        s += 0.5f * (s0 + s1);
       }
       if (greedy) {
         // the lanes that hold the warp's maximum look it up where they met it
@@ -647,44 +661,52 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
           if (at_max >= 0) best = max64(best, logit_key(m + 0.f, (uint32_t)at_max));
         }
         best = warp_max64(best);
-        if (lane == 0) sh.part_a[r_mine][w_mine] = best;
+        if (lane == 0) sh.part[r_mine][w_mine] = best;
       } else {
         for (int i = t0; i < n_end; i += step) {
           const float x = load_elem<LB>(x_row, end_at(i));
           if (x > m) {
-            s = m == -INFINITY ? 0.f : s * weight(m, x);
+            s = m == -INFINITY ? 0.f : (ones + s) * weight(m, x);
+            ones = 0.f;
             m = x;
           }
-          if (m > -INFINITY) s += weight(x, m);
+          if (m > -INFINITY) {
+            const float w = weight(x, m);
+            if (w >= 1.f) ones += 1.f;
+            else s += w;
+          }
         }
         // thread -> warp -> CTA -> cluster: each part against its own maximum,
-        // joined against the common one
+        // joined against the common one, whose own weight -- in the first part
+        // that has it -- is left out
         const float wm = warp_max(m);
-        const uint64_t wsum = warp_add64(__float2ull_rn(m == -INFINITY ? 0.f : s * weight(m, wm) * sum_unit));
-        if (lane == 0) {
-          sh.part_a[r_mine][w_mine] = __float_as_uint(wm);
-          sh.part_b[r_mine][w_mine] = wsum;
-        }
+        const uint32_t tops = __ballot_sync(0xffffffffu, m == wm);
+        const float tail = warp_add(m == -INFINITY             ? 0.f
+                                    : lane == __ffs(tops) - 1 ? (ones - 1.f) + s
+                                                               : (ones + s) * weight(m, wm));
+        if (lane == 0) sh.part[r_mine][w_mine] = (uint64_t)__float_as_uint(tail) << 32 | __float_as_uint(wm);
       }
     }
     __syncthreads();
     if (!noise_first && v == 0 && tid == kThreads - 1) prefetch_noise();
-    // the lanes' maxima and sums, joined in every lane
-    auto join = [&](float pm, uint64_t pf, float* mo) -> uint64_t {
+    // the lanes' maxima and tails, joined in every lane
+    auto join = [&](float pm, float pt, float* mo) -> float {
       const float jm = warp_max(pm);
+      const uint32_t tops = __ballot_sync(0xffffffffu, pm == jm);
       *mo = jm;
-      return warp_add64(pm > -INFINITY ? scale64(pf, weight(pm, jm)) : 0);
+      return warp_add(pm == -INFINITY ? 0.f : lane == __ffs(tops) - 1 ? pt : (1.f + pt) * weight(pm, jm));
     };
-    float m = -INFINITY;
-    uint64_t f_sum = 0;
+    float m = -INFINITY, tail = 0.f;
     int am = -1;
     uint64_t mine_a = 0;
     if (mine >= 0) {
       const bool in = lane < row_warps;
-      if (greedy) mine_a = warp_max64(in ? sh.part_a[warp][lane] : 0);
-      else
-        mine_a = join(in ? __uint_as_float((uint32_t)sh.part_a[warp][lane]) : -INFINITY,
-                      in ? sh.part_b[warp][lane] : 0, &m);
+      if (greedy) {
+        mine_a = warp_max64(in ? sh.part[warp][lane] : 0);
+      } else {
+        const uint64_t part = in ? sh.part[warp][lane] : (uint64_t)0xff800000u;   // (no part: -inf)
+        mine_a = __float_as_uint(join(__uint_as_float((uint32_t)part), __uint_as_float((uint32_t)(part >> 32)), &m));
+      }
     }
     if (!exchange(kStats | ((uint32_t)v & 0xffffffu) << 4 | (uint32_t)n, mine_a, __float_as_uint(m))) {
       give_up(true);
@@ -699,10 +721,12 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
     double A = 0.0, B = 1.0;
     float Af = 0.f, Bf = 1.f;             // (their fp32 values: conversions take the fp64 pipe)
     auto child_w = [&]() { return greedy ? (ctok == am && cx > -INFINITY ? 1.f : 0.f) : weight(cx, m); };
-    // u q B < p - A q, times the sum, in fp64: where fp32 is too close to tell
+    // u q B < p - A q, times the sum, in fp64: where fp32 is too close to tell.
+    // (The token's weight anew; sum, A and B as they are.)
+    auto sum64 = [&]() { return 1.0 + (double)tail; };
     auto precisely = [&](float x, float q, float u, double b) {
       const double w = exp(((double)x - (double)m) / (double)sh.temp);
-      const double sum = sum_value(f_sum);
+      const double sum = sum64();
       return (double)u * b * (double)q * sum < w - (QT ? A * (double)q * sum : 0.0);
     };
     auto decide = [&]() {
@@ -742,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
             bool yes = true;
             if ((close >> j) & 1u) {
               double b = B;
-              for (int i = 0; i < j; ++i) b -= (double)__shfl_sync(0xffffffffu, cw, i) / sum_value(f_sum);
+              for (int i = 0; i < j; ++i) b -= (double)__shfl_sync(0xffffffffu, cw, i) / sum64();
               yes = precisely(xj, 1.f, uj, fmax(b, 0.0));
             }
             if (yes) {
@@ -797,16 +821,16 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         am = dead ? 0 : (int)(0xffffffffu - (uint32_t)key);
       } else {
         const Message in = sh.ex[phase][warp][lane < C ? lane : 0];
-        f_sum = join(lane < C ? __uint_as_float((uint32_t)in.b) : -INFINITY, in.a, &m);
-        dead = f_sum == 0;
-        sf = __ull2float_rn(f_sum) * __int_as_float((129 - sum_bits) << 23);
+        tail = join(lane < C ? __uint_as_float((uint32_t)in.b) : -INFINITY, __uint_as_float((uint32_t)in.a), &m);
+        dead = m == -INFINITY;
+        sf = 1.f + tail;
       }
       child_values();
       if (!dead) cw = child_w();
       if (lane == 0) {
         sh.node[warp] = mine;
         rs.m = m;
-        rs.sum = f_sum;
+        rs.tail = tail;
         rs.sf = sf;
         rs.am = am;
         rs.dead = dead;
@@ -825,9 +849,9 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
         if (i < kNodes) {
           sh.lx[i] = e.x;
           sh.lm[i] = e.m;
-          sh.lsum[i] = e.sum;
+          sh.lt[i] = e.tail;
         } else if (p.logprobs) {
-          p.logprobs[o + i] = greedy ? 0.f : log_prob(e.x, e.m, c_hi, c_lo, e.sum, 2 - sum_bits);
+          p.logprobs[o + i] = greedy ? 0.f : log_prob(e.x, e.m, c_hi, c_lo, e.tail);
         }
       }
       k += count;
@@ -867,9 +891,9 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
           t += fmaxf(fmaf(-as, load_elem<QT == 1>(q_row, i), weight(load_elem<LB>(x_row, i), rm)), 0.f);
       }
       uint64_t f = warp_add64(__float2ull_rn(t * inv * 0x1p50f));
-      if (lane == 0) sh.part_a[0][warp] = f;
+      if (lane == 0) sh.part[0][warp] = f;
       __syncthreads();
-      if (warp == 0) f = warp_add64(lane < kWarps ? sh.part_a[0][lane] : 0);
+      if (warp == 0) f = warp_add64(lane < kWarps ? sh.part[0][lane] : 0);
       if (!exchange(kResidual | ((uint32_t)at & 0xffffffu) << 4 | (uint32_t)r, f, 0)) {
         give_up(true);
         return;
@@ -1024,9 +1048,9 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
             const uint32_t owners = __ballot_sync(0xffffffffu, top == warp_top && top > 0.f);
             if (owners && lane == __ffs(owners) - 1) exact(i_first + top_g * 8 * kThreads);
             const float beat_warp = warp_max(best_i >= 0 ? __fdiv_rn(best_w, best_e) : 0.f);
-            if (lane == 0) sh.part_b[0][warp] = __float_as_uint(beat_warp);
+            if (lane == 0) sh.beat[warp] = beat_warp;
             __syncthreads();
-            const float beat = warp_max(lane < kWarps ? __uint_as_float((uint32_t)sh.part_b[0][lane]) : 0.f);
+            const float beat = warp_max(lane < kWarps ? sh.beat[lane] : 0.f);
             best_w = 0.f;
             best_e = 1.f;
             best_i = -1;
@@ -1039,9 +1063,9 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
           race(std::false_type());
         }
         uint64_t key = warp_max64(best_i >= 0 ? race_key(__fdiv_rn(best_w, best_e), (uint32_t)best_i) : 0);
-        if (lane == 0) sh.part_a[0][warp] = key;
+        if (lane == 0) sh.part[0][warp] = key;
         __syncthreads();
-        if (warp == 0) key = warp_max64(lane < kWarps ? sh.part_a[0][lane] : 0);
+        if (warp == 0) key = warp_max64(lane < kWarps ? sh.part[0][lane] : 0);
         if (!exchange(kBonus | ((uint32_t)at & 0xffffffu) << 4 | (plain ? 1u : 0u), key, 0)) {
           give_up(true);
           return;
@@ -1067,7 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 1) accept_sample_kernel(const Sample
           if (i < k && i >= kNodes) continue;   // (written on the way)
           const bool end = i == k;
           const float x = !end ? sh.lx[i] : bonus >= 0 ? load_elem<LB>(x_row, bonus) : 0.f;
-          const float lp = greedy ? 0.f : log_prob(x, end ? last.m : sh.lm[i], c_hi, c_lo, end ? last.sum : sh.lsum[i], 2 - sum_bits);
+          const float lp = greedy ? 0.f : log_prob(x, end ? last.m : sh.lm[i], c_hi, c_lo, end ? last.tail : sh.lt[i]);
           p.logprobs[o + i] = end && bonus < 0 ? 0.f : lp;
         }
       }
