@@ -109,11 +109,11 @@ __global__ void __launch_bounds__(256, kCtas) paged_kv_compact_kernel(const Comp
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
   if (p.batch > 65535) return cudaErrorInvalidValue;
-  // At most the CTAs that are resident together (kCtas on each of 152 SMs): every
-  // CTA of a request walks the same tables first, and a second wave would
-  // do so after the first.
+  // At most the CTAs that are resident together (kCtas on each SM): every CTA
+  // of a request walks the same tables first, and a second wave would do so
+  // after the first.
   const long long threads = (long long)p.layers * p.h_kv * (p.k_chunks + p.v_chunks);
-  const long long most = std::max(1, kCtas * 152 / p.batch);
+  const long long most = std::max(1, kCtas * p.num_sms / p.batch);
   const long long blocks = std::min<long long>((threads + 255) / 256, most);
   void* args[] = {const_cast<CompactParams*>(&p)};
   return launch_kernel(reinterpret_cast<const void*>(paged_kv_compact_kernel),

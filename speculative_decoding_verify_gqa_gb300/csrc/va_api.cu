@@ -1109,6 +1109,8 @@ int paged_kv_compact(const int32_t* accept_len, const int32_t* accepted_nodes,
   const unsigned __int128 rows = (unsigned __int128)num_layers * num_kv_heads * page_size * num_pages;
   const uintptr_t k0 = reinterpret_cast<uintptr_t>(k_cache), v0 = reinterpret_cast<uintptr_t>(v_cache);
   if (k0 < v0 ? k0 + rows * p.k_chunks * 16 > v0 : v0 + rows * p.v_chunks * 16 > k0) return VA_ERR_INVALID_ARGUMENT;
+  rc = query_sms(&p.num_sms);
+  if (rc) return rc;
   cudaError_t e = launch_compact(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }

@@ -157,6 +157,7 @@ struct CompactParams {
   int batch, layers, h_kv, page_size, log2_page, num_pages;
   int k_chunks, v_chunks;     // 16-byte chunks of a K / V row
   int nhd;
+  int num_sms;                // of the device that it is launched on
 };
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
 
