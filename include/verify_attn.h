@@ -627,10 +627,16 @@ int verify_accept_greedy(const void* logits, va_dtype logits_dtype, int64_t tota
  * does one whose inputs are overwritten during the call (and VA_DEV_TIMEOUT if
  * a wait among its CTAs ran out).
  * Rows may start at any element (16-byte aligned rows of a vocabulary that is
- * a multiple of 8 are read fastest).  Weights and residuals are computed in
- * fp32 and summed in 64-bit fixed point; decisions too close for fp32 are made
- * in fp64.  Rows of nodes that are not reached are not read.  The outputs may
- * not overlap the inputs.  No workspace.
+ * a multiple of 8 are read fastest).  Rows of nodes that are not reached are
+ * not read.  The outputs may not overlap the inputs.  No workspace.
+ * Precision: weights are computed in fp32 and added in fp32 by each thread,
+ * across threads as integers, so p is good to about 1e-6 of itself (1.1e-5 at
+ * worst for p above 1e-19), log p to as much of itself, and what rejections
+ * leave of p -- the sum that normalises r -- to as much of 1: where little is
+ * left, r is coarser by its inverse.  A comparison within 4e-6 of its border is
+ * made again in fp64, with the token's weight taken anew and the sums as they
+ * are; one closer to its border than the sums' error may fall either way.  A
+ * token of probability 0 is never emitted.
  * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED (dtypes, sizes past 32
  * bits), VA_ERR_CUDA.
  */
