@@ -254,7 +254,8 @@ int verify_attn_plan(const int32_t* kv_indptr_h, const int32_t* qo_indptr_h,
  * the workspace.  mask /
  * mask_indptr are NULL iff the plan was made with has_mask = 0.
  * sm_scale <= 0 selects head_dim^-1/2.  k_scale / v_scale multiply the
- * stored keys / values (1 for bf16 caches); both must be finite and > 0.
+ * stored keys / values (1 for bf16 caches); both must be finite and > 0, and
+ * sm_scale * k_scale finite.
  * lse may be NULL.  A row (token, query head) that sees no key gives out 0 and
  * lse -inf.  A NaN in its q, or in a key that it sees, makes the row NaN in out
  * and lse; keys that its mask hides may hold anything.  A NaN or infinity in an

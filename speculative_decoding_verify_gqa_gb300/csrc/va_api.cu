@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <string.h>
 
@@ -109,6 +110,7 @@ int check_run(const void* q, const void* k_cache, const void* v_cache, const int
     return VA_ERR_INVALID_ARGUMENT;
   if (!isfinite(*sm_scale)) return VA_ERR_INVALID_ARGUMENT;
   if (*sm_scale <= 0.f) *sm_scale = 1.0f / sqrtf((float)head_dim);
+  if (!isfinite(*sm_scale * k_scale * 1.4426950408889634f)) return VA_ERR_INVALID_ARGUMENT;
   *hd_out = hd;
   if (hd->n_items == 0) return VA_OK;
   if (!q || !k_cache || !v_cache || !kv_indptr || !kv_indices || !last_page_len || !qo_indptr ||
@@ -156,7 +158,8 @@ PartialParams make_partial(const void* q, const void* k_cache, const void* v_cac
   p.log2_page = log2_int(hd->page_size);
   p.num_pages = num_pages;
   p.scale_nat = sm_scale * k_scale;
-  p.scale_log2 = sm_scale * k_scale * 1.4426950408889634f;
+  // not 0 where the product underflows: a masked score is -inf times it
+  p.scale_log2 = fmaxf(sm_scale * k_scale * 1.4426950408889634f, FLT_MIN);
   p.v_scale = v_scale;
   p.n_items = hd->n_items;
   p.n_ctas = (int)hd->n_ctas;
