@@ -141,7 +141,7 @@ typedef struct {
                             with positions) */
     int q_fp8;           /* 1 (fp8-e4m3 caches, tcgen05 variants): run the MMAs on e4m3
                             operands (kind::f8f6f4): each query row quantised to e4m3 with
-                            its own scale amax|q| / 448, P rounded to e4m3, K / V as
+                            its own scale amax|q| / 448 (a row below 1e-30: 0), P rounded to e4m3, K / V as
                             stored -- twice the tensor rate of the default, which widens
                             K / V to f16, at coarser precision (3 mantissa bits on q and
                             P).  Against attention over the quantised query rows the LSE

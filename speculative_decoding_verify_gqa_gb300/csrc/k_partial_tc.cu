@@ -816,8 +816,11 @@ __global__ void __launch_bounds__(TcCfg<FP8, NQ, F8MMA>::THREADS, 1)
                 amax = fmax3(amax, fabsf(__uint_as_float(wb4[k] << 16)), fabsf(__uint_as_float(wb4[k] & 0xffff0000u)));
               }
             }
-            const float inv = amax > 0.f ? 448.f / amax : 1.f;
-            qsc = amax > 0.f ? amax / 448.f : 1.f;
+            // (a row below 1e-30, whose 448 / amax nears infinity, is 0 to e4m3:
+            // its scores are below 1e-25 of the scales either way)
+            const bool scaled = amax >= 1e-30f;
+            const float inv = scaled ? 448.f / amax : 1.f;
+            qsc = scaled ? amax / 448.f : 1.f;
             const int x = r & 7;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -841,7 +844,7 @@ __global__ void __launch_bounds__(TcCfg<FP8, NQ, F8MMA>::THREADS, 1)
         if (lane == 0) mbar_arrive(bar(B_Q_READY));
       }
       ++nit;
-      if constexpr (F8MMA) c = p.scale_log2 * qsc;
+      if constexpr (F8MMA) c = fmaxf(p.scale_log2 * qsc, 1.17549435e-38f);   // not 0: see scale_log2
       if (!mine) {
         u0 += 2 * g.n_tiles;
         continue;

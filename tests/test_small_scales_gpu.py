@@ -1,4 +1,4 @@
-"""Scales so small that every score is 0 to fp32: attention is the mean of the
+"""Queries and scales so small that every score is 0 to fp32: attention is the mean of the
 values that a row sees, its LSE the logarithm of their number."""
 import ctypes
 
@@ -61,6 +61,22 @@ def test_small_scales(va, kernel, form):
     opts = dict(q_fp8=True) if form == "e4m3" else {}
     for splits in (1, 0):
         out, lse, _ = dw.run(kernel=kernel, max_splits=splits, target_ctas=200, min_chunk=64, **opts)
+        _check(wl, out, lse, TOL)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", [3, 4])
+@pytest.mark.parametrize("size", [1e-28, 1e-31, 1e-37, 3e-39, 1e-40])
+def test_small_queries_with_e4m3_operands(va, kernel, size):
+    """Rows whose largest element is far below the e4m3 scale's range, zeros among them."""
+    wl = _workload(True)
+    dw = DeviceWorkload(wl)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = (torch.rand(dw.q.shape, generator=g, device="cuda") - 0.5) * 2 * size
+    q[..., ::3] = 0
+    dw.q.copy_(q.to(torch.bfloat16))
+    for splits in (1, 0):
+        out, lse, _ = dw.run(kernel=kernel, q_fp8=True, max_splits=splits, target_ctas=200, min_chunk=64)
         _check(wl, out, lse, TOL)
 
 
