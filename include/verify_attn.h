@@ -302,8 +302,8 @@ typedef struct {
  * With a plan made for RoPE, each query row is rotated at q_position[token]
  * (LLaMA rotate-half, angle position / rope_scale * rope_theta^(-2i /
  * head_dim); FlashInfer PR #286's ROPE_LLAMA at the tree positions of
- * FlashInfer issue #152) in fp32 and rounded to the MMA operand type (bf16,
- * or f16 with an fp8 cache) before Q K^T.  NULL options = verify_attn_run.
+ * FlashInfer issue #152) in fp32 and rounded to bf16 (which an fp8 cache's f16
+ * operands hold exactly) before Q K^T.  NULL options = verify_attn_run.
  * Errors: as verify_attn_run; VA_ERR_PLAN_MISMATCH when q_position is given
  * without a RoPE plan or missing with one.
  */
