@@ -677,6 +677,137 @@ int paged_kv_compact(const int32_t* accept_len, const int32_t* accepted_nodes,
                      va_kv_layout kv_layout, int32_t* kv_len_out, int* status_d, void* stream);
 
 /*
+ * Norm, rotation and append of a step's new tokens in one pass: what lies
+ * between the projection and the attention.  Row i of q / k / v (bf16,
+ * [heads, width] contiguous, rows q_stride / k_stride / v_stride elements
+ * apart: slices of one fused projection, or tensors of their own) belongs to
+ * the request with append_indptr[b] <= i < append_indptr[b + 1].
+ *
+ * Every q head is divided by its root mean square and weighted when q_weight
+ * is given, every k head when k_weight is (NULL: as it is):
+ *   x' = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)
+ * then, with positions, its first rotary_dim elements are rotated at angle
+ * positions[i] / rope_scale * rope_theta^(-2j / rotary_dim), j < rotary_dim /
+ * 2, in pairs (j, j + rotary_dim / 2) -- paged_kv_append_ex's pairing -- or
+ * (2j, 2j + 1) when interleaved.  inv_freq (host, rotary_dim / 2 doubles,
+ * finite; NULL: the formula) replaces rope_theta^(-2j / rotary_dim) /
+ * rope_scale: scaled rotations of long contexts.  The angle is exact to 2^-64
+ * of the position and 1e-9 of a radian before its sine and cosine (fp32).
+ * Everything is computed in fp32 and rounded once: q to q_out ([total_new,
+ * num_qo_heads, head_dim] bf16), k into the token's slot of k_cache, v as it is
+ * into v_cache, which are bf16, or e4m3 codes of x / k_scale and x / v_scale as
+ * paged_kv_append_ex stores them.  verify_attn_run then takes q_out with a plan
+ * without RoPE.
+ *
+ * Slots, checks and status bits are paged_kv_append's; a token that they skip
+ * leaves its row of q_out as it was.  Rows at or behind append_indptr[batch]
+ * are padding and left alone without a status bit.  q_out may be q itself when
+ * q is contiguous; it may not overlap q, k or v otherwise.  NaN and infinity
+ * go their way within their head.  All-zero options with options->eps = 0 and
+ * no weights: a bf16 HND append that also copies q.
+ * Errors: VA_ERR_INVALID_ARGUMENT (null or misaligned pointers: rows start on
+ * 16 bytes; strides below a row; eps negative; scales, theta, positions
+ * without rotary_dim or the other way round; overlap), VA_ERR_UNSUPPORTED
+ * (rotary_dim not a multiple of 16 up to head_dim), VA_ERR_CUDA.
+ */
+typedef struct {
+    const void* q_weight;    /* device [head_dim], weight_dtype, or NULL */
+    const void* k_weight;
+    va_dtype weight_dtype;   /* VA_BF16 or VA_F32 */
+    float weight_offset;     /* added to every weight (1: weights stored around 0) */
+    float eps;               /* >= 0, finite */
+    const int32_t* positions; /* device [total_new], or NULL: no rotation */
+    int rotary_dim;          /* elements of a head that are rotated; 0 without positions */
+    int interleaved;         /* 1: pairs of neighbours */
+    float rope_theta;        /* > 0, finite (unless inv_freq) */
+    float rope_scale;        /* > 0, finite; 0 means 1 */
+    const double* inv_freq;  /* HOST [rotary_dim / 2], or NULL */
+    float k_scale, v_scale;  /* e4m3 cache: > 0, finite */
+    va_kv_layout kv_layout;
+    int head_dim_v;          /* elements of a V row, 64 or 128; 0 means head_dim */
+    int reserved[4];         /* must be zero */
+} va_qkv_options_t;
+int paged_qkv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, const int32_t* append_indptr, const int32_t* kv_indptr,
+                     const int32_t* kv_indices, const int32_t* last_page_len, void* q_out, void* k_cache,
+                     void* v_cache, int batch, int num_qo_heads, int num_kv_heads, int head_dim,
+                     int page_size, int num_pages, va_dtype kv_dtype, int64_t total_new,
+                     const va_qkv_options_t* options, int* status_d, void* stream);
+
+/*
+ * Attention weight that each cached key receives from a step's queries, summed
+ * over the queries and over the query heads of its KV head: what eviction goes
+ * by.  For key j of request b and KV head h,
+ *   w[j] = base + sum_t sum_g exp(s(t, g, j) - lse[t, g])
+ * over the query tokens t that see j, s and what they see as in
+ * verify_attn_run (the same q, k_cache, tables, mask, sm_scale, k_scale; a plan
+ * with RoPE or e4m3 queries has no counterpart: give the rotated q), and lse
+ * [total_qo, num_qo_heads] fp32 that call's result.  base = decay * w[j] for
+ * the keys of the prefix (decay 0: the old value is not read), 0 for the
+ * step's own L_b keys.
+ *
+ * key_weights: fp32, one per cache row in the cache's order of rows,
+ * [num_pages, num_kv_heads, page_size] (HND) or [num_pages, page_size,
+ * num_kv_heads] (NHD), updated in place.  Slots that no request's keys lie in
+ * are not touched.  Requests that share pages are not supported (their sums
+ * for the shared keys would race).
+ *
+ * accept_len / accepted_nodes (both or neither; verify_accept_greedy's or
+ * verify_accept_sample's results for this step; mask and mask_indptr must then
+ * be NULL): only the accepted nodes' queries count -- each sees the prefix and
+ * the path up to itself -- and the key of node accepted_nodes[qo_indptr[b] + k]
+ * is weighed in the slot of position prefix + k, where paged_kv_compact, called
+ * next with the same tables, moves the key.  Slots of the other drafts are
+ * not touched.
+ *
+ * A query whose lse is -inf saw nothing and counts nothing; NaN in lse, q or a
+ * key makes the weights NaN of the keys seen with it.  Masked keys may hold
+ * anything.  A request whose tables or path are invalid is skipped with
+ * VA_DEV_BAD_TABLE, a key whose page lies outside the pool with VA_DEV_BAD_PAGE
+ * (status_d, nullable).  Each sum is made in fp32 in a fixed order.  No
+ * workspace; num_sms <= 0 queries the current device.
+ * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED, VA_ERR_CUDA.
+ */
+int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* kv_indptr,
+                            const int32_t* kv_indices, const int32_t* last_page_len,
+                            const int32_t* qo_indptr, const uint8_t* mask, const int32_t* mask_indptr,
+                            const int32_t* accept_len, const int32_t* accepted_nodes, const float* lse,
+                            float* key_weights, int64_t total_qo, int batch, int num_qo_heads,
+                            int num_kv_heads, int head_dim, int page_size, int num_pages,
+                            va_dtype kv_dtype, va_kv_layout kv_layout, int mask_layout, float sm_scale,
+                            float k_scale, float decay, int* status_d, int num_sms, void* stream);
+
+/*
+ * Eviction from the paged cache by attention weight.  Of request b's kv_len_b
+ * keys, every layer and KV head keeps min(keep_len[b], kv_len_b): the first
+ * `sinks`, then the last `recent` (as many of both as keep_len leaves room
+ * for), then of the keys between them those with the largest key_weights -- the
+ * lower position among equal ones; -0 equals 0, NaN counts as largest.  They
+ * move, bit for bit and in place, to the front in their order: the k-th
+ * survivor's K and V rows and its weight to position k.  Slots past them, and
+ * requests with keep_len[b] >= kv_len_b, are left as they are.  kv_len_out
+ * (nullable, [batch]) receives the new lengths; the pages past them are free.
+ * Keys keep the rotation that they were stored with, so the queries' positions
+ * go on counting.
+ *
+ * key_weights [num_layers, ...] as verify_attn_key_weights writes them, k_cache
+ * / v_cache [num_layers, num_pages, ...] as for paged_kv_compact; the three
+ * pools do not overlap.  keep_len: device [batch], >= 0.  max_kv_len: an upper
+ * bound of the requests' lengths, at most 524288.  A request that exceeds it,
+ * or whose tables are invalid, is skipped with VA_DEV_BAD_TABLE, one that lists
+ * a page outside the pool with VA_DEV_BAD_PAGE (status_d, nullable); kv_len_out
+ * then receives the unchanged length.  Requests that share pages are not
+ * supported.  No workspace; num_sms <= 0 queries the current device.
+ * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED, VA_ERR_CUDA.
+ */
+int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* kv_indptr,
+                   const int32_t* kv_indices, const int32_t* last_page_len, void* k_cache, void* v_cache,
+                   int num_layers, int batch, int num_kv_heads, int head_dim, int head_dim_v,
+                   int page_size, int num_pages, va_dtype kv_dtype, va_kv_layout kv_layout,
+                   int64_t max_kv_len, int sinks, int recent, int32_t* kv_len_out, int* status_d,
+                   int num_sms, void* stream);
+
+/*
  * verify_attn_run for callers that cannot allocate device memory.
  *
  * No page describes this entry point; it exists for callers that may not

@@ -37,6 +37,7 @@ __all__ = [
     "verify_attn_shared_groups", "verify_attn_plan_shared_bounds", "verify_attn_plan_shared_host",
     "verify_attn_plan_shared",
     "verify_accept_greedy", "verify_accept_sample", "paged_kv_compact",
+    "paged_qkv_append", "verify_attn_key_weights", "paged_kv_evict",
     "status_string", "num_sms", "KV_BF16", "KV_FP8_E4M3", "library_path",
 ]
 
@@ -82,6 +83,17 @@ class AppendOptions(ctypes.Structure):
                 ("positions", ctypes.c_void_p), ("rope_theta", ctypes.c_float),
                 ("rope_scale", ctypes.c_float), ("head_dim_v", ctypes.c_int),
                 ("reserved", ctypes.c_int * 3)]
+
+
+class QkvOptions(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("weight_dtype", ctypes.c_int), ("weight_offset", ctypes.c_float),
+                ("eps", ctypes.c_float), ("positions", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("rope_theta", ctypes.c_float), ("rope_scale", ctypes.c_float),
+                ("inv_freq", ctypes.c_void_p), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float), ("kv_layout", ctypes.c_int),
+                ("head_dim_v", ctypes.c_int), ("reserved", ctypes.c_int * 4)]
 
 
 class StepOffsets(ctypes.Structure):
@@ -150,6 +162,12 @@ def lib():
                                        P, P, P, P, P, i32, P]),
         "paged_kv_compact": (i32, [P, P, P, i64, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32,
                                    i32, P, P, P]),
+        "paged_qkv_append": (i32, [P, i64, P, i64, P, i64, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32,
+                                   i32, i64, P, P, P]),
+        "verify_attn_key_weights": (i32, [P, P, P, P, P, P, P, P, P, P, P, P, i64, i32, i32, i32, i32, i32,
+                                          i32, i32, i32, i32, f32, f32, f32, P, i32, P]),
+        "paged_kv_evict": (i32, [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, i64, i32,
+                                 i32, P, P, i32, P]),
         "verify_attn_merge": (i32, [P, i32, i32, i32, P, P, P, P, sz, P]),
         "verify_attn_plan_launches": (i32, [P, Pi]),
         "verify_attn_plan_upload": (i32, [P, P, sz, P]),
@@ -995,6 +1013,176 @@ def paged_kv_compact(accept_len, accepted_nodes, qo_indptr, kv_indptr, kv_indice
     _check("paged_kv_compact", rc)
 
 
+def _token_rows(t, name, heads, width, total, dev):
+    """(address, elements between rows) of [total, heads, width] bf16 rows that may lie apart."""
+    if t.dtype is not torch.bfloat16 or t.shape != (total, heads, width) or t.get_device() != dev:
+        raise ValueError("%s must be a [%d, %d, %d] bfloat16 tensor on cuda:%d" % (name, total, heads, width, dev))
+    if t.is_contiguous():
+        return t.data_ptr(), heads * width
+    rows, head, col = t.stride()
+    if (col != 1 and width > 1) or (head != width and heads > 1):
+        raise ValueError("%s must have contiguous heads" % name)
+    return t.data_ptr(), (heads * width if total <= 1 else rows)
+
+
+def _cache_shape(k_cache, v_cache, layout):
+    """(num_pages, page_size, num_kv_heads, head_dim, head_dim_v) of one layer's pools."""
+    k_shape = k_cache.shape
+    if len(k_shape) != 4 or v_cache.shape[:-1] != k_shape[:-1]:
+        raise ValueError("k_cache / v_cache must be pools [pages, ...] of like shape")
+    if k_cache.dtype not in _CACHE_CODES:
+        raise ValueError("k_cache / v_cache must be bfloat16 or float8_e4m3fn")
+    pages, a, c, d = k_shape
+    return (pages, a, c, d, v_cache.shape[-1]) if layout == LAYOUT_NHD else (pages, c, a, d, v_cache.shape[-1])
+
+
+def paged_qkv_append(q, k, v, append_indptr, kv_indptr, kv_indices, last_page_len, k_cache, v_cache,
+                     q_weight=None, k_weight=None, weight_offset=0.0, eps=1e-6, positions=None,
+                     rope_theta=10000.0, rope_scale=1.0, rotary_dim=None, interleaved=False,
+                     inv_freq=None, k_scale=None, v_scale=None, kv_layout="hnd", q_out=None,
+                     status=None, stream=None):
+    """Norm and rotation of new queries and keys and their append (see
+    include/verify_attn.h): q [total, h_q, d], k [total, h_kv, d], v [total,
+    h_kv, dv] bf16, whose rows may be slices of one projection.  Heads of q / k
+    are divided by their root mean square and multiplied by q_weight / k_weight
+    + weight_offset ([d] bf16 or fp32; None: not normalised), then rotated at
+    positions ([total] int32; None: not rotated), the first rotary_dim (None:
+    all) elements of each, at rope_theta / rope_scale's frequencies or at
+    inv_freq ([rotary_dim / 2], on the host).  k and v go to their cache slots,
+    quantised by k_scale / v_scale into an fp8 cache.  Returns q as bf16
+    [total, h_q, d], in q_out when given.  All on the current device."""
+    dev = _current(k_cache, "k_cache")
+    layout = _LAYOUTS[kv_layout]
+    pages, page_size, h_kv, d, dv = _cache_shape(k_cache, v_cache, layout)
+    code = _CACHE_CODES[k_cache.dtype]
+    if code == KV_FP8_E4M3 and (k_scale is None or v_scale is None):
+        raise ValueError("an fp8 cache needs k_scale and v_scale")
+    if q.dim() != 3:
+        raise ValueError("q must be [total, heads, head_dim]")
+    total, h_q = q.shape[0], q.shape[1]
+    batch, i32 = append_indptr.shape[0] - 1, torch.int32
+    qp, qs = _token_rows(q, "q", h_q, d, total, dev)
+    kp, ks = _token_rows(k, "k", h_kv, d, total, dev)
+    vp, vs = _token_rows(v, "v", h_kv, dv, total, dev)
+    if q_out is None:
+        q_out = torch.empty((total, h_q, d), dtype=torch.bfloat16, device=q.device)
+    elif q_out.shape != (total, h_q, d):
+        raise ValueError("q_out must be [%d, %d, %d]" % (total, h_q, d))
+    o = QkvOptions()
+    w = q_weight if q_weight is not None else k_weight
+    if w is not None:
+        if w.dtype not in _CODES:
+            raise ValueError("q_weight and k_weight must be bfloat16 or float32")
+        o.weight_dtype = _CODES[w.dtype]
+        o.q_weight = _arg(q_weight, "q_weight", w.dtype, d, dev)
+        o.k_weight = _arg(k_weight, "k_weight", w.dtype, d, dev)
+        o.weight_offset, o.eps = weight_offset, eps
+    freq = None
+    if positions is not None:
+        o.positions = _arg(positions, "positions", i32, total, dev)
+        o.rotary_dim = rotary_dim = d if rotary_dim is None else int(rotary_dim)
+        o.interleaved = 1 if interleaved else 0
+        if inv_freq is None:
+            o.rope_theta, o.rope_scale = rope_theta, rope_scale
+        else:
+            freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+            if freq.shape != (rotary_dim // 2,):
+                raise ValueError("inv_freq must hold %d frequencies" % (rotary_dim // 2))
+            o.inv_freq = freq.ctypes.data
+    if code == KV_FP8_E4M3:
+        o.k_scale, o.v_scale = k_scale, v_scale
+    o.kv_layout, o.head_dim_v = layout, dv
+    rc = lib().paged_qkv_append(
+        qp, qs, kp, ks, vp, vs, _arg(append_indptr, "append_indptr", i32, batch + 1, dev),
+        _arg(kv_indptr, "kv_indptr", i32, batch + 1, dev),
+        _arg(kv_indices, "kv_indices", i32, kv_indices.shape[0], dev),
+        _arg(last_page_len, "last_page_len", i32, batch, dev),
+        _arg(q_out, "q_out", torch.bfloat16, total * h_q * d, dev),
+        _arg(k_cache, "k_cache", k_cache.dtype, k_cache.numel(), dev),
+        _arg(v_cache, "v_cache", k_cache.dtype, v_cache.numel(), dev), batch, h_q, h_kv, d, page_size, pages,
+        code, total, ctypes.byref(o), _arg(status, "status", i32, 1, dev), _device_stream(stream, dev))
+    _check("paged_qkv_append", rc)
+    return q_out
+
+
+def verify_attn_key_weights(q, k_cache, kv_indptr, kv_indices, last_page_len, qo_indptr, lse, key_weights,
+                            mask=None, mask_indptr=None, accept_len=None, accepted_nodes=None,
+                            sm_scale=0.0, k_scale=1.0, decay=1.0, kv_layout="hnd", mask_layout="qlen",
+                            status=None, stream=None):
+    """Add to key_weights the attention weight that every cached key receives
+    from the step's queries (see include/verify_attn.h): q [total, h_q, d] and
+    lse [total, h_q] as verify_attn_run took and returned them, key_weights
+    fp32 [pages, h_kv, P] (or [pages, P, h_kv] with kv_layout "nhd"), updated in
+    place and returned.  The prefix's old weights are multiplied by decay first
+    (0: dropped); the step's own keys start at 0.  With accept_len /
+    accepted_nodes (an acceptance's results) only the accepted path counts, in
+    the slots where paged_kv_compact moves its keys."""
+    dev = _current(k_cache, "k_cache")
+    layout = _LAYOUTS[kv_layout]
+    pages, page_size, h_kv, d, _ = _cache_shape(k_cache, k_cache, layout)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q must be [total, heads, %d]" % d)
+    total, h_q = q.shape[0], q.shape[1]
+    if key_weights.shape != k_cache.shape[:-1]:
+        raise ValueError("key_weights must be %s" % (tuple(k_cache.shape[:-1]),))
+    if mask is not None and mask.dtype != torch.uint8:
+        raise ValueError("mask must be uint8")
+    batch, i32, f32 = qo_indptr.shape[0] - 1, torch.int32, torch.float32
+    rc = lib().verify_attn_key_weights(
+        _arg(q, "q", torch.bfloat16, total * h_q * d, dev),
+        _arg(k_cache, "k_cache", k_cache.dtype, k_cache.numel(), dev),
+        _arg(kv_indptr, "kv_indptr", i32, batch + 1, dev),
+        _arg(kv_indices, "kv_indices", i32, kv_indices.shape[0], dev),
+        _arg(last_page_len, "last_page_len", i32, batch, dev), _arg(qo_indptr, "qo_indptr", i32, batch + 1, dev),
+        None if mask is None else _arg(mask, "mask", torch.uint8, mask.numel(), dev),
+        _arg(mask_indptr, "mask_indptr", i32, batch + 1, dev), _arg(accept_len, "accept_len", i32, batch, dev),
+        _arg(accepted_nodes, "accepted_nodes", i32, total, dev), _arg(lse, "lse", f32, total * h_q, dev),
+        _arg(key_weights, "key_weights", f32, key_weights.numel(), dev), total, batch, h_q, h_kv, d, page_size,
+        pages, _CACHE_CODES[k_cache.dtype], layout, _MASK_LAYOUTS[mask_layout], sm_scale, k_scale, decay,
+        _arg(status, "status", i32, 1, dev), 0, _device_stream(stream, dev))
+    _check("verify_attn_key_weights", rc)
+    return key_weights
+
+
+def paged_kv_evict(key_weights, keep_len, kv_indptr, kv_indices, last_page_len, k_cache, v_cache,
+                   max_kv_len=None, sinks=0, recent=0, kv_layout="hnd", kv_len_out=None, status=None,
+                   stream=None):
+    """Keep keep_len [B] (int32, device) keys of every request, layer and KV
+    head -- the first `sinks`, the last `recent` and the largest key_weights
+    between them -- and move them to the front, in place (see
+    include/verify_attn.h).  key_weights, k_cache and v_cache are one layer's
+    pools or [layers, ...] pools of several.  max_kv_len bounds the requests'
+    lengths (None: the pages listed).  kv_len_out [B] int32 receives the new
+    lengths.  All on the current device."""
+    dev = _current(k_cache, "k_cache")
+    k_shape, v_shape = k_cache.shape, v_cache.shape
+    if len(k_shape) not in (4, 5) or v_shape[:-1] != k_shape[:-1] or key_weights.shape != k_shape[:-1]:
+        raise ValueError("k_cache / v_cache / key_weights must be pools of like shape")
+    if k_cache.dtype not in _CACHE_CODES:
+        raise ValueError("k_cache / v_cache must be bfloat16 or float8_e4m3fn")
+    layers = k_shape[0] if len(k_shape) == 5 else 1
+    layout = _LAYOUTS[kv_layout]
+    num_pages, a, c, d = k_shape[-4:]
+    page_size, h_kv = (a, c) if layout == LAYOUT_NHD else (c, a)
+    i32, batch = torch.int32, keep_len.shape[0]
+    if kv_indices.dim() != 1:
+        raise ValueError("kv_indices must be one-dimensional")
+    if max_kv_len is None:
+        max_kv_len = min(kv_indices.shape[0] * page_size, EVICT_MAX_KEYS)
+    rc = lib().paged_kv_evict(
+        _arg(key_weights, "key_weights", torch.float32, key_weights.numel(), dev),
+        _arg(keep_len, "keep_len", i32, batch, dev), _arg(kv_indptr, "kv_indptr", i32, batch + 1, dev),
+        _arg(kv_indices, "kv_indices", i32, kv_indices.shape[0], dev),
+        _arg(last_page_len, "last_page_len", i32, batch, dev),
+        _arg(k_cache, "k_cache", k_cache.dtype, k_cache.numel(), dev),
+        _arg(v_cache, "v_cache", k_cache.dtype, v_cache.numel(), dev), layers, batch, h_kv, d, v_shape[-1],
+        page_size, num_pages, _CACHE_CODES[k_cache.dtype], layout, max_kv_len, sinks, recent,
+        _arg(kv_len_out, "kv_len_out", i32, batch, dev), _arg(status, "status", i32, 1, dev), 0,
+        _device_stream(stream, dev))
+    _check("paged_kv_evict", rc)
+
+
+EVICT_MAX_KEYS = 1 << 19   # keys of a request that paged_kv_evict takes
 STATIC_SCRATCH_BYTES = 32 << 20
 
 

@@ -1118,6 +1118,236 @@ int paged_kv_compact(const int32_t* accept_len, const int32_t* accepted_nodes,
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }
 
+namespace {
+// whether [a, a + na) and [b, b + nb) share a byte
+bool overlap(const void* a, unsigned __int128 na, const void* b, unsigned __int128 nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na && nb && x < y + nb && y < x + na;
+}
+}  // namespace
+
+int paged_qkv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, const int32_t* append_indptr, const int32_t* kv_indptr,
+                     const int32_t* kv_indices, const int32_t* last_page_len, void* q_out, void* k_cache,
+                     void* v_cache, int batch, int num_qo_heads, int num_kv_heads, int head_dim,
+                     int page_size, int num_pages, va_dtype kv_dtype, int64_t total_new,
+                     const va_qkv_options_t* options, int* status_d, void* stream) {
+  if (!options || batch < 0 || total_new < 0) return VA_ERR_INVALID_ARGUMENT;
+  const va_qkv_options_t& o = *options;
+  int rc = check_common(num_qo_heads, num_kv_heads, head_dim, page_size, VA_DTYPE_BF16, kv_dtype);
+  if (rc) return rc;
+  for (int r : o.reserved)
+    if (r) return VA_ERR_INVALID_ARGUMENT;
+  if (o.kv_layout != VA_LAYOUT_HND && o.kv_layout != VA_LAYOUT_NHD) return VA_ERR_INVALID_ARGUMENT;
+  if (o.interleaved != 0 && o.interleaved != 1) return VA_ERR_INVALID_ARGUMENT;
+  if (o.head_dim_v < 0 || o.rotary_dim < 0) return VA_ERR_INVALID_ARGUMENT;
+  const int head_dim_v = o.head_dim_v ? o.head_dim_v : head_dim;
+  if (head_dim_v != 64 && head_dim_v != 128) return VA_ERR_UNSUPPORTED;
+  if (o.weight_dtype != VA_BF16 && o.weight_dtype != VA_F32) return VA_ERR_UNSUPPORTED;
+  if (!(isfinite(o.eps) && o.eps >= 0.f) || !isfinite(o.weight_offset)) return VA_ERR_INVALID_ARGUMENT;
+  const bool quant = kv_dtype == VA_DTYPE_FP8_E4M3;
+  if (quant && !(isfinite(o.k_scale) && o.k_scale > 0.f && isfinite(o.v_scale) && o.v_scale > 0.f))
+    return VA_ERR_INVALID_ARGUMENT;
+  if (total_new > 0 && (o.rotary_dim > 0) != (o.positions != nullptr)) return VA_ERR_INVALID_ARGUMENT;
+  if (o.rotary_dim % 16 || o.rotary_dim > head_dim) return VA_ERR_UNSUPPORTED;
+  const float rope_scale = o.rope_scale == 0.f ? 1.f : o.rope_scale;
+  if (o.rotary_dim > 0 && !o.inv_freq &&
+      !(isfinite(o.rope_theta) && o.rope_theta > 0.f && isfinite(rope_scale) && rope_scale > 0.f))
+    return VA_ERR_INVALID_ARGUMENT;
+  const int64_t q_row = (int64_t)num_qo_heads * head_dim, k_row = (int64_t)num_kv_heads * head_dim,
+                v_row = (int64_t)num_kv_heads * head_dim_v;
+  constexpr int64_t kMaxStride = (int64_t)1 << 31;
+  if (total_new > 0x7fffffffLL || q_stride > kMaxStride || k_stride > kMaxStride || v_stride > kMaxStride)
+    return VA_ERR_UNSUPPORTED;
+  if (q_stride < q_row || k_stride < k_row || v_stride < v_row || q_stride % 8 || k_stride % 8 || v_stride % 8)
+    return VA_ERR_INVALID_ARGUMENT;
+  if (total_new == 0) return VA_OK;
+  if (batch == 0) return VA_ERR_INVALID_ARGUMENT;
+  if (!q || !k || !v || !append_indptr || !kv_indptr || !kv_indices || !last_page_len || !q_out || !k_cache ||
+      !v_cache || num_pages <= 0)
+    return VA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) ||
+      !aligned16(v_cache))
+    return VA_ERR_INVALID_ARGUMENT;
+  // q_out replaces q row by row, or lies apart from what other CTAs still read
+  const unsigned __int128 n1 = (unsigned __int128)(total_new - 1);
+  const unsigned __int128 out_bytes = (n1 + 1) * q_row * 2;
+  if (!(q_out == q && q_stride == q_row) && overlap(q_out, out_bytes, q, (n1 * q_stride + q_row) * 2))
+    return VA_ERR_INVALID_ARGUMENT;
+  if (overlap(q_out, out_bytes, k, (n1 * k_stride + k_row) * 2) || overlap(q_out, out_bytes, v, (n1 * v_stride + v_row) * 2))
+    return VA_ERR_INVALID_ARGUMENT;
+  QkvParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_weight = o.q_weight;
+  p.k_weight = o.k_weight;
+  p.append_indptr = append_indptr;
+  p.kv_indptr = kv_indptr;
+  p.kv_indices = kv_indices;
+  p.last_page_len = last_page_len;
+  p.positions = o.positions;
+  p.q_out = q_out;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.status = status_d;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.total_new = total_new;
+  p.batch = batch;
+  p.h_q = num_qo_heads;
+  p.h_kv = num_kv_heads;
+  p.page_size = page_size;
+  p.log2_page = log2_int(page_size);
+  p.num_pages = num_pages;
+  p.head_dim_v = head_dim_v;
+  p.rot = o.rotary_dim;
+  p.interleaved = o.interleaved;
+  p.weight_f32 = o.weight_dtype == VA_F32;
+  p.quant = quant;
+  p.nhd = o.kv_layout == VA_LAYOUT_NHD;
+  p.weight_offset = o.weight_offset;
+  p.eps = o.eps;
+  p.k_scale = o.k_scale;
+  p.v_scale = o.v_scale;
+  for (int j = 0; 2 * j < o.rotary_dim; ++j) {
+    const double f = o.inv_freq ? o.inv_freq[j] : pow((double)o.rope_theta, -2.0 * j / o.rotary_dim) / (double)rope_scale;
+    if (!isfinite(f)) return VA_ERR_INVALID_ARGUMENT;
+    const double turns = f * 0.15915494309189533577;   // 1 / (2 pi)
+    const double part = turns - floor(turns);           // positions are whole: whole turns drop out
+    p.turn[j] = part >= 1.0 ? 0 : (uint64_t)ldexp(part, 64);
+  }
+  cudaError_t e = launch_qkv_append(p, head_dim, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
+}
+
+int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* kv_indptr,
+                            const int32_t* kv_indices, const int32_t* last_page_len,
+                            const int32_t* qo_indptr, const uint8_t* mask, const int32_t* mask_indptr,
+                            const int32_t* accept_len, const int32_t* accepted_nodes, const float* lse,
+                            float* key_weights, int64_t total_qo, int batch, int num_qo_heads,
+                            int num_kv_heads, int head_dim, int page_size, int num_pages,
+                            va_dtype kv_dtype, va_kv_layout kv_layout, int mask_layout, float sm_scale,
+                            float k_scale, float decay, int* status_d, int num_sms, void* stream) {
+  if (batch < 0 || total_qo < 0) return VA_ERR_INVALID_ARGUMENT;
+  int rc = check_common(num_qo_heads, num_kv_heads, head_dim, page_size, VA_DTYPE_BF16, kv_dtype);
+  if (rc) return rc;
+  if (kv_layout != VA_LAYOUT_HND && kv_layout != VA_LAYOUT_NHD) return VA_ERR_INVALID_ARGUMENT;
+  if (mask_layout != VA_MASK_QLEN && mask_layout != VA_MASK_FULL) return VA_ERR_INVALID_ARGUMENT;
+  if ((mask == nullptr) != (mask_indptr == nullptr) || (accept_len == nullptr) != (accepted_nodes == nullptr) ||
+      (mask && accept_len))
+    return VA_ERR_INVALID_ARGUMENT;
+  const float scale = sm_scale > 0.f ? sm_scale : 1.f / sqrtf((float)head_dim);
+  if (!(isfinite(k_scale) && k_scale > 0.f) || !isfinite(scale * k_scale) || !(isfinite(decay) && decay >= 0.f))
+    return VA_ERR_INVALID_ARGUMENT;
+  if (total_qo > 0x7fffffffLL) return VA_ERR_UNSUPPORTED;
+  if (batch == 0) return VA_OK;
+  if (!k_cache || !kv_indptr || !kv_indices || !last_page_len || !qo_indptr || !key_weights || num_pages <= 0 ||
+      (total_qo > 0 && (!q || !lse)))
+    return VA_ERR_INVALID_ARGUMENT;
+  if ((q && !aligned16(q)) || !aligned16(k_cache)) return VA_ERR_INVALID_ARGUMENT;
+  if (num_sms <= 0) {
+    rc = query_sms(&num_sms);
+    if (rc) return rc;
+  }
+  KeyWeightParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = q;
+  p.k_cache = k_cache;
+  p.kv_indptr = kv_indptr;
+  p.kv_indices = kv_indices;
+  p.last_page_len = last_page_len;
+  p.qo_indptr = qo_indptr;
+  p.mask = mask;
+  p.mask_indptr = mask_indptr;
+  p.accept_len = accept_len;
+  p.path = accepted_nodes;
+  p.lse = lse;
+  p.key_weights = key_weights;
+  p.status = status_d;
+  p.total_qo = total_qo;
+  p.batch = batch;
+  p.h_q = num_qo_heads;
+  p.h_kv = num_kv_heads;
+  p.group = num_qo_heads / num_kv_heads;
+  p.page_size = page_size;
+  p.log2_page = log2_int(page_size);
+  p.num_pages = num_pages;
+  p.nhd = kv_layout == VA_LAYOUT_NHD;
+  p.mask_full = mask_layout == VA_MASK_FULL;
+  p.scale_log2 = scale * k_scale * 1.4426950408889634f;
+  p.decay = decay;
+  cudaError_t e = launch_key_weights(p, head_dim, kv_dtype == VA_DTYPE_FP8_E4M3, num_sms,
+                                     static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
+}
+
+int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* kv_indptr,
+                   const int32_t* kv_indices, const int32_t* last_page_len, void* k_cache, void* v_cache,
+                   int num_layers, int batch, int num_kv_heads, int head_dim, int head_dim_v,
+                   int page_size, int num_pages, va_dtype kv_dtype, va_kv_layout kv_layout,
+                   int64_t max_kv_len, int sinks, int recent, int32_t* kv_len_out, int* status_d,
+                   int num_sms, void* stream) {
+  if (batch < 0 || num_layers <= 0 || head_dim_v < 0 || max_kv_len < 0 || sinks < 0 || recent < 0)
+    return VA_ERR_INVALID_ARGUMENT;
+  int rc = check_common(num_kv_heads, num_kv_heads, head_dim, page_size, VA_DTYPE_BF16, kv_dtype);
+  if (rc) return rc;
+  if (head_dim_v == 0) head_dim_v = head_dim;
+  if (head_dim_v != 64 && head_dim_v != 128) return VA_ERR_UNSUPPORTED;
+  if (kv_layout != VA_LAYOUT_HND && kv_layout != VA_LAYOUT_NHD) return VA_ERR_INVALID_ARGUMENT;
+  if (max_kv_len > kEvictMaxKeys) return VA_ERR_UNSUPPORTED;
+  constexpr int kMaxCluster = 8;
+  const int64_t units = (int64_t)num_layers * batch;   // (both below 2^31)
+  if (units > 0x7fffffffLL / kMaxCluster / num_kv_heads) return VA_ERR_UNSUPPORTED;
+  if (batch == 0) return VA_OK;
+  if (!key_weights || !keep_len || !kv_indptr || !last_page_len || !k_cache || !v_cache || num_pages <= 0 ||
+      (max_kv_len > 0 && !kv_indices))
+    return VA_ERR_INVALID_ARGUMENT;
+  if (!aligned16(k_cache) || !aligned16(v_cache) || reinterpret_cast<uintptr_t>(key_weights) % 4)
+    return VA_ERR_INVALID_ARGUMENT;
+  EvictParams p;
+  memset(&p, 0, sizeof(p));
+  p.key_weights = key_weights;
+  p.keep_len = keep_len;
+  p.kv_indptr = kv_indptr;
+  p.kv_indices = kv_indices;
+  p.last_page_len = last_page_len;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.kv_len_out = kv_len_out;
+  p.status = status_d;
+  p.batch = batch;
+  p.layers = num_layers;
+  p.h_kv = num_kv_heads;
+  p.page_size = page_size;
+  p.log2_page = log2_int(page_size);
+  p.num_pages = num_pages;
+  const int es = kv_dtype == VA_DTYPE_FP8_E4M3 ? 1 : 2;
+  p.k_chunks = head_dim * es / 16;
+  p.v_chunks = head_dim_v * es / 16;
+  p.nhd = kv_layout == VA_LAYOUT_NHD;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.max_kv_len = (int)max_kv_len;
+  p.words = (int)((max_kv_len + 31) / 32);
+  // all three move in place: no pool may reach into another
+  const unsigned __int128 rows = (unsigned __int128)num_layers * num_kv_heads * page_size * num_pages;
+  if (overlap(k_cache, rows * p.k_chunks * 16, v_cache, rows * p.v_chunks * 16) ||
+      overlap(key_weights, rows * 4, k_cache, rows * p.k_chunks * 16) ||
+      overlap(key_weights, rows * 4, v_cache, rows * p.v_chunks * 16))
+    return VA_ERR_INVALID_ARGUMENT;
+  if (num_sms <= 0) {
+    rc = query_sms(&num_sms);
+    if (rc) return rc;
+  }
+  p.cluster = 1;
+  while (p.cluster < kMaxCluster && units * num_kv_heads * p.cluster * 2 <= 4LL * num_sms) p.cluster *= 2;
+  cudaError_t e = launch_evict(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
+}
+
 int paged_kv_append(const void* k_new, const void* v_new, const int32_t* append_indptr,
                     const int32_t* kv_indptr, const int32_t* kv_indices,
                     const int32_t* last_page_len, void* k_cache, void* v_cache, int batch,

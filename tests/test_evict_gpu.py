@@ -1,0 +1,175 @@
+"""GPU test of paged_kv_evict against a host copy of all three pools: the
+survivors at the front in their order bit for bit, every other slot as it was."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import budget
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def va():
+    import __graft_entry__
+    __graft_entry__.build()
+    import speculative_decoding_verify_gqa_gb300 as m
+    return m
+
+
+class Case:
+    def __init__(self, seed, lens, keep, sinks=0, recent=0, page=16, h=2, d=64, dv=None, fp8=False, nhd=False,
+                 layers=None, values="spread"):
+        rng = np.random.default_rng(seed)
+        need = [-(-n // page) for n in lens]
+        pages = sum(need) + 2
+        self.ids = rng.permutation(pages)[:max(1, sum(need))].astype(np.int32)
+        self.kvp = np.concatenate([[0], np.cumsum(need)]).astype(np.int32)
+        self.last = np.array([(n - 1) % page + 1 if n else 0 for n in lens], np.int32)
+        self.keep = np.array(keep, np.int32)
+        self.lens, self.sinks, self.recent, self.page, self.nhd, self.layers = lens, sinks, recent, page, nhd, layers
+        mid = (page, h) if nhd else (h, page)
+        shape = (() if layers is None else (layers,)) + (pages,) + mid
+        es = 1 if fp8 else 2
+        self.k, self.v = (rng.integers(0, 256, shape + (w * es,), dtype=np.uint8) for w in (d, dv or d))
+        w = rng.lognormal(0, 2, shape)
+        if values == "equal":
+            w[:] = 1.5
+        elif values == "few":
+            w = rng.integers(0, 4, shape) * 0.25 - 0.25
+            w[w == 0] *= rng.choice([-1.0, 1.0], w[w == 0].shape)     # -0 equals 0
+        elif values == "special":
+            pick = rng.integers(0, 8, shape)
+            w = np.select([pick == 0, pick == 1, pick == 2, pick == 3], [np.nan, np.inf, -np.inf, -w], w)
+        elif values == "close":
+            w = (1 + rng.integers(0, 3000, shape) * 2.0 ** -23)
+        self.w = w.astype(np.float32)
+        self.dt = torch.float8_e4m3fn if fp8 else torch.bfloat16
+        t = lambda x: torch.from_numpy(x.copy()).cuda()  # noqa: E731
+        self.dev = dict(w=t(self.w), keep=t(self.keep), kvp=t(self.kvp), ids=t(self.ids), last=t(self.last),
+                        k=t(self.k).view(self.dt), v=t(self.v).view(self.dt))
+        self.kv_len = torch.full((len(lens),), -7, dtype=torch.int32, device="cuda")
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run(self, va, **kw):
+        x = self.dev
+        args = dict(sinks=self.sinks, recent=self.recent, kv_layout="nhd" if self.nhd else "hnd",
+                    kv_len_out=self.kv_len, status=self.status)
+        args.update(kw)
+        va.paged_kv_evict(x["w"], x["keep"], x["kvp"], x["ids"], x["last"], x["k"], x["v"], **args)
+
+    def expect(self, skip=()):
+        out = []
+        w5 = self.w if self.layers is not None else self.w[None]
+        moves = []
+        for layer in range(w5.shape[0]):
+            for b in range(len(self.lens)):
+                if b in skip:
+                    continue
+                pages, slots = budget.slots_of(self.kvp, self.ids, self.last, self.page, b)
+                for h in range(w5.shape[2] if not self.nhd else w5.shape[3]):
+                    at = [(layer, p, s, h) if self.nhd else (layer, p, h, s) for p, s in zip(pages, slots)]
+                    rows = budget.survivors(np.array([w5[a] for a in at]), int(self.keep[b]), self.sinks, self.recent)
+                    moves += [(at[j], at[i]) for i, j in enumerate(rows)]
+        for x in (self.k, self.v, self.w):
+            y = x.copy()
+            x5, y5 = (x, y) if self.layers is not None else (x[None], y[None])
+            for s, d in moves:
+                y5[d] = x5[s]
+            out.append(y)
+        return out
+
+    def check(self, skip=(), status=0):
+        torch.cuda.synchronize()
+        assert int(self.status) == status
+        k, v, w = self.expect(skip)
+        assert np.array_equal(self.dev["k"].view(torch.uint8).cpu().numpy(), k)
+        assert np.array_equal(self.dev["v"].view(torch.uint8).cpu().numpy(), v)
+        assert np.array_equal(self.dev["w"].cpu().numpy().view(np.uint32), w.view(np.uint32))
+        want = [n if b in skip else min(n, int(c)) for b, (n, c) in enumerate(zip(self.lens, self.keep))]
+        assert self.kv_len.tolist() == want
+
+
+CASES = [
+    dict(lens=[100], keep=[50]),
+    dict(lens=[1], keep=[1]),
+    dict(lens=[1, 0, 2], keep=[0, 0, 1]),
+    dict(lens=[33, 700, 64, 5], keep=[32, 100, 64, 9], sinks=4, recent=16, h=3),
+    dict(lens=[257, 31], keep=[128, 30], sinks=1, recent=300, page=1, nhd=True, d=128),
+    dict(lens=[513], keep=[3], sinks=4, recent=4),
+    dict(lens=[513], keep=[6], sinks=4, recent=4),
+    dict(lens=[2000, 900], keep=[1999, 1], page=32, fp8=True, nhd=True, d=128, dv=64, layers=2),
+    dict(lens=[300], keep=[100], values="equal", sinks=3),
+    dict(lens=[1000, 450], keep=[333, 200], values="few", recent=7, page=8),
+    dict(lens=[1000, 450], keep=[400, 100], values="special", sinks=2, recent=7, page=64),
+    dict(lens=[1200], keep=[600], values="close", h=1, d=128, fp8=True),
+    dict(lens=[40] * 40, keep=[13] * 40, layers=3, h=2),
+    dict(lens=[3000], keep=[0]),
+    dict(lens=[9000], keep=[4500], sinks=4, recent=100, h=1, page=128),
+]
+
+
+@pytest.mark.parametrize("n", range(len(CASES)))
+def test_against_definition(va, n):
+    c = Case(n, **CASES[n])
+    c.run(va)
+    c.check()
+
+
+def test_skipped_requests(va):
+    """Lengths past max_kv_len, bad pages and bad tables leave their request alone."""
+    c = Case(100, [90, 300, 40], [20, 20, 20])
+    c.run(va, max_kv_len=299)
+    c.check(skip=[1], status=2)
+    c = Case(101, [90, 300, 40], [20, 20, 20])
+    c.dev["ids"][int(c.kvp[1])] = -1
+    c.run(va)
+    c.check(skip=[1], status=1)
+    c = Case(102, [90, 300, 40], [20, 20, 20])
+    c.dev["keep"][2] = -1
+    c.run(va)
+    c.check(skip=[2], status=2)
+
+
+def test_twice_and_graph(va):
+    """A graph captured over one pool, replayed after the tables have moved on."""
+    c = Case(103, [400, 77], [200, 50], sinks=2, recent=8)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run(va, max_kv_len=1000)
+    g.replay()
+    c.check()
+    k, v, w = c.expect()
+    c.k, c.v, c.w = k, v, w
+    c.lens, c.keep = [200, 50], np.array([60, 50], np.int32)
+    page = c.page
+    # the same pages listed, fewer keys: pages past the new length are dropped
+    need = [-(-n // page) for n in c.lens]
+    c.ids = np.concatenate([c.ids[c.kvp[b]:c.kvp[b] + need[b]] for b in range(2)]).astype(np.int32)
+    c.kvp = np.concatenate([[0], np.cumsum(need)]).astype(np.int32)
+    c.last = np.array([(n - 1) % page + 1 for n in c.lens], np.int32)
+    c.dev["ids"][:len(c.ids)] = torch.from_numpy(c.ids)
+    for n in ("kvp", "last", "keep"):
+        c.dev[n].copy_(torch.from_numpy(getattr(c, n)))
+    g.replay()
+    c.check()
+
+
+def test_far_rows(va):
+    """Rows of the last layer lie behind 2^31 bytes and 2^31 elements."""
+    layers, pages, h, P, d = 3, 45000, 2, 64, 128
+    k = torch.zeros((layers, pages, h, P, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    w = torch.zeros((layers, pages, h, P), device="cuda")
+    at = pages - 2
+    row = torch.arange(P, device="cuda").float()
+    k[2, at] = row[:, None].to(torch.bfloat16)
+    v[2, at] = -row[:, None].to(torch.bfloat16)
+    w[2, at] = row % 7
+    i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    va.paged_kv_evict(w, i([20]), i([0, 1]), i([at]), i([P]), k, v)
+    rows = budget.survivors((np.arange(P) % 7).astype(np.float32), 20, 0, 0)
+    for x, sign in ((k, 1), (v, -1)):
+        assert x[2, at, 0, :20, 0].float().tolist() == [float(sign * r) for r in rows]
+        assert x[2, at, 1, 20:, 5].float().tolist() == [float(sign * r) for r in range(20, P)]
+        assert int((x[1] != 0).any()) == 0
