@@ -9,9 +9,32 @@
 // key prefix + k is read from slot prefix + path[k] and weighed in slot
 // prefix + k, where compaction moves it.
 //
-// One thread per key: its row of K in registers, the queries broadcast from
-// shared memory, so the sum over the queries never crosses threads and its
-// order is fixed.
+// The product is taken transposed, S = K Q^T on the 5th-generation tensor cores
+// (M = 128 keys, N = up to 128 query rows, accumulators in tensor memory): a
+// key is a lane of tensor memory, so one thread holds a key and adds up its
+// own weight -- the sum never crosses threads, needs no atomics, and its order
+// is fixed.  K is read once and V not at all: HBM bounds the step of a serving
+// batch, the tensor cores and the SFU's 2^x (one for each pair) a prompt's.
+//
+// A unit is one or two tiles of 128 keys of one (request, KV head); the CTA's
+// roles walk the same sequence of units (one CTA per SM):
+//  * 4 loader warps gather K rows by 16-byte asynchronous copies into the
+//    128-byte-swizzled operand layout (any page size and layout; a tile's rows
+//    need not be neighbours), and the query rows of 128-row chunks the same
+//    way, up to three such loads under way.  Their completion is passed on by a
+//    proxy fence and an mbarrier.  e4m3 rows are widened to f16 between a raw
+//    buffer and the operand (exact), and bf16 queries with them, as the
+//    attention kernels do;
+//  * one thread issues tcgen05.mma: for each chunk of rows and tile of keys 4 or
+//    8 steps of K = 16 into one of two buffers of the tile;
+//  * 4 warps per tile take 2^(s c - lse log2 e) of their lane's columns and add.
+// Chunks of a (request, head) of up to 256 rows stay in shared memory from unit
+// to unit.  Longer ones (prompts) are streamed, from the first chunk that sees
+// the unit's keys on.
+//
+// Units are dealt in runs of neighbours where rows are few: all cost the same
+// bytes.  Where a request has more than 256 rows they are sorted by their number
+// of chunks and dealt back and forth over the CTAs, the long ones first.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -21,16 +44,35 @@
 #include "../../include/verify_attn.h"
 #include "va_device.cuh"
 #include "va_kernels.h"
+#include "va_tc.cuh"
 
 namespace va {
 namespace {
 
-constexpr int kTile = 128;   // keys of a CTA
-constexpr int kQRows = 16;   // query rows in shared memory
+constexpr int kTile = 128;    // keys of a tile, query rows of a chunk
+constexpr int kEpiWarps = 8;  // 4 for each of the unit's tiles
+constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kLoadWarp + 4, kThreads = 32 * (kMmaWarp + 1);
+constexpr int kList = 512;    // units (of all heads) that are sorted
+constexpr int kResident = 2;  // chunks that stay in shared memory
+constexpr int kFlight = 3;    // loads under way per loader thread
+
+template <int D, bool FP8>
+struct Cfg {
+  static constexpr int OP = kTile * D * 2;         // one operand tile: [D / 64 halves][128 rows][128 bytes]
+  static constexpr int RAW = FP8 ? kTile * D : 0;  // e4m3 rows as they are
+  static constexpr int NK = FP8 ? 3 : 4;           // K operand tiles
+  static constexpr int OFF_Q = 0, OFF_K = 2 * OP, OFF_RAW = OFF_K + NK * OP, OFF_L2 = OFF_RAW + kFlight * RAW,
+                       OFF_LIST = OFF_L2 + 2 * kTile * 4, OFF_BAR = OFF_LIST + kList * 8, SMEM = OFF_BAR + 256;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(kList * 12 <= NK * OP, "the unsorted list lies in the K tiles");
+};
+
+enum { B_KF = 0, B_KE = 4, B_QF = 8, B_QE = 10, B_SF = 12, B_SE = 16, B_DONE = 20, B_COUNT = 21 };
 
 struct Request {
-  int o, L, n, pg0, npg;  // first query row, query tokens, those counted, page table
-  int pre, keys;          // prefix length, keys weighed (0: nothing to do)
+  int o, L, n, pg0;  // first query row, query tokens, those counted, page table
+  int pre, keys;     // prefix length, keys weighed (0: nothing to do)
+  int rows, chunks;  // n * group query rows, in chunks
   bool bad;
 };
 
@@ -39,131 +81,574 @@ __device__ __forceinline__ Request load_request(const KeyWeightParams& p, int b)
   r.o = p.qo_indptr[b];
   r.L = p.qo_indptr[b + 1] - r.o;
   r.pg0 = p.kv_indptr[b];
-  r.npg = p.kv_indptr[b + 1] - r.pg0;
-  const int lpl = r.npg > 0 ? p.last_page_len[b] : 1;
+  const int npg = p.kv_indptr[b + 1] - r.pg0;
+  const int lpl = npg > 0 ? p.last_page_len[b] : 1;
   r.n = p.accept_len ? p.accept_len[b] : r.L;
-  const long long len = r.npg > 0 ? (long long)(r.npg - 1) * p.page_size + lpl : 0, pre = len - r.L;
-  r.bad = r.o < 0 || r.L < 0 || (long long)r.o + r.L > p.total_qo || r.npg < 0 || r.pg0 < 0 || lpl < 1 ||
-          lpl > p.page_size || pre < 0 || len > 0x7fffffffLL || r.n < 0 || r.n > r.L;
+  const long long len = npg > 0 ? (long long)(npg - 1) * p.page_size + lpl : 0, pre = len - r.L;
+  r.bad = r.o < 0 || r.L < 0 || (long long)r.o + r.L > p.total_qo || npg < 0 || r.pg0 < 0 || lpl < 1 ||
+          lpl > p.page_size || pre < 0 || len > 0x7fffffffLL - 2 * kTile || r.n < 0 || r.n > r.L ||
+          (long long)r.n * p.group > 0x7fffffffLL - kTile;
   r.pre = r.bad ? 0 : (int)pre;
   r.keys = r.bad ? 0 : r.pre + r.n;
+  r.rows = r.bad ? 0 : r.n * p.group;
+  r.chunks = (r.rows + kTile - 1) / kTile;
   return r;
 }
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(kTile) verify_attn_key_weights_kernel(const KeyWeightParams p) {
-  __shared__ __align__(16) float qs[kQRows][D];
-  __shared__ float l2[kQRows];
-  const int tid = threadIdx.x;
-  grid_dependency_wait();
-  grid_dependents_launch();
-  long long unit = 0;  // of (request, head, tile)
-  for (int b = 0; b < p.batch; ++b) {
-    const Request rq = load_request(p, b);
-    int bad = rq.bad;
-    if (!bad && p.accept_len)
-      for (int k = tid; k < rq.n; k += kTile) {
+// What the roles share of the schedule.
+struct Sched {
+  unsigned long long tiles1, tiles2;  // tiles of 128 keys, units of 256, of all heads
+  int most_rows, entries;             // rows of the longest request, units of one head
+  int kt;                             // tiles of a unit
+  int sorted;                         // units are dealt from the sorted list
+  int b0;                             // runs: first request, and units to skip there
+  long long off, count;
+};
+
+// One role's walk over the CTA's units; all lanes of a warp take the same steps.
+struct Walk {
+  const KeyWeightParams& p;
+  const Sched& s;
+  const int2* list;
+  Request rq;
+  long long at, left;
+  int b, h, tile, tiles;
+  bool fresh, last;  // first / last unit of this (request, head) in a row
+  bool first;
+
+  __device__ Walk(const KeyWeightParams& p_, const Sched& s_, const int2* l) : p(p_), s(s_), list(l), at(0), left(s_.count), b(-1), h(0), tile(0), tiles(0), first(true) {}
+
+  __device__ void enter(int nb) {
+    b = nb;
+    rq = load_request(p, b);
+    if (!rq.bad && p.accept_len) {
+      bool bad = false;
+      for (int k = threadIdx.x & 31; k < rq.n; k += 32) {
         const int node = p.path[rq.o + k];
         bad |= node >= rq.L || node < k || (k > 0 && p.path[rq.o + k - 1] >= node);
       }
-    bad = __syncthreads_or(bad);
-    if (bad) {
-      if (blockIdx.x == 0 && tid == 0 && p.status) atomicOr(p.status, VA_DEV_BAD_TABLE);
-      continue;
+      rq.bad = __any_sync(0xffffffffu, bad);
     }
-    const int tiles = (rq.keys + kTile - 1) / kTile;
-    const long long units = (long long)tiles * p.h_kv;
-    long long u = (long long)blockIdx.x - unit % gridDim.x;
-    if (u < 0) u += gridDim.x;
-    unit += units;
-    for (; u < units; u += gridDim.x) {
-      const int h = (int)(u / tiles), j = (int)(u % tiles) * kTile + tid;
-      const bool live = j < rq.keys;
-      const int at = live ? (j < rq.pre || !p.accept_len ? j : rq.pre + min(max(p.path[rq.o + j - rq.pre], 0), rq.L - 1)) : 0;
-      auto row_of = [&](int pos) -> long long {
-        const unsigned page = (unsigned)p.kv_indices[rq.pg0 + (pos >> p.log2_page)];
-        if (page >= (unsigned)p.num_pages) return -1;
-        const long long slot = pos & (p.page_size - 1);
-        return p.nhd ? ((long long)page * p.page_size + slot) * p.h_kv + h
-                     : ((long long)page * p.h_kv + h) * p.page_size + slot;
-      };
-      const long long src = live ? row_of(at) : -1, dst = live ? row_of(j) : -1;
-      if (live && (src < 0 || dst < 0) && p.status) atomicOr(p.status, VA_DEV_BAD_PAGE);
-      const bool ok = src >= 0 && dst >= 0;
-      uint32_t k[D / 2];  // bf16 pairs
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        if constexpr (FP8) {
-          const uint2 x = ok ? static_cast<const uint2*>(p.k_cache)[src * (D / 8) + c] : make_uint2(0, 0);
-          k[4 * c] = e4m3x2_to_bf16x2((uint16_t)x.x);
-          k[4 * c + 1] = e4m3x2_to_bf16x2((uint16_t)(x.x >> 16));
-          k[4 * c + 2] = e4m3x2_to_bf16x2((uint16_t)x.y);
-          k[4 * c + 3] = e4m3x2_to_bf16x2((uint16_t)(x.y >> 16));
-        } else {
-          const uint4 x = ok ? static_cast<const uint4*>(p.k_cache)[src * (D / 8) + c] : make_uint4(0, 0, 0, 0);
-          k[4 * c] = x.x;
-          k[4 * c + 1] = x.y;
-          k[4 * c + 2] = x.z;
-          k[4 * c + 3] = x.w;
+    if (rq.bad) rq.rows = rq.chunks = 0;   // (its units are walked over)
+    const int u = kTile * s.kt;
+    tiles = (rq.keys + u - 1) / u;
+  }
+  __device__ bool next() {
+    if (s.sorted) {
+      const long long u = at * gridDim.x + ((at & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      ++at;
+      if (u >= s.count) return false;
+      const int2 e = list[u / p.h_kv];
+      h = (int)(u % p.h_kv);
+      if (e.x != b) enter(e.x);
+      tile = e.y;
+      fresh = last = true;
+      return true;
+    }
+    if (left-- <= 0) return false;
+    if (first) {
+      first = false;
+      enter(s.b0);
+      if (tiles == 0) return false;   // (tables that change during the call)
+      h = (int)(s.off / tiles);
+      tile = (int)(s.off % tiles);
+      fresh = true;
+    } else {
+      fresh = false;
+      if (++tile == tiles) {
+        tile = 0;
+        fresh = true;
+        if (++h == p.h_kv) {
+          h = 0;
+          do {
+            if (b + 1 >= p.batch) return false;   // (the same)
+            enter(b + 1);
+          } while (tiles == 0);
         }
       }
-      const int draft = j - rq.pre, len = rq.pre + rq.L;
-      float sum = 0.f;
-      for (int r0 = 0; r0 < rq.n * p.group; r0 += kQRows) {
-        const int m = min(kQRows, rq.n * p.group - r0);
-        __syncthreads();
-        for (int i = tid; i < m * (D / 8); i += kTile) {
-          const int r = i / (D / 8), c = i % (D / 8), t = (r0 + r) / p.group, g = (r0 + r) % p.group;
-          const int row = rq.o + (p.accept_len ? min(max(p.path[rq.o + t], 0), rq.L - 1) : t);
-          const uint4 x = reinterpret_cast<const uint4*>(p.q)[((long long)row * p.h_q + h * p.group + g) * (D / 8) + c];
-          const uint32_t u4[4] = {x.x, x.y, x.z, x.w};
-          for (int e = 0; e < 4; ++e) {
-            qs[r][8 * c + 2 * e] = __uint_as_float(u4[e] << 16);
-            qs[r][8 * c + 2 * e + 1] = __uint_as_float(u4[e] & 0xffff0000u);
-          }
-          if (c == 0) {
-            const float lse = p.lse[(long long)row * p.h_q + h * p.group + g];
-            l2[r] = lse == -INFINITY ? INFINITY : lse * kLog2e;  // a row that saw nothing counts nothing
-          }
-        }
-        __syncthreads();
-        for (int r = 0; r < m; ++r) {
-          const int t = (r0 + r) / p.group;
-          bool vis = draft <= t;
-          if (p.mask) {
-            vis = draft < 0;
-            if (p.mask_full || (draft >= 0 && ok)) {
-              const long long bit = p.mask_indptr[b] + (p.mask_full ? (long long)t * len + min(j, len - 1)
-                                                                    : (long long)t * rq.L + draft);
-              vis = (p.mask[bit >> 3] >> (bit & 7)) & 1;
-            }
-          }
-          float s = 0.f;
-#pragma unroll
-          for (int e = 0; e < D / 2; ++e) {
-            s = fmaf(qs[r][2 * e], __uint_as_float(k[e] << 16), s);
-            s = fmaf(qs[r][2 * e + 1], __uint_as_float(k[e] & 0xffff0000u), s);
-          }
-          if (vis) sum += ex2(fmaf(s, p.scale_log2, -l2[r]));
-        }
+    }
+    last = tile == tiles - 1 || left == 0;
+    return true;
+  }
+  __device__ int key0() const { return tile * kTile * s.kt; }
+  __device__ int tiles_here() const { return min(s.kt, (rq.keys - key0() + kTile - 1) / kTile); }
+  __device__ bool resident() const { return rq.chunks <= kResident; }
+  // chunks before this one see none of the unit's keys
+  __device__ int chunk0() const {
+    if (resident() || p.mask) return 0;
+    return (int)min((long long)max(0, key0() - rq.pre) * p.group / kTile, (long long)rq.chunks);
+  }
+  // position that key j is read from
+  __device__ int source(int j) const {
+    return !p.accept_len || j < rq.pre ? j : rq.pre + min(max(p.path[rq.o + j - rq.pre], 0), rq.L - 1);
+  }
+  __device__ int page_of(int pos) const { return p.kv_indices[rq.pg0 + (pos >> p.log2_page)]; }
+  __device__ long long row_of(int page, int pos) const {
+    if ((unsigned)page >= (unsigned)p.num_pages) return -1;
+    const long long slot = pos & (p.page_size - 1);
+    return p.nhd ? ((long long)page * p.page_size + slot) * p.h_kv + h
+                 : ((long long)page * p.h_kv + h) * p.page_size + slot;
+  }
+};
+
+__device__ __forceinline__ uint32_t op_addr(uint32_t base, int row, int chunk) {  // of a 16-byte chunk of an operand row
+  return base + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// mbar_wait by a whole warp, with one answer
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+// f16 instruction descriptor: fp32 accumulator, both operands K-major
+template <bool FP8>
+__device__ __forceinline__ uint32_t idesc_n(int n) {
+  return (1u << 4) | (FP8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(const KeyWeightParams p) {
+  using C = Cfg<D, FP8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Sched sched;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_shared;
+  volatile int* const abort_flag = &abort_shared;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = smem_u32(smem), bars = sbase + C::OFF_BAR;
+  auto bar = [&](int i) { return bars + 8 * i; };
+  float* const l2s = reinterpret_cast<float*>(smem + C::OFF_L2);
+  int2* const list = reinterpret_cast<int2*>(smem + C::OFF_LIST);
+
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(B_KF + i), 128);
+      mbar_init(bar(B_KE + i), 1);
+      mbar_init(bar(B_SF + i), 1);
+      mbar_init(bar(B_SE + i), 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_QF + i), 128);
+      mbar_init(bar(B_QE + i), 1 + kEpiWarps);
+    }
+    mbar_init(bar(B_DONE), 1);
+    abort_shared = 0;
+    sched.tiles1 = sched.tiles2 = 0;
+    sched.most_rows = sched.entries = 0;
+    mbar_fence_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(&tmem_slot), 512);
+  grid_dependency_wait();
+  grid_dependents_launch();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  // ---- the schedule ----
+  for (int b = tid; b < p.batch; b += kThreads) {
+    const Request rq = load_request(p, b);
+    if (rq.bad && blockIdx.x == 0 && p.status) atomicOr(p.status, VA_DEV_BAD_TABLE);
+    if (rq.keys == 0) continue;
+    const int one = (rq.keys + kTile - 1) / kTile, two = (one + 1) / 2;
+    atomicAdd(&sched.tiles1, (unsigned long long)one * p.h_kv);
+    atomicAdd(&sched.tiles2, (unsigned long long)two * p.h_kv);
+    atomicMax(&sched.most_rows, rq.rows);
+    atomicAdd(&sched.entries, min(two, kList + 1));
+  }
+  __syncthreads();
+  const int kt = sched.tiles1 <= gridDim.x ? 1 : 2;
+  const bool sorted = kt == 2 && sched.most_rows > kResident * kTile && sched.entries <= kList;
+  const long long total = (long long)(kt == 1 ? sched.tiles1 : sched.tiles2);
+  if (sorted) {
+    // rank = units with more chunks, or as many and listed before
+    int* const cost = reinterpret_cast<int*>(smem + C::OFF_K);
+    int2* const unit = reinterpret_cast<int2*>(smem + C::OFF_K + kList * 4);
+    __syncthreads();
+    if (tid == 0) sched.entries = 0;
+    __syncthreads();
+    for (int b = tid; b < p.batch; b += kThreads) {
+      const Request rq = load_request(p, b);
+      const int n = (rq.keys + 2 * kTile - 1) / (2 * kTile);
+      if (n == 0) continue;
+      const int first = atomicAdd(&sched.entries, n);
+      for (int i = 0; i < n && first + i < kList; ++i) {
+        const int skip = p.mask || rq.chunks <= kResident ? 0 : (int)((long long)max(0, i * 2 * kTile - rq.pre) * p.group / kTile);
+        cost[first + i] = max(0, rq.chunks - skip);
+        unit[first + i] = make_int2(b, i);
       }
-      if (ok) {
-        float* const w = p.key_weights + dst;
-        *w = j < rq.pre && p.decay != 0.f ? fmaf(p.decay, *w, sum) : sum;
+    }
+    __syncthreads();
+    const int n = min(sched.entries, kList);
+    for (int i = tid; i < n; i += kThreads) {
+      const int c = cost[i];
+      const int2 u = unit[i];
+      int rank = 0;
+      for (int k = 0; k < n; ++k) {
+        // equals by request and tile: the atomics' order differs from CTA to CTA
+        const int2 v = unit[k];
+        rank += cost[k] > c || (cost[k] == c && (v.x < u.x || (v.x == u.x && v.y < u.y)));
       }
+      list[rank] = u;
     }
   }
+  if (warp == 0) {
+    const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+    long long run = 0;
+    if (!sorted && lo < hi)
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        long long units = 0;
+        if (b0 + lane < p.batch) {
+          const int keys = load_request(p, b0 + lane).keys;
+          units = (long long)((keys + kTile * kt - 1) / (kTile * kt)) * p.h_kv;
+        }
+        long long sum = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long t = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += t;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, run + sum > lo);
+        if (hit) {
+          if (lane == __ffs(hit) - 1) {
+            sched.b0 = b0 + lane;
+            sched.off = lo - (run + sum - units);
+          }
+          break;
+        }
+        run += __shfl_sync(0xffffffffu, sum, 31);
+      }
+    if (lane == 0) {
+      sched.kt = kt;
+      sched.sorted = sorted;
+      sched.count = sorted ? total : hi - lo;
+    }
+  }
+  __syncthreads();
+
+  Walk w(p, sched, list);
+  int qn = 0, qbase = 0;     // chunk loads so far, and at the first of the resident ones
+  int sn[2] = {0, 0};        // products so far of each tile
+  bool live = true;
+
+  if (warp < kEpiWarps) {
+    // ---------------- weights: one thread per key ----------------
+    const int t = warp >> 2, slot = (warp & 3) * 32 + lane;
+    const uint32_t cols = tmem + t * 256 + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint64_t scale = f32x2(p.scale_log2, p.scale_log2);
+    int page_next = -1;        // page of this thread's key of the next unit, when it is the next of this head
+    bool have_next = false;
+    int products = 0;
+    while (live && w.next()) {
+      const Request& rq = w.rq;
+      if (rq.bad) {
+        if (warp == 0 && lane == 0 && p.status) atomicOr(p.status, VA_DEV_BAD_TABLE);
+        have_next = false;
+        continue;
+      }
+      const int j = w.key0() + t * kTile + slot;
+      const bool here = t < w.tiles_here(), mine = here && j < rq.keys;
+      long long dst = -1;
+      float old = 0.f;
+      if (mine) {
+        dst = w.row_of(have_next ? page_next : w.page_of(j), j);
+        const int src = w.source(j);
+        if (src != j && w.row_of(w.page_of(src), src) < 0) dst = -1;
+        if (dst < 0 && p.status) atomicOr(p.status, VA_DEV_BAD_PAGE);
+        if (dst >= 0 && j < rq.pre && p.decay != 0.f) old = p.key_weights[dst];
+      }
+      have_next = !w.last;
+      if (have_next) page_next = j + kTile * sched.kt < rq.keys ? w.page_of(j + kTile * sched.kt) : -1;
+      const int draft = j - rq.pre, tile_last = w.key0() + t * kTile + kTile - 1;
+      float sum = 0.f;
+      if (w.fresh && w.resident()) {
+        qbase = qn;
+        qn += rq.chunks;
+      }
+      for (int c = w.chunk0(); live && c < rq.chunks; ++c) {
+        const int e = w.resident() ? qbase + c : qn++;
+        if (w.fresh || !w.resident()) live = warp_wait(bar(B_QF + (e & 1)), (e >> 1) & 1, abort_flag);
+        if (!live) break;
+        if (here) {
+          const int buf = products & 1;
+          live = warp_wait(bar(B_SF + t * 2 + buf), (products >> 1) & 1, abort_flag);
+          if (!live) break;
+          ++products;
+          tc_fence_after();
+          const int r0 = c * kTile, nr = min(kTile, rq.rows - r0);
+          // all rows of the chunk see all keys of the tile
+          const bool plain = p.mask ? !p.mask_full && tile_last < rq.pre
+                                    : (long long)(tile_last - rq.pre) * p.group <= r0;
+          const uint32_t at = cols + buf * kTile;
+          const float* const l2 = l2s + (e & 1) * kTile;
+          uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll 1
+          for (int k = 0; k * 32 < nr; ++k) {
+            uint32_t s[32];
+            tmem_ld32(at + k * 32, s);
+            tmem_wait_ld();
+            if (plain && (k + 1) * 32 <= nr) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(l2 + k * 32 + i);
+                const uint64_t a = fma_f32x2(f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale, l.x);
+                const uint64_t b = fma_f32x2(f32x2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scale, l.y);
+                acc0 = add_f32x2(acc0, f32x2(ex2(f32x2_lo(a)), ex2(f32x2_hi(a))));
+                acc1 = add_f32x2(acc1, f32x2(ex2(f32x2_lo(b)), ex2(f32x2_hi(b))));
+              }
+            } else {
+              // row by row: the chunk's end, the causal border, or the mask's bits
+              int tok = (r0 + k * 32) / p.group, g = (r0 + k * 32) - tok * p.group;
+              bool vis = false;
+              float part = 0.f;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                if (k * 32 + i < nr && mine) {
+                  if (i == 0 || g == 0) {
+                    vis = draft <= tok;
+                    if (p.mask) {
+                      vis = draft < 0;
+                      if (p.mask_full || draft >= 0) {
+                        const long long bit = p.mask_indptr[w.b] + (p.mask_full ? (long long)tok * rq.keys + j
+                                                                                : (long long)tok * rq.L + draft);
+                        vis = (p.mask[bit >> 3] >> (bit & 7)) & 1;
+                      }
+                    }
+                  }
+                  if (vis) part += ex2(fmaf(__uint_as_float(s[i]), p.scale_log2, l2[k * 32 + i]));
+                  if (++g == p.group) {
+                    g = 0;
+                    ++tok;
+                  }
+                }
+              }
+              acc0 = add_f32x2(acc0, f32x2(part, 0.f));
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(bar(B_SE + t * 2 + buf));
+          acc0 = add_f32x2(acc0, acc1);
+          sum += f32x2_lo(acc0) + f32x2_hi(acc0);
+        }
+        if (w.last || !w.resident()) {   // the chunk's lse have been read
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_QE + (e & 1)));
+        }
+      }
+      if (live && dst >= 0) p.key_weights[dst] = fmaf(p.decay, old, sum);
+    }
+    tc_fence_before();
+  } else if (warp < kMmaWarp) {
+    // ---------------- loads ----------------
+    constexpr int KCH = (FP8 ? D : 2 * D) / 16, QCH = 2 * D / 16;  // 16-byte chunks of a row
+    const int lw = warp - kLoadWarp, own = lw * 32 + lane;          // this thread's row of a tile
+    int pend[kFlight], np = 0, kn = 0;                              // loads under way: slot, and 8: a chunk of q
+    // the oldest load has landed: widen it, and pass it on
+    auto finish = [&]() {
+      if (np == 3) cp_async_wait<2>();
+      else if (np == 2) cp_async_wait<1>();
+      else cp_async_wait<0>();
+      const int what = pend[0];
+      pend[0] = pend[1];
+      pend[1] = pend[2];
+      --np;
+      if constexpr (FP8) {
+        if (what & 8) {
+          const uint32_t base = sbase + C::OFF_Q + (what & 1) * C::OP;
+#pragma unroll
+          for (int s = 0; s < QCH; ++s) {
+            const int row = lw * 32 + s * (32 / QCH) + lane / QCH;
+            const uint32_t a = op_addr(base, row, lane % QCH);
+            uint4 v = lds128(a);
+            v.x = bf16x2_to_f16x2(v.x);
+            v.y = bf16x2_to_f16x2(v.y);
+            v.z = bf16x2_to_f16x2(v.z);
+            v.w = bf16x2_to_f16x2(v.w);
+            sts128(a, v);
+          }
+        } else {
+          // what >> 4: number of the K tile
+          const int n = what >> 4, ks = n % C::NK;
+          if (n >= C::NK && !warp_wait(bar(B_KE + ks), (n / C::NK - 1) & 1, abort_flag)) {
+            live = false;
+            return;
+          }
+          const uint32_t raw = sbase + C::OFF_RAW + (n % kFlight) * C::RAW, base = sbase + C::OFF_K + ks * C::OP;
+#pragma unroll
+          for (int s = 0; s < KCH; ++s) {
+            const int row = lw * 32 + s * (32 / KCH) + lane / KCH, ch = lane % KCH;
+            const uint4 v = lds128(raw + row * D + ((ch ^ (row & (KCH - 1))) << 4));
+            sts128(op_addr(base, row, 2 * ch), make_uint4(e4m3x2_to_f16x2((uint16_t)v.x), e4m3x2_to_f16x2((uint16_t)(v.x >> 16)),
+                                                          e4m3x2_to_f16x2((uint16_t)v.y), e4m3x2_to_f16x2((uint16_t)(v.y >> 16))));
+            sts128(op_addr(base, row, 2 * ch + 1), make_uint4(e4m3x2_to_f16x2((uint16_t)v.z), e4m3x2_to_f16x2((uint16_t)(v.z >> 16)),
+                                                              e4m3x2_to_f16x2((uint16_t)v.w), e4m3x2_to_f16x2((uint16_t)(v.w >> 16))));
+          }
+        }
+      }
+      fence_proxy_async();
+      mbar_arrive(bar((what & 8) ? B_QF + (what & 1) : B_KF + (what >> 4) % C::NK));
+    };
+    // wait for a buffer to be free: nothing that its readers wait for may be held back
+    auto wait_free = [&](uint32_t b, uint32_t parity) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return;
+      while (np > 0 && live) finish();
+      if (live) live = warp_wait(b, parity, abort_flag);
+    };
+    auto room = [&]() {
+      if (np == kFlight) finish();
+    };
+    int page_next[2];
+    bool have_next = false;
+    while (live && w.next()) {
+      const Request& rq = w.rq;
+      if (rq.chunks == 0) {
+        have_next = false;
+        continue;
+      }
+      const int nt = w.tiles_here(), key0 = w.key0();
+      long long row[2] = {-1, -1};
+      int pg[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int j = key0 + t * kTile + own;
+        pg[t] = t < nt && j < rq.keys ? (have_next ? page_next[t] : w.page_of(w.source(j))) : -1;
+      }
+      have_next = !w.last;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int j = key0 + t * kTile + own, jn = j + sched.kt * kTile;
+        if (t < nt && j < rq.keys) row[t] = w.row_of(pg[t], w.source(j));
+        if (have_next) page_next[t] = t < sched.kt && jn < rq.keys ? w.page_of(w.source(jn)) : -1;
+      }
+      for (int t = 0; t < nt && live; ++t) {
+        const int n = kn++, ks = n % C::NK;
+        if constexpr (!FP8)
+          if (n >= C::NK) wait_free(bar(B_KE + ks), (n / C::NK - 1) & 1);
+        if (live) room();
+        if (!live) break;
+        const uint32_t base = FP8 ? sbase + C::OFF_RAW + (n % kFlight) * C::RAW : sbase + C::OFF_K + ks * C::OP;
+        const long long mine = t == 0 ? row[0] : row[1];
+#pragma unroll
+        for (int s = 0; s < KCH; ++s) {
+          const int from = s * (32 / KCH) + lane / KCH, r = lw * 32 + from, ch = lane % KCH;
+          const long long k = __shfl_sync(0xffffffffu, mine, from);
+          if (k >= 0)   // rows past the keys, and bad pages: whatever the buffer holds stays in its own lane
+            cp_async_16(FP8 ? base + r * D + ((ch ^ (r & (KCH - 1))) << 4) : op_addr(base, r, ch),
+                        static_cast<const uint8_t*>(p.k_cache) + (k * KCH + ch) * 16, 16);
+        }
+        cp_async_commit();
+        pend[np++] = n << 4;
+      }
+      if (!live) break;
+      const bool keep = w.resident();
+      if (keep && !w.fresh) continue;
+      for (int c = w.chunk0(); c < rq.chunks && live; ++c) {
+        const int e = qn++, r = c * kTile + own;
+        long long qrow = -1;
+        float l = INFINITY;   // rows past the end, and rows that saw nothing, count nothing
+        if (r < rq.rows) {
+          const int tok = r / p.group, g = r - tok * p.group;
+          const int node = p.accept_len ? min(max(p.path[rq.o + tok], 0), rq.L - 1) : tok;
+          qrow = (long long)(rq.o + node) * p.h_q + w.h * p.group + g;
+          const float lse = p.lse[qrow];
+          l = lse == -INFINITY ? INFINITY : lse * kLog2e;
+        }
+        if (e >= 2) wait_free(bar(B_QE + (e & 1)), ((e >> 1) - 1) & 1);
+        if (live) room();
+        if (!live) break;
+        const uint32_t base = sbase + C::OFF_Q + (e & 1) * C::OP;
+#pragma unroll
+        for (int s = 0; s < QCH; ++s) {
+          const int from = s * (32 / QCH) + lane / QCH, ch = lane % QCH;
+          const long long k = __shfl_sync(0xffffffffu, qrow, from);
+          cp_async_16(op_addr(base, lw * 32 + from, ch),
+                      static_cast<const uint8_t*>(p.q) + (max(k, 0ll) * QCH + ch) * 16, k >= 0 ? 16 : 0);
+        }
+        cp_async_commit();
+        l2s[(e & 1) * kTile + own] = -l;
+        pend[np] = 8 | (e & 1);
+        ++np;
+      }
+    }
+    while (np > 0 && live) finish();
+    cp_async_wait<0>();
+  } else {
+    // ---------------- products ----------------
+    int kn = 0;
+    bool issued = false;
+    while (live && w.next()) {
+      const Request& rq = w.rq;
+      if (rq.chunks == 0) continue;
+      const int nt = w.tiles_here();
+      if (w.fresh && w.resident()) {
+        qbase = qn;
+        qn += rq.chunks;
+      }
+      for (int t = 0; t < nt && live; ++t) live = warp_wait(bar(B_KF + (kn + t) % C::NK), ((kn + t) / C::NK) & 1, abort_flag);
+      for (int c = w.chunk0(); live && c < rq.chunks; ++c) {
+        const int e = w.resident() ? qbase + c : qn++;
+        if (w.fresh || !w.resident()) live = warp_wait(bar(B_QF + (e & 1)), (e >> 1) & 1, abort_flag);
+        const uint32_t id = idesc_n<FP8>((min(kTile, rq.rows - c * kTile) + 15) & ~15);
+        for (int t = 0; t < nt && live; ++t) {
+          const int buf = sn[t] & 1;
+          if (sn[t] >= 2) live = warp_wait(bar(B_SE + t * 2 + buf), ((sn[t] >> 1) - 1) & 1, abort_flag);
+          if (!live) break;
+          ++sn[t];
+          if (lane == 0) {
+            tc_fence_after();
+            const uint32_t ka = sbase + C::OFF_K + (kn + t) % C::NK * C::OP, qa = sbase + C::OFF_Q + (e & 1) * C::OP;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = (k >> 2) * (kTile * 128) + (k & 3) * 32;
+              umma_bf16(tmem + t * 256 + buf * kTile, smem_desc_sw128(ka + off, 16, 1024), smem_desc_sw128(qa + off, 16, 1024),
+                        id, k > 0);
+            }
+            umma_commit(bar(B_SF + t * 2 + buf));
+            if (c == rq.chunks - 1) umma_commit(bar(B_KE + (kn + t) % C::NK));
+          }
+          issued = true;
+          __syncwarp();
+        }
+        if (live && (w.last || !w.resident()) && lane == 0) umma_commit(bar(B_QE + (e & 1)));
+        __syncwarp();
+      }
+      kn += nt;
+    }
+    if (issued) {   // every commit has arrived before the CTA's shared memory goes away
+      if (lane == 0) umma_commit(bar(B_DONE));
+      __syncwarp();
+      warp_wait(bar(B_DONE), 0, abort_flag);
+    }
+  }
+
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (tid == 0 && *abort_flag && p.status) atomicOr(p.status, VA_DEV_TIMEOUT);
+}
+
+template <int D, bool FP8>
+cudaError_t launch(const KeyWeightParams& p, int num_sms, cudaStream_t stream) {
+  using C = Cfg<D, FP8>;
+  const void* k = reinterpret_cast<const void*>(verify_attn_key_weights_kernel<D, FP8>);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  void* args[] = {const_cast<KeyWeightParams*>(&p)};
+  return launch_kernel(k, dim3((unsigned)num_sms), dim3(kThreads), C::SMEM, stream, args, /*pdl=*/true);
 }
 
 }  // namespace
 
 cudaError_t launch_key_weights(const KeyWeightParams& p, int head_dim, bool kv_fp8, int num_sms, cudaStream_t stream) {
-  void* args[] = {const_cast<KeyWeightParams*>(&p)};
-  const void* k = head_dim == 64 ? (kv_fp8 ? reinterpret_cast<const void*>(verify_attn_key_weights_kernel<64, true>)
-                                           : reinterpret_cast<const void*>(verify_attn_key_weights_kernel<64, false>))
-                                 : (kv_fp8 ? reinterpret_cast<const void*>(verify_attn_key_weights_kernel<128, true>)
-                                           : reinterpret_cast<const void*>(verify_attn_key_weights_kernel<128, false>));
-  return launch_kernel(k, dim3((unsigned)num_sms * 4), dim3(kTile), 0, stream, args, /*pdl=*/true);
+  if (head_dim == 64) return kv_fp8 ? launch<64, true>(p, num_sms, stream) : launch<64, false>(p, num_sms, stream);
+  return kv_fp8 ? launch<128, true>(p, num_sms, stream) : launch<128, false>(p, num_sms, stream);
 }
 
 }  // namespace va
