@@ -60,14 +60,31 @@ template <int D, bool FP8>
 struct Cfg {
   static constexpr int OP = kTile * D * 2;         // one operand tile: [D / 64 halves][128 rows][128 bytes]
   static constexpr int RAW = FP8 ? kTile * D : 0;  // e4m3 rows as they are
-  static constexpr int NK = FP8 ? 3 : 4;           // K operand tiles
-  static constexpr int OFF_Q = 0, OFF_K = 2 * OP, OFF_RAW = OFF_K + NK * OP, OFF_L2 = OFF_RAW + kFlight * RAW,
-                       OFF_LIST = OFF_L2 + 2 * kTile * 4, OFF_BAR = OFF_LIST + kList * 8, SMEM = OFF_BAR + 256;
-  static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(kList * 12 <= NK * OP, "the unsorted list lies in the K tiles");
+  // Operand slots, the first for tiles of K and the rest for chunks of q: two
+  // chunks stay where rows are few; where they are streamed they are what has
+  // to come in, and a unit's own tiles are enough of K.
+  static constexpr int SLOTS = FP8 ? 5 : 6;
+  static constexpr int K_RUNS = SLOTS - kResident, K_SORTED = 2;
+  static constexpr int OFF_RAW = SLOTS * OP, OFF_L2 = OFF_RAW + kFlight * RAW, OFF_LIST = OFF_L2 + (SLOTS - K_SORTED) * kTile * 4,
+                       OFF_BAR = OFF_LIST + kList * 8, SMEM = OFF_BAR + 256;
+  static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
+  static_assert(kList * 12 <= SLOTS * OP, "the unsorted list lies in the operand slots");
 };
 
-enum { B_KF = 0, B_KE = 4, B_QF = 8, B_QE = 10, B_SF = 12, B_SE = 16, B_DONE = 20, B_COUNT = 21 };
+// Barriers: a slot full / free, products full / free.
+enum { B_FULL = 0, B_FREE = 6, B_SF = 12, B_SE = 16, B_DONE = 20, B_COUNT = 21 };
+
+// A place in a ring of n slots and the parity of its round.
+struct Ring {
+  int n, slot = 0, round = 0;
+  __device__ explicit Ring(int n_) : n(n_) {}
+  __device__ void step() {
+    if (++slot == n) {
+      slot = 0;
+      ++round;
+    }
+  }
+};
 
 struct Request {
   int o, L, n, pg0;  // first query row, query tokens, those counted, page table
@@ -173,10 +190,10 @@ struct Walk {
   __device__ int key0() const { return tile * kTile * s.kt; }
   __device__ int tiles_here() const { return min(s.kt, (rq.keys - key0() + kTile - 1) / kTile); }
   __device__ bool resident() const { return rq.chunks <= kResident; }
-  // chunks before this one see none of the unit's keys
-  __device__ int chunk0() const {
+  // chunks before this one see none of the keys of the unit's tile t
+  __device__ int chunk0(int t = 0) const {
     if (resident() || p.mask) return 0;
-    return (int)min((long long)max(0, key0() - rq.pre) * p.group / kTile, (long long)rq.chunks);
+    return (int)min((long long)max(0, key0() + t * kTile - rq.pre) * p.group / kTile, (long long)rq.chunks);
   }
   // position that key j is read from
   __device__ int source(int j) const {
@@ -227,15 +244,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
   int2* const list = reinterpret_cast<int2*>(smem + C::OFF_LIST);
 
   if (tid == 0) {
+    for (int i = 0; i < C::SLOTS; ++i) mbar_init(bar(B_FULL + i), 128);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(B_KF + i), 128);
-      mbar_init(bar(B_KE + i), 1);
       mbar_init(bar(B_SF + i), 1);
       mbar_init(bar(B_SE + i), 128);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(B_QF + i), 128);
-      mbar_init(bar(B_QE + i), 1 + kEpiWarps);
     }
     mbar_init(bar(B_DONE), 1);
     abort_shared = 0;
@@ -267,8 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
   const long long total = (long long)(kt == 1 ? sched.tiles1 : sched.tiles2);
   if (sorted) {
     // rank = units with more chunks, or as many and listed before
-    int* const cost = reinterpret_cast<int*>(smem + C::OFF_K);
-    int2* const unit = reinterpret_cast<int2*>(smem + C::OFF_K + kList * 4);
+    int* const cost = reinterpret_cast<int*>(smem);
+    int2* const unit = reinterpret_cast<int2*>(smem + kList * 4);
     __syncthreads();
     if (tid == 0) sched.entries = 0;
     __syncthreads();
@@ -324,6 +336,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         run += __shfl_sync(0xffffffffu, sum, 31);
       }
     if (lane == 0) {
+      // a chunk's slot is free when its products are done and the sums' warps have read its lse
+      for (int i = 0; i < C::SLOTS; ++i)
+        mbar_init(bar(B_FREE + i), i < (sorted ? C::K_SORTED : C::K_RUNS) ? 1 : 1 + kEpiWarps);
+      mbar_fence_init();
       sched.kt = kt;
       sched.sorted = sorted;
       sched.count = sorted ? total : hi - lo;
@@ -332,8 +348,24 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
   __syncthreads();
 
   Walk w(p, sched, list);
-  int qn = 0, qbase = 0;     // chunk loads so far, and at the first of the resident ones
-  int sn[2] = {0, 0};        // products so far of each tile
+  const int nk = sorted ? C::K_SORTED : C::K_RUNS;
+  Ring kr(nk), qr(C::SLOTS - nk);  // of this role's next tile of K and chunk of q
+  int held[kResident], held_p[kResident];  // resident chunks: slot, parity
+  // the chunk's place: its own, or that of the next load
+  auto take_chunk = [&](int c, int* slot, int* parity) {
+    if (w.fresh || !w.resident()) {
+      *slot = nk + qr.slot;
+      *parity = qr.round & 1;
+      qr.step();
+      if (w.resident()) {
+        if (c == 0) held[0] = *slot, held_p[0] = *parity;
+        else held[1] = *slot, held_p[1] = *parity;
+      }
+    } else {
+      *slot = c == 0 ? held[0] : held[1];
+      *parity = c == 0 ? held_p[0] : held_p[1];
+    }
+  };
   bool live = true;
 
   if (warp < kEpiWarps) {
@@ -366,15 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
       if (have_next) page_next = j + kTile * sched.kt < rq.keys ? w.page_of(j + kTile * sched.kt) : -1;
       const int draft = j - rq.pre, tile_last = w.key0() + t * kTile + kTile - 1;
       float sum = 0.f;
-      if (w.fresh && w.resident()) {
-        qbase = qn;
-        qn += rq.chunks;
-      }
+      const int c_mine = here ? w.chunk0(t) : rq.chunks;
       for (int c = w.chunk0(); live && c < rq.chunks; ++c) {
-        const int e = w.resident() ? qbase + c : qn++;
-        if (w.fresh || !w.resident()) live = warp_wait(bar(B_QF + (e & 1)), (e >> 1) & 1, abort_flag);
+        int qs, qp;
+        take_chunk(c, &qs, &qp);
+        // the chunk's lse are there; a warp that skips the chunk waits as well, so that it frees the slot in its turn
+        live = warp_wait(bar(B_FULL + qs), qp, abort_flag);
         if (!live) break;
-        if (here) {
+        if (c >= c_mine) {
           const int buf = products & 1;
           live = warp_wait(bar(B_SF + t * 2 + buf), (products >> 1) & 1, abort_flag);
           if (!live) break;
@@ -385,49 +416,52 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
           const bool plain = p.mask ? !p.mask_full && tile_last < rq.pre
                                     : (long long)(tile_last - rq.pre) * p.group <= r0;
           const uint32_t at = cols + buf * kTile;
-          const float* const l2 = l2s + (e & 1) * kTile;
+          const float* const l2 = l2s + (qs - nk) * kTile;
           uint64_t acc0 = 0, acc1 = 0;
 #pragma unroll 1
           for (int k = 0; k * 32 < nr; ++k) {
             uint32_t s[32];
             tmem_ld32(at + k * 32, s);
             tmem_wait_ld();
+            const float* const lk = l2 + k * 32;
             if (plain && (k + 1) * 32 <= nr) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
-                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(l2 + k * 32 + i);
+                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(lk + i);
                 const uint64_t a = fma_f32x2(f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale, l.x);
                 const uint64_t b = fma_f32x2(f32x2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scale, l.y);
                 acc0 = add_f32x2(acc0, f32x2(ex2(f32x2_lo(a)), ex2(f32x2_hi(a))));
                 acc1 = add_f32x2(acc1, f32x2(ex2(f32x2_lo(b)), ex2(f32x2_hi(b))));
               }
             } else {
-              // row by row: the chunk's end, the causal border, or the mask's bits
-              int tok = (r0 + k * 32) / p.group, g = (r0 + k * 32) - tok * p.group;
-              bool vis = false;
-              float part = 0.f;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                if (k * 32 + i < nr && mine) {
-                  if (i == 0 || g == 0) {
-                    vis = draft <= tok;
-                    if (p.mask) {
-                      vis = draft < 0;
-                      if (p.mask_full || draft >= 0) {
-                        const long long bit = p.mask_indptr[w.b] + (p.mask_full ? (long long)tok * rq.keys + j
-                                                                                : (long long)tok * rq.L + draft);
-                        vis = (p.mask[bit >> 3] >> (bit & 7)) & 1;
-                      }
+              // which of the 32 rows see the key: up to the chunk's end, from the causal border on, or by the mask
+              uint32_t on = 0;
+              if (mine) {
+                const int first = r0 + k * 32;
+                if (!p.mask || (!p.mask_full && draft < 0)) {
+                  const int lo = draft <= 0 ? 0 : (int)min((long long)draft * p.group - first, 32ll);
+                  on = lo >= 32 ? 0u : 0xffffffffu << max(lo, 0);
+                } else {
+                  const long long row0 = p.mask_indptr[w.b] + (p.mask_full ? j : draft);
+                  const int width = p.mask_full ? rq.keys : rq.L;
+                  for (int tok = first / p.group, e = tok * p.group - first; e < 32 && tok < rq.n; ++tok, e += p.group) {
+                    const long long bit = row0 + (long long)tok * width;
+                    if ((p.mask[bit >> 3] >> (bit & 7)) & 1) {
+                      const int z = min(e + p.group, 32);   // rows e .. z - 1 of this token
+                      on |= (z == 32 ? 0xffffffffu : (1u << z) - 1u) & (0xffffffffu << max(e, 0));
                     }
                   }
-                  if (vis) part += ex2(fmaf(__uint_as_float(s[i]), p.scale_log2, l2[k * 32 + i]));
-                  if (++g == p.group) {
-                    g = 0;
-                    ++tok;
-                  }
                 }
+                if (nr - k * 32 < 32) on &= (1u << (nr - k * 32)) - 1u;
               }
-              acc0 = add_f32x2(acc0, f32x2(part, 0.f));
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(lk + i);
+                const uint64_t a = fma_f32x2(f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale, l.x);
+                const uint64_t b = fma_f32x2(f32x2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scale, l.y);
+                acc0 = add_f32x2(acc0, f32x2((on >> i) & 1 ? ex2(f32x2_lo(a)) : 0.f, (on >> (i + 1)) & 1 ? ex2(f32x2_hi(a)) : 0.f));
+                acc1 = add_f32x2(acc1, f32x2((on >> (i + 2)) & 1 ? ex2(f32x2_lo(b)) : 0.f, (on >> (i + 3)) & 1 ? ex2(f32x2_hi(b)) : 0.f));
+              }
             }
           }
           tc_fence_before();
@@ -437,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         }
         if (w.last || !w.resident()) {   // the chunk's lse have been read
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_QE + (e & 1)));
+          if (lane == 0) mbar_arrive(bar(B_FREE + qs));
         }
       }
       if (live && dst >= 0) p.key_weights[dst] = fmaf(p.decay, old, sum);
@@ -447,23 +481,25 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
     // ---------------- loads ----------------
     constexpr int KCH = (FP8 ? D : 2 * D) / 16, QCH = 2 * D / 16;  // 16-byte chunks of a row
     const int lw = warp - kLoadWarp, own = lw * 32 + lane;          // this thread's row of a tile
-    int pend[kFlight], np = 0, kn = 0;                              // loads under way: slot, and 8: a chunk of q
+    int p0 = 0, p1 = 0, p2 = 0, np = 0;  // loads under way, the oldest first: slot, and 8: a chunk of q
+    Ring rr(kFlight), rf(kFlight);       // raw buffers: of the next load, of the next one widened
+    Ring kf(nk);                         // the K slot that is widened into next
     // the oldest load has landed: widen it, and pass it on
     auto finish = [&]() {
       if (np == 3) cp_async_wait<2>();
       else if (np == 2) cp_async_wait<1>();
       else cp_async_wait<0>();
-      const int what = pend[0];
-      pend[0] = pend[1];
-      pend[1] = pend[2];
+      int slot = p0 & 7;
+      const bool is_q = p0 & 8;
+      p0 = p1;
+      p1 = p2;
       --np;
       if constexpr (FP8) {
-        if (what & 8) {
-          const uint32_t base = sbase + C::OFF_Q + (what & 1) * C::OP;
+        if (is_q) {
+          const uint32_t base = sbase + slot * C::OP;
 #pragma unroll
           for (int s = 0; s < QCH; ++s) {
-            const int row = lw * 32 + s * (32 / QCH) + lane / QCH;
-            const uint32_t a = op_addr(base, row, lane % QCH);
+            const uint32_t a = op_addr(base, lw * 32 + s * (32 / QCH) + lane / QCH, lane % QCH);
             uint4 v = lds128(a);
             v.x = bf16x2_to_f16x2(v.x);
             v.y = bf16x2_to_f16x2(v.y);
@@ -472,13 +508,14 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
             sts128(a, v);
           }
         } else {
-          // what >> 4: number of the K tile
-          const int n = what >> 4, ks = n % C::NK;
-          if (n >= C::NK && !warp_wait(bar(B_KE + ks), (n / C::NK - 1) & 1, abort_flag)) {
+          slot = kf.slot;
+          if (kf.round > 0 && !warp_wait(bar(B_FREE + slot), (kf.round - 1) & 1, abort_flag)) {
             live = false;
             return;
           }
-          const uint32_t raw = sbase + C::OFF_RAW + (n % kFlight) * C::RAW, base = sbase + C::OFF_K + ks * C::OP;
+          kf.step();
+          const uint32_t raw = sbase + C::OFF_RAW + rf.slot * C::RAW, base = sbase + slot * C::OP;
+          rf.step();
 #pragma unroll
           for (int s = 0; s < KCH; ++s) {
             const int row = lw * 32 + s * (32 / KCH) + lane / KCH, ch = lane % KCH;
@@ -491,16 +528,25 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         }
       }
       fence_proxy_async();
-      mbar_arrive(bar((what & 8) ? B_QF + (what & 1) : B_KF + (what >> 4) % C::NK));
+      mbar_arrive(bar(B_FULL + slot));
     };
-    // wait for a buffer to be free: nothing that its readers wait for may be held back
-    auto wait_free = [&](uint32_t b, uint32_t parity) {
-      if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return;
-      while (np > 0 && live) finish();
-      if (live) live = warp_wait(b, parity, abort_flag);
-    };
+    // room for one more load under way
     auto room = [&]() {
       if (np == kFlight) finish();
+    };
+    // wait for a buffer to be free: what its readers may wait for is passed on meanwhile
+    auto wait_free = [&](uint32_t b, uint32_t parity) {
+      while (live && !__all_sync(0xffffffffu, mbar_try_wait(b, parity))) {
+        if (np > 0) finish();
+        else live = warp_wait(b, parity, abort_flag);
+      }
+    };
+    auto put = [&](int what) {
+      cp_async_commit();
+      if (np == 0) p0 = what;
+      else if (np == 1) p1 = what;
+      else p2 = what;
+      ++np;
     };
     int page_next[2];
     bool have_next = false;
@@ -526,12 +572,11 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         if (have_next) page_next[t] = t < sched.kt && jn < rq.keys ? w.page_of(w.source(jn)) : -1;
       }
       for (int t = 0; t < nt && live; ++t) {
-        const int n = kn++, ks = n % C::NK;
+        room();
         if constexpr (!FP8)
-          if (n >= C::NK) wait_free(bar(B_KE + ks), (n / C::NK - 1) & 1);
-        if (live) room();
+          if (live && kr.round > 0) wait_free(bar(B_FREE + kr.slot), (kr.round - 1) & 1);
         if (!live) break;
-        const uint32_t base = FP8 ? sbase + C::OFF_RAW + (n % kFlight) * C::RAW : sbase + C::OFF_K + ks * C::OP;
+        const uint32_t base = sbase + (FP8 ? C::OFF_RAW + rr.slot * C::RAW : kr.slot * C::OP);
         const long long mine = t == 0 ? row[0] : row[1];
 #pragma unroll
         for (int s = 0; s < KCH; ++s) {
@@ -541,27 +586,29 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
             cp_async_16(FP8 ? base + r * D + ((ch ^ (r & (KCH - 1))) << 4) : op_addr(base, r, ch),
                         static_cast<const uint8_t*>(p.k_cache) + (k * KCH + ch) * 16, 16);
         }
-        cp_async_commit();
-        pend[np++] = n << 4;
+        put(kr.slot);
+        rr.step();
+        kr.step();
       }
       if (!live) break;
-      const bool keep = w.resident();
-      if (keep && !w.fresh) continue;
+      if (w.resident() && !w.fresh) continue;
+      // row c of the chunks and its lse, one chunk ahead
+      auto q_row = [&](int c) -> long long {
+        const int r = c * kTile + own;
+        if (r >= rq.rows) return -1;
+        const int tok = r / p.group, g = r - tok * p.group;
+        const int node = p.accept_len ? min(max(p.path[rq.o + tok], 0), rq.L - 1) : tok;
+        return (long long)(rq.o + node) * p.h_q + w.h * p.group + g;
+      };
+      long long qrow = q_row(w.chunk0());
+      float lse = qrow >= 0 ? p.lse[qrow] : -INFINITY;
       for (int c = w.chunk0(); c < rq.chunks && live; ++c) {
-        const int e = qn++, r = c * kTile + own;
-        long long qrow = -1;
-        float l = INFINITY;   // rows past the end, and rows that saw nothing, count nothing
-        if (r < rq.rows) {
-          const int tok = r / p.group, g = r - tok * p.group;
-          const int node = p.accept_len ? min(max(p.path[rq.o + tok], 0), rq.L - 1) : tok;
-          qrow = (long long)(rq.o + node) * p.h_q + w.h * p.group + g;
-          const float lse = p.lse[qrow];
-          l = lse == -INFINITY ? INFINITY : lse * kLog2e;
-        }
-        if (e >= 2) wait_free(bar(B_QE + (e & 1)), ((e >> 1) - 1) & 1);
-        if (live) room();
+        const long long qnext = c + 1 < rq.chunks ? q_row(c + 1) : -1;
+        const float lnext = qnext >= 0 ? p.lse[qnext] : -INFINITY;
+        room();
+        if (live && qr.round > 0) wait_free(bar(B_FREE + nk + qr.slot), (qr.round - 1) & 1);
         if (!live) break;
-        const uint32_t base = sbase + C::OFF_Q + (e & 1) * C::OP;
+        const uint32_t base = sbase + (nk + qr.slot) * C::OP;
 #pragma unroll
         for (int s = 0; s < QCH; ++s) {
           const int from = s * (32 / QCH) + lane / QCH, ch = lane % QCH;
@@ -569,39 +616,47 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
           cp_async_16(op_addr(base, lw * 32 + from, ch),
                       static_cast<const uint8_t*>(p.q) + (max(k, 0ll) * QCH + ch) * 16, k >= 0 ? 16 : 0);
         }
-        cp_async_commit();
-        l2s[(e & 1) * kTile + own] = -l;
-        pend[np] = 8 | (e & 1);
-        ++np;
+        // rows past the end, and rows that saw nothing, count nothing
+        l2s[qr.slot * kTile + own] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+        put(8 | (nk + qr.slot));
+        qr.step();
+        qrow = qnext;
+        lse = lnext;
       }
     }
     while (np > 0 && live) finish();
     cp_async_wait<0>();
   } else {
     // ---------------- products ----------------
-    int kn = 0;
+    int sn[2] = {0, 0};   // products so far of each tile
     bool issued = false;
     while (live && w.next()) {
       const Request& rq = w.rq;
       if (rq.chunks == 0) continue;
-      const int nt = w.tiles_here();
-      if (w.fresh && w.resident()) {
-        qbase = qn;
-        qn += rq.chunks;
+      const int nt = w.tiles_here(), c1 = w.chunk0(1);
+      Ring ks[2] = {kr, kr};
+      kr.step();
+      if (nt == 2) {
+        ks[1] = kr;
+        kr.step();
       }
-      for (int t = 0; t < nt && live; ++t) live = warp_wait(bar(B_KF + (kn + t) % C::NK), ((kn + t) / C::NK) & 1, abort_flag);
-      for (int c = w.chunk0(); live && c < rq.chunks; ++c) {
-        const int e = w.resident() ? qbase + c : qn++;
-        if (w.fresh || !w.resident()) live = warp_wait(bar(B_QF + (e & 1)), (e >> 1) & 1, abort_flag);
+      const int c0 = w.chunk0();
+      for (int c = c0; live && c < rq.chunks; ++c) {
+        int qs, qp;
+        take_chunk(c, &qs, &qp);
+        if (w.fresh || !w.resident()) live = warp_wait(bar(B_FULL + qs), qp, abort_flag);
         const uint32_t id = idesc_n<FP8>((min(kTile, rq.rows - c * kTile) + 15) & ~15);
-        for (int t = 0; t < nt && live; ++t) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!live || t >= nt || (t == 1 && c < c1)) continue;
+          if (c == (t == 0 ? c0 : max(c0, c1))) live = warp_wait(bar(B_FULL + ks[t].slot), ks[t].round & 1, abort_flag);
           const int buf = sn[t] & 1;
-          if (sn[t] >= 2) live = warp_wait(bar(B_SE + t * 2 + buf), ((sn[t] >> 1) - 1) & 1, abort_flag);
-          if (!live) break;
+          if (live && sn[t] >= 2) live = warp_wait(bar(B_SE + t * 2 + buf), ((sn[t] >> 1) - 1) & 1, abort_flag);
+          if (!live) continue;
           ++sn[t];
           if (lane == 0) {
             tc_fence_after();
-            const uint32_t ka = sbase + C::OFF_K + (kn + t) % C::NK * C::OP, qa = sbase + C::OFF_Q + (e & 1) * C::OP;
+            const uint32_t ka = sbase + ks[t].slot * C::OP, qa = sbase + qs * C::OP;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t off = (k >> 2) * (kTile * 128) + (k & 3) * 32;
@@ -609,15 +664,14 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
                         id, k > 0);
             }
             umma_commit(bar(B_SF + t * 2 + buf));
-            if (c == rq.chunks - 1) umma_commit(bar(B_KE + (kn + t) % C::NK));
+            if (c == rq.chunks - 1) umma_commit(bar(B_FREE + ks[t].slot));
           }
           issued = true;
           __syncwarp();
         }
-        if (live && (w.last || !w.resident()) && lane == 0) umma_commit(bar(B_QE + (e & 1)));
+        if (live && (w.last || !w.resident()) && lane == 0) umma_commit(bar(B_FREE + qs));
         __syncwarp();
       }
-      kn += nt;
     }
     if (issued) {   // every commit has arrived before the CTA's shared memory goes away
       if (lane == 0) umma_commit(bar(B_DONE));
