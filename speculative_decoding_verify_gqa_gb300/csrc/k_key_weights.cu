@@ -244,10 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
   int2* const list = reinterpret_cast<int2*>(smem + C::OFF_LIST);
 
   if (tid == 0) {
-    for (int i = 0; i < C::SLOTS; ++i) mbar_init(bar(B_FULL + i), 128);
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(B_SF + i), 1);
-      mbar_init(bar(B_SE + i), 128);
+      mbar_init(bar(B_SE + i), 4);
     }
     mbar_init(bar(B_DONE), 1);
     abort_shared = 0;
@@ -336,9 +335,15 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         run += __shfl_sync(0xffffffffu, sum, 31);
       }
     if (lane == 0) {
-      // a chunk's slot is free when its products are done and the sums' warps have read its lse
-      for (int i = 0; i < C::SLOTS; ++i)
-        mbar_init(bar(B_FREE + i), i < (sorted ? C::K_SORTED : C::K_RUNS) ? 1 : 1 + kEpiWarps);
+      // Full: each warp's own arrival for what it has stored (a chunk's lse,
+      // widened rows), and each thread's asynchronous one behind its copies.
+      // A chunk's slot is free when its products are done and the sums' warps
+      // have read its lse.
+      for (int i = 0; i < C::SLOTS; ++i) {
+        const bool k = i < (sorted ? C::K_SORTED : C::K_RUNS);
+        mbar_init(bar(B_FULL + i), FP8 ? 4 : k ? 128 : 128 + 4);
+        mbar_init(bar(B_FREE + i), k ? 1 : 1 + kEpiWarps);
+      }
       mbar_fence_init();
       sched.kt = kt;
       sched.sorted = sorted;
@@ -465,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
             }
           }
           tc_fence_before();
-          mbar_arrive(bar(B_SE + t * 2 + buf));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_SE + t * 2 + buf));
           acc0 = add_f32x2(acc0, acc1);
           sum += f32x2_lo(acc0) + f32x2_hi(acc0);
         }
@@ -527,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
           }
         }
       }
-      fence_proxy_async();
-      mbar_arrive(bar(B_FULL + slot));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_FULL + slot));
     };
     // room for one more load under way
     auto room = [&]() {
@@ -541,7 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         else live = warp_wait(b, parity, abort_flag);
       }
     };
+    // a load has been issued: its copies arrive at the barrier by themselves, or are widened when they have landed
     auto put = [&](int what) {
+      if constexpr (!FP8) {
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(B_FULL + (what & 7))) : "memory");
+        return;
+      }
       cp_async_commit();
       if (np == 0) p0 = what;
       else if (np == 1) p1 = what;
@@ -618,6 +629,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         }
         // rows past the end, and rows that saw nothing, count nothing
         l2s[qr.slot * kTile + own] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+        if constexpr (!FP8) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_FULL + nk + qr.slot));
+        }
         put(8 | (nk + qr.slot));
         qr.step();
         qrow = qnext;
@@ -656,6 +671,9 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
           ++sn[t];
           if (lane == 0) {
             tc_fence_after();
+            // what the copies and the loaders' stores left is there for the tensor cores: the fence stands here and not
+            // with the loaders, where it would wait for all their copies under way
+            fence_proxy_async();
             const uint32_t ka = sbase + ks[t].slot * C::OP, qa = sbase + qs * C::OP;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
