@@ -16,13 +16,15 @@
 // is fixed.  K is read once and V not at all: HBM bounds the step of a serving
 // batch, the tensor cores and the SFU's 2^x (one for each pair) a prompt's.
 //
-// A unit is one or two tiles of 128 keys of one (request, KV head); the CTA's
-// roles walk the same sequence of units (one CTA per SM):
+// A unit is one or two tiles of 128 keys of one (request, KV head).  One CTA per
+// SM, its warps in roles that run through the same units:
+//  * one warp walks the schedule: it looks the pages of a unit's keys up and
+//    posts the unit -- its geometry, its places in all rings, its cache rows --
+//    in a queue in shared memory, so that the others' loops stay short;
 //  * 4 loader warps gather K rows by 16-byte asynchronous copies into the
 //    128-byte-swizzled operand layout (any page size and layout; a tile's rows
 //    need not be neighbours), and the query rows of 128-row chunks the same
-//    way, up to three such loads under way.  Their completion is passed on by a
-//    proxy fence and an mbarrier.  e4m3 rows are widened to f16 between a raw
+//    way.  The copies arrive at an mbarrier by themselves.  e4m3 rows are widened to f16 between a raw
 //    buffer and the operand (exact), and bf16 queries with them, as the
 //    attention kernels do;
 //  * one thread issues tcgen05.mma: for each chunk of rows and tile of keys 4 or
@@ -51,10 +53,11 @@ namespace {
 
 constexpr int kTile = 128;    // keys of a tile, query rows of a chunk
 constexpr int kEpiWarps = 8;  // 4 for each of the unit's tiles
-constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kLoadWarp + 4, kThreads = 32 * (kMmaWarp + 1);
+constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kLoadWarp + 4, kWalkWarp = kMmaWarp + 1, kThreads = 32 * (kWalkWarp + 1);
 constexpr int kList = 512;    // units (of all heads) that are sorted
 constexpr int kResident = 2;  // chunks that stay in shared memory
-constexpr int kFlight = 3;    // loads under way per loader thread
+constexpr int kFlight = 3;    // e4m3: loads under way per loader thread
+constexpr int kQueue = 3;     // units posted ahead
 
 template <int D, bool FP8>
 struct Cfg {
@@ -66,18 +69,19 @@ struct Cfg {
   static constexpr int SLOTS = FP8 ? 5 : 6;
   static constexpr int K_RUNS = SLOTS - kResident, K_SORTED = 2;
   static constexpr int OFF_RAW = SLOTS * OP, OFF_L2 = OFF_RAW + kFlight * RAW, OFF_LIST = OFF_L2 + (SLOTS - K_SORTED) * kTile * 4,
-                       OFF_BAR = OFF_LIST + kList * 8, SMEM = OFF_BAR + 256;
+                       OFF_UNIT = OFF_LIST + kList * 8, OFF_ROW = OFF_UNIT + kQueue * 128,
+                       OFF_BAR = OFF_ROW + kQueue * 2 * kTile * 8, SMEM = OFF_BAR + 256;
   static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
   static_assert(kList * 12 <= SLOTS * OP, "the unsorted list lies in the operand slots");
 };
 
-// Barriers: a slot full / free, products full / free.
-enum { B_FULL = 0, B_FREE = 6, B_SF = 12, B_SE = 16, B_DONE = 20, B_COUNT = 21 };
+// Barriers: a slot full / free, products full / free, a unit posted / taken.
+enum { B_FULL = 0, B_FREE = 6, B_SF = 12, B_SE = 16, B_UF = 20, B_UE = 23, B_DONE = 26, B_COUNT = 27 };
 
 // A place in a ring of n slots and the parity of its round.
 struct Ring {
-  int n, slot = 0, round = 0;
-  __device__ explicit Ring(int n_) : n(n_) {}
+  int n, slot, round;
+  __device__ explicit Ring(int n_, int slot_ = 0, int round_ = 0) : n(n_), slot(slot_), round(round_) {}
   __device__ void step() {
     if (++slot == n) {
       slot = 0;
@@ -122,7 +126,25 @@ struct Sched {
   long long off, count;
 };
 
-// One role's walk over the CTA's units; all lanes of a warp take the same steps.
+// A unit as it is posted.
+struct __align__(16) Unit {
+  int nt;                  // tiles (0: no more units)
+  int chunks, c0, c1;      // chunks of the request; the first that tile 0 / 1 takes part in
+  int flags;               // kBad ..
+  int rows, keys, pre;     // of the request, as in Request
+  int key0, h, o, L;
+  int n, mask_row;         // mask_indptr of the request
+  int k_slot, k_round;     // ring places of tile 0 ...
+  int k_slot1, k_round1;   // ... and 1,
+  int q_slot, q_round;     // of chunk c0,
+  int s0, s1;              // and numbers of the first products of tile 0 and 1
+  int pg0;                 // page table of the request
+  int pad[9];
+};
+static_assert(sizeof(Unit) == 128, "Unit");
+enum { kBad = 1, kFresh = 2, kLast = 4 };  // skipped; its chunks are loaded; its chunks' slots are given back
+
+// The walk over the CTA's units; all lanes of the warp take the same steps.
 struct Walk {
   const KeyWeightParams& p;
   const Sched& s;
@@ -229,6 +251,34 @@ __device__ __forceinline__ uint32_t idesc_n(int n) {
   return (1u << 4) | (FP8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
 }
 
+// D[tmem] = A B^T, K = D, from shared-memory descriptors of the operands' first
+// 16 columns: the next 16 lie 32 bytes on, the second 64 a half tile.
+template <int D>
+__device__ __forceinline__ void mma_tile(uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
+  constexpr int kHalf = kTile * 128 / 16;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n setp.ne.b32 p, %3, %3;\n"
+      " add.s64 a1, %1, 2;\n add.s64 b1, %2, 2;\n add.s64 a2, %1, 4;\n add.s64 b2, %2, 4;\n"
+      " add.s64 a3, %1, 6;\n add.s64 b3, %2, 6;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id)
+      : "memory");
+  if constexpr (D == 128)
+    asm volatile(
+        "{\n .reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n"
+        " add.s64 a0, %1, %4;\n add.s64 b0, %2, %4;\n add.s64 a1, a0, 2;\n add.s64 b1, b0, 2;\n"
+        " add.s64 a2, a0, 4;\n add.s64 b2, b0, 4;\n add.s64 a3, a0, 6;\n add.s64 b3, b0, 6;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %3, 1;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "n"(kHalf)
+        : "memory");
+}
+
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(const KeyWeightParams p) {
   using C = Cfg<D, FP8>;
@@ -244,6 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
   int2* const list = reinterpret_cast<int2*>(smem + C::OFF_LIST);
 
   if (tid == 0) {
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(bar(B_UF + i), 1);
+      mbar_init(bar(B_UE + i), kEpiWarps + 4 + 1);
+    }
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(B_SF + i), 1);
       mbar_init(bar(B_SE + i), 4);
@@ -352,76 +406,135 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
   }
   __syncthreads();
 
-  Walk w(p, sched, list);
-  const int nk = sorted ? C::K_SORTED : C::K_RUNS;
-  Ring kr(nk), qr(C::SLOTS - nk);  // of this role's next tile of K and chunk of q
-  int held[kResident], held_p[kResident];  // resident chunks: slot, parity
-  // the chunk's place: its own, or that of the next load
-  auto take_chunk = [&](int c, int* slot, int* parity) {
-    if (w.fresh || !w.resident()) {
-      *slot = nk + qr.slot;
-      *parity = qr.round & 1;
-      qr.step();
-      if (w.resident()) {
-        if (c == 0) held[0] = *slot, held_p[0] = *parity;
-        else held[1] = *slot, held_p[1] = *parity;
-      }
-    } else {
-      *slot = c == 0 ? held[0] : held[1];
-      *parity = c == 0 ? held_p[0] : held_p[1];
-    }
-  };
+  const int nk = sorted ? C::K_SORTED : C::K_RUNS, nq = C::SLOTS - nk;
+  Unit* const units = reinterpret_cast<Unit*>(smem + C::OFF_UNIT);
+  long long* const unit_rows = reinterpret_cast<long long*>(smem + C::OFF_ROW);
+  Ring ur(kQueue);   // this role's place in the queue
   bool live = true;
 
-  if (warp < kEpiWarps) {
+  if (warp == kWalkWarp) {
+    // ---------------- the walk ----------------
+    Walk w(p, sched, list);
+    Ring kr(nk), qr(nq), hold(nq);
+    int sn[2] = {0, 0};
+    while (live) {
+      const bool more = w.next();
+      const Request& rq = w.rq;
+      // the pages of the unit's keys, before the wait
+      long long row[8];
+      int bad_page = 0;
+      const int key0 = more ? w.key0() : 0, nt = more ? w.tiles_here() : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = key0 + i * 32 + lane;
+        row[i] = -1;
+        if (more && i < 4 * sched.kt && j < rq.keys && !rq.bad) {
+          const int src = w.source(j);
+          row[i] = w.row_of(w.page_of(src), src);
+          bad_page |= row[i] < 0;
+        }
+      }
+      if (bad_page && p.status) atomicOr(p.status, VA_DEV_BAD_PAGE);
+      if (more && rq.bad && lane == 0 && p.status) atomicOr(p.status, VA_DEV_BAD_TABLE);
+      if (ur.round > 0) live = warp_wait(bar(B_UE + ur.slot), (ur.round - 1) & 1, abort_flag);
+      if (!live) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) unit_rows[ur.slot * 2 * kTile + i * 32 + lane] = row[i];
+      if (lane == 0) {
+        Unit u;
+        u.nt = nt;
+        if (more) {
+          u.chunks = rq.chunks;
+          u.c0 = w.chunk0();
+          u.c1 = nt == 2 ? w.chunk0(1) : rq.chunks;
+          u.flags = (rq.bad ? kBad : 0) | (w.fresh || !w.resident() ? kFresh : 0) | (w.last || !w.resident() ? kLast : 0);
+          u.rows = rq.rows;
+          u.keys = rq.keys;
+          u.pre = rq.pre;
+          u.key0 = key0;
+          u.h = w.h;
+          u.o = rq.o;
+          u.L = rq.L;
+          u.pg0 = rq.pg0;
+          u.n = rq.n;
+          u.mask_row = p.mask ? p.mask_indptr[w.b] : 0;
+          if (rq.chunks > 0) {
+            u.k_slot = kr.slot;
+            u.k_round = kr.round;
+            kr.step();
+            u.k_slot1 = kr.slot;
+            u.k_round1 = kr.round;
+            if (nt == 2) kr.step();
+            if (u.flags & kFresh) {
+              hold = qr;
+              for (int c = u.c0; c < rq.chunks; ++c) qr.step();
+            }
+            u.q_slot = hold.slot;
+            u.q_round = hold.round;
+            u.s0 = sn[0];
+            u.s1 = sn[1];
+            sn[0] += rq.chunks - u.c0;
+            sn[1] += rq.chunks - u.c1;
+          }
+        }
+        units[ur.slot] = u;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_UF + ur.slot));
+      ur.step();
+      if (!more) break;
+    }
+  } else if (warp < kEpiWarps) {
     // ---------------- weights: one thread per key ----------------
     const int t = warp >> 2, slot = (warp & 3) * 32 + lane;
     const uint32_t cols = tmem + t * 256 + ((uint32_t)((warp & 3) * 32) << 16);
     const uint64_t scale = f32x2(p.scale_log2, p.scale_log2);
-    int page_next = -1;        // page of this thread's key of the next unit, when it is the next of this head
-    bool have_next = false;
-    int products = 0;
-    while (live && w.next()) {
-      const Request& rq = w.rq;
-      if (rq.bad) {
-        if (warp == 0 && lane == 0 && p.status) atomicOr(p.status, VA_DEV_BAD_TABLE);
-        have_next = false;
-        continue;
-      }
-      const int j = w.key0() + t * kTile + slot;
-      const bool here = t < w.tiles_here(), mine = here && j < rq.keys;
-      long long dst = -1;
+    while (live) {
+      live = warp_wait(bar(B_UF + ur.slot), ur.round & 1, abort_flag);
+      if (!live) break;
+      const Unit u = units[ur.slot];
+      long long dst = unit_rows[ur.slot * 2 * kTile + t * kTile + slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_UE + ur.slot));
+      ur.step();
+      if (u.nt == 0) break;
+      if (u.flags & kBad) continue;
+      const int j = u.key0 + t * kTile + slot;
+      const bool mine = t < u.nt && j < u.keys;
+      const int draft = j - u.pre, tile_last = u.key0 + t * kTile + kTile - 1;
       float old = 0.f;
-      if (mine) {
-        dst = w.row_of(have_next ? page_next : w.page_of(j), j);
-        const int src = w.source(j);
-        if (src != j && w.row_of(w.page_of(src), src) < 0) dst = -1;
-        if (dst < 0 && p.status) atomicOr(p.status, VA_DEV_BAD_PAGE);
-        if (dst >= 0 && j < rq.pre && p.decay != 0.f) old = p.key_weights[dst];
+      if (mine && dst >= 0) {
+        if (draft < 0) {
+          if (p.decay != 0.f) old = p.key_weights[dst];
+        } else if (p.accept_len) {   // read from the node's slot, weighed in the one that it moves to
+          const unsigned page = (unsigned)p.kv_indices[u.pg0 + (j >> p.log2_page)];
+          const long long at = j & (p.page_size - 1);
+          dst = page >= (unsigned)p.num_pages ? -1 : p.nhd ? ((long long)page * p.page_size + at) * p.h_kv + u.h
+                                                           : ((long long)page * p.h_kv + u.h) * p.page_size + at;
+          if (dst < 0 && p.status) atomicOr(p.status, VA_DEV_BAD_PAGE);
+        }
       }
-      have_next = !w.last;
-      if (have_next) page_next = j + kTile * sched.kt < rq.keys ? w.page_of(j + kTile * sched.kt) : -1;
-      const int draft = j - rq.pre, tile_last = w.key0() + t * kTile + kTile - 1;
       float sum = 0.f;
-      const int c_mine = here ? w.chunk0(t) : rq.chunks;
-      for (int c = w.chunk0(); live && c < rq.chunks; ++c) {
-        int qs, qp;
-        take_chunk(c, &qs, &qp);
+      Ring qr(nq, u.q_slot, u.q_round);
+      int product = t == 0 ? u.s0 : u.s1;
+      const int c_mine = t < u.nt ? (t == 0 ? u.c0 : u.c1) : u.chunks;
+      for (int c = u.c0; c < u.chunks; ++c) {
         // the chunk's lse are there; a warp that skips the chunk waits as well, so that it frees the slot in its turn
-        live = warp_wait(bar(B_FULL + qs), qp, abort_flag);
+        const int qs = qr.slot;
+        live = warp_wait(bar(B_FULL + nk + qs), qr.round & 1, abort_flag);
+        qr.step();
         if (!live) break;
         if (c >= c_mine) {
-          const int buf = products & 1;
-          live = warp_wait(bar(B_SF + t * 2 + buf), (products >> 1) & 1, abort_flag);
+          const int buf = product & 1;
+          live = warp_wait(bar(B_SF + t * 2 + buf), (product >> 1) & 1, abort_flag);
           if (!live) break;
-          ++products;
+          ++product;
           tc_fence_after();
-          const int r0 = c * kTile, nr = min(kTile, rq.rows - r0);
+          const int r0 = c * kTile, nr = min(kTile, u.rows - r0);
           // all rows of the chunk see all keys of the tile
-          const bool plain = p.mask ? !p.mask_full && tile_last < rq.pre
-                                    : (long long)(tile_last - rq.pre) * p.group <= r0;
+          const bool plain = p.mask ? !p.mask_full && tile_last < u.pre : (long long)(tile_last - u.pre) * p.group <= r0;
           const uint32_t at = cols + buf * kTile;
-          const float* const l2 = l2s + (qs - nk) * kTile;
+          const float* const l2 = l2s + qs * kTile;
           uint64_t acc0 = 0, acc1 = 0;
 #pragma unroll 1
           for (int k = 0; k * 32 < nr; ++k) {
@@ -447,9 +560,9 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
                   const int lo = draft <= 0 ? 0 : (int)min((long long)draft * p.group - first, 32ll);
                   on = lo >= 32 ? 0u : 0xffffffffu << max(lo, 0);
                 } else {
-                  const long long row0 = p.mask_indptr[w.b] + (p.mask_full ? j : draft);
-                  const int width = p.mask_full ? rq.keys : rq.L;
-                  for (int tok = first / p.group, e = tok * p.group - first; e < 32 && tok < rq.n; ++tok, e += p.group) {
+                  const long long row0 = u.mask_row + (p.mask_full ? j : draft);
+                  const int width = p.mask_full ? u.keys : u.L;
+                  for (int tok = first / p.group, e = tok * p.group - first; e < 32 && tok < u.n; ++tok, e += p.group) {
                     const long long bit = row0 + (long long)tok * width;
                     if ((p.mask[bit >> 3] >> (bit & 7)) & 1) {
                       const int z = min(e + p.group, 32);   // rows e .. z - 1 of this token
@@ -475,22 +588,22 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
           acc0 = add_f32x2(acc0, acc1);
           sum += f32x2_lo(acc0) + f32x2_hi(acc0);
         }
-        if (w.last || !w.resident()) {   // the chunk's lse have been read
+        if (u.flags & kLast) {   // the chunk's lse have been read
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_FREE + qs));
+          if (lane == 0) mbar_arrive(bar(B_FREE + nk + qs));
         }
       }
-      if (live && dst >= 0) p.key_weights[dst] = fmaf(p.decay, old, sum);
+      if (live && mine && dst >= 0) p.key_weights[dst] = fmaf(p.decay, old, sum);
     }
     tc_fence_before();
   } else if (warp < kMmaWarp) {
     // ---------------- loads ----------------
     constexpr int KCH = (FP8 ? D : 2 * D) / 16, QCH = 2 * D / 16;  // 16-byte chunks of a row
-    const int lw = warp - kLoadWarp, own = lw * 32 + lane;          // this thread's row of a tile
-    int p0 = 0, p1 = 0, p2 = 0, np = 0;  // loads under way, the oldest first: slot, and 8: a chunk of q
+    const int lw = warp - kLoadWarp, own = lw * 32 + lane;          // this thread's row of a chunk
+    int p0 = 0, p1 = 0, p2 = 0, np = 0;  // e4m3: loads under way, the oldest first: slot, and 8: a chunk of q
     Ring rr(kFlight), rf(kFlight);       // raw buffers: of the next load, of the next one widened
     Ring kf(nk);                         // the K slot that is widened into next
-    // the oldest load has landed: widen it, and pass it on
+    // e4m3: the oldest load has landed: widen it, and pass it on
     auto finish = [&]() {
       if (np == 3) cp_async_wait<2>();
       else if (np == 2) cp_async_wait<1>();
@@ -500,121 +613,111 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
       p0 = p1;
       p1 = p2;
       --np;
-      if constexpr (FP8) {
-        if (is_q) {
-          const uint32_t base = sbase + slot * C::OP;
+      if (is_q) {
+        const uint32_t base = sbase + slot * C::OP;
 #pragma unroll
-          for (int s = 0; s < QCH; ++s) {
-            const uint32_t a = op_addr(base, lw * 32 + s * (32 / QCH) + lane / QCH, lane % QCH);
-            uint4 v = lds128(a);
-            v.x = bf16x2_to_f16x2(v.x);
-            v.y = bf16x2_to_f16x2(v.y);
-            v.z = bf16x2_to_f16x2(v.z);
-            v.w = bf16x2_to_f16x2(v.w);
-            sts128(a, v);
-          }
-        } else {
-          slot = kf.slot;
-          if (kf.round > 0 && !warp_wait(bar(B_FREE + slot), (kf.round - 1) & 1, abort_flag)) {
-            live = false;
-            return;
-          }
-          kf.step();
-          const uint32_t raw = sbase + C::OFF_RAW + rf.slot * C::RAW, base = sbase + slot * C::OP;
-          rf.step();
+        for (int s = 0; s < QCH; ++s) {
+          const uint32_t a = op_addr(base, lw * 32 + s * (32 / QCH) + lane / QCH, lane % QCH);
+          uint4 v = lds128(a);
+          v.x = bf16x2_to_f16x2(v.x);
+          v.y = bf16x2_to_f16x2(v.y);
+          v.z = bf16x2_to_f16x2(v.z);
+          v.w = bf16x2_to_f16x2(v.w);
+          sts128(a, v);
+        }
+      } else {
+        slot = kf.slot;
+        if (kf.round > 0 && !warp_wait(bar(B_FREE + slot), (kf.round - 1) & 1, abort_flag)) {
+          live = false;
+          return;
+        }
+        kf.step();
+        const uint32_t raw = sbase + C::OFF_RAW + rf.slot * C::RAW, base = sbase + slot * C::OP;
+        rf.step();
 #pragma unroll
-          for (int s = 0; s < KCH; ++s) {
-            const int row = lw * 32 + s * (32 / KCH) + lane / KCH, ch = lane % KCH;
-            const uint4 v = lds128(raw + row * D + ((ch ^ (row & (KCH - 1))) << 4));
-            sts128(op_addr(base, row, 2 * ch), make_uint4(e4m3x2_to_f16x2((uint16_t)v.x), e4m3x2_to_f16x2((uint16_t)(v.x >> 16)),
-                                                          e4m3x2_to_f16x2((uint16_t)v.y), e4m3x2_to_f16x2((uint16_t)(v.y >> 16))));
-            sts128(op_addr(base, row, 2 * ch + 1), make_uint4(e4m3x2_to_f16x2((uint16_t)v.z), e4m3x2_to_f16x2((uint16_t)(v.z >> 16)),
-                                                              e4m3x2_to_f16x2((uint16_t)v.w), e4m3x2_to_f16x2((uint16_t)(v.w >> 16))));
-          }
+        for (int s = 0; s < KCH; ++s) {
+          const int row = lw * 32 + s * (32 / KCH) + lane / KCH, ch = lane % KCH;
+          const uint4 v = lds128(raw + row * D + ((ch ^ (row & (KCH - 1))) << 4));
+          sts128(op_addr(base, row, 2 * ch), make_uint4(e4m3x2_to_f16x2((uint16_t)v.x), e4m3x2_to_f16x2((uint16_t)(v.x >> 16)),
+                                                        e4m3x2_to_f16x2((uint16_t)v.y), e4m3x2_to_f16x2((uint16_t)(v.y >> 16))));
+          sts128(op_addr(base, row, 2 * ch + 1), make_uint4(e4m3x2_to_f16x2((uint16_t)v.z), e4m3x2_to_f16x2((uint16_t)(v.z >> 16)),
+                                                            e4m3x2_to_f16x2((uint16_t)v.w), e4m3x2_to_f16x2((uint16_t)(v.w >> 16))));
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_FULL + slot));
     };
-    // room for one more load under way
+    // e4m3: room for one more load under way
     auto room = [&]() {
-      if (np == kFlight) finish();
+      if constexpr (FP8)
+        if (np == kFlight) finish();
     };
     // wait for a buffer to be free: what its readers may wait for is passed on meanwhile
     auto wait_free = [&](uint32_t b, uint32_t parity) {
-      while (live && !__all_sync(0xffffffffu, mbar_try_wait(b, parity))) {
-        if (np > 0) finish();
-        else live = warp_wait(b, parity, abort_flag);
-      }
+      if constexpr (FP8)
+        while (live && np > 0 && !__all_sync(0xffffffffu, mbar_try_wait(b, parity))) finish();
+      if (live) live = warp_wait(b, parity, abort_flag);
     };
     // a load has been issued: its copies arrive at the barrier by themselves, or are widened when they have landed
     auto put = [&](int what) {
       if constexpr (!FP8) {
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(B_FULL + (what & 7))) : "memory");
-        return;
+      } else {
+        cp_async_commit();
+        if (np == 0) p0 = what;
+        else if (np == 1) p1 = what;
+        else p2 = what;
+        ++np;
       }
-      cp_async_commit();
-      if (np == 0) p0 = what;
-      else if (np == 1) p1 = what;
-      else p2 = what;
-      ++np;
     };
-    int page_next[2];
-    bool have_next = false;
-    while (live && w.next()) {
-      const Request& rq = w.rq;
-      if (rq.chunks == 0) {
-        have_next = false;
-        continue;
-      }
-      const int nt = w.tiles_here(), key0 = w.key0();
-      long long row[2] = {-1, -1};
-      int pg[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int j = key0 + t * kTile + own;
-        pg[t] = t < nt && j < rq.keys ? (have_next ? page_next[t] : w.page_of(w.source(j))) : -1;
-      }
-      have_next = !w.last;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int j = key0 + t * kTile + own, jn = j + sched.kt * kTile;
-        if (t < nt && j < rq.keys) row[t] = w.row_of(pg[t], w.source(j));
-        if (have_next) page_next[t] = t < sched.kt && jn < rq.keys ? w.page_of(w.source(jn)) : -1;
-      }
-      for (int t = 0; t < nt && live; ++t) {
-        room();
-        if constexpr (!FP8)
-          if (live && kr.round > 0) wait_free(bar(B_FREE + kr.slot), (kr.round - 1) & 1);
-        if (!live) break;
-        const uint32_t base = sbase + (FP8 ? C::OFF_RAW + rr.slot * C::RAW : kr.slot * C::OP);
-        const long long mine = t == 0 ? row[0] : row[1];
-#pragma unroll
-        for (int s = 0; s < KCH; ++s) {
-          const int from = s * (32 / KCH) + lane / KCH, r = lw * 32 + from, ch = lane % KCH;
-          const long long k = __shfl_sync(0xffffffffu, mine, from);
-          if (k >= 0)   // rows past the keys, and bad pages: whatever the buffer holds stays in its own lane
-            cp_async_16(FP8 ? base + r * D + ((ch ^ (r & (KCH - 1))) << 4) : op_addr(base, r, ch),
-                        static_cast<const uint8_t*>(p.k_cache) + (k * KCH + ch) * 16, 16);
-        }
-        put(kr.slot);
-        rr.step();
-        kr.step();
-      }
+    const uint8_t* const kbase = static_cast<const uint8_t*>(p.k_cache) + (lane % KCH) * 16;
+    const uint8_t* const qbase = static_cast<const uint8_t*>(p.q) + (lane % QCH) * 16;
+    while (live) {
+      // (posted units may be awaited for longer than the loads under way: pass those on first)
+      wait_free(bar(B_UF + ur.slot), ur.round & 1);
       if (!live) break;
-      if (w.resident() && !w.fresh) continue;
+      const Unit u = units[ur.slot];
+      const long long* const rows = unit_rows + ur.slot * 2 * kTile + lw * 32 + lane / KCH;
+      const int done = ur.slot;
+      ur.step();
+      if (u.nt > 0 && u.chunks > 0) {
+        for (int t = 0; t < u.nt && live; ++t) {
+          const int slot = t == 0 ? u.k_slot : u.k_slot1, round = t == 0 ? u.k_round : u.k_round1;
+          room();
+          if constexpr (!FP8)
+            if (live && round > 0) wait_free(bar(B_FREE + slot), (round - 1) & 1);
+          if (!live) break;
+          const uint32_t base = sbase + (FP8 ? C::OFF_RAW + rr.slot * C::RAW : slot * C::OP);
+          long long k[KCH];
+#pragma unroll
+          for (int s = 0; s < KCH; ++s) k[s] = rows[t * kTile + s * (32 / KCH)];
+#pragma unroll
+          for (int s = 0; s < KCH; ++s) {
+            const int r = lw * 32 + s * (32 / KCH) + lane / KCH, ch = lane % KCH;
+            if (k[s] >= 0)   // rows past the keys, and bad pages: whatever the buffer holds stays in its own lane
+              cp_async_16(FP8 ? base + r * D + ((ch ^ (r & (KCH - 1))) << 4) : op_addr(base, r, ch), kbase + k[s] * (KCH * 16), 16);
+          }
+          put(slot);
+          rr.step();
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_UE + done));
+      if (u.nt == 0) break;
+      if (!live || u.chunks == 0 || !(u.flags & kFresh)) continue;
       // row c of the chunks and its lse, one chunk ahead
       auto q_row = [&](int c) -> long long {
         const int r = c * kTile + own;
-        if (r >= rq.rows) return -1;
+        if (r >= u.rows) return -1;
         const int tok = r / p.group, g = r - tok * p.group;
-        const int node = p.accept_len ? min(max(p.path[rq.o + tok], 0), rq.L - 1) : tok;
-        return (long long)(rq.o + node) * p.h_q + w.h * p.group + g;
+        const int node = p.accept_len ? min(max(p.path[u.o + tok], 0), u.L - 1) : tok;
+        return (long long)(u.o + node) * p.h_q + u.h * p.group + g;
       };
-      long long qrow = q_row(w.chunk0());
+      Ring qr(nq, u.q_slot, u.q_round);
+      long long qrow = q_row(u.c0);
       float lse = qrow >= 0 ? p.lse[qrow] : -INFINITY;
-      for (int c = w.chunk0(); c < rq.chunks && live; ++c) {
-        const long long qnext = c + 1 < rq.chunks ? q_row(c + 1) : -1;
+      for (int c = u.c0; c < u.chunks && live; ++c) {
+        const long long qnext = c + 1 < u.chunks ? q_row(c + 1) : -1;
         const float lnext = qnext >= 0 ? p.lse[qnext] : -INFINITY;
         room();
         if (live && qr.round > 0) wait_free(bar(B_FREE + nk + qr.slot), (qr.round - 1) & 1);
@@ -622,10 +725,9 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         const uint32_t base = sbase + (nk + qr.slot) * C::OP;
 #pragma unroll
         for (int s = 0; s < QCH; ++s) {
-          const int from = s * (32 / QCH) + lane / QCH, ch = lane % QCH;
+          const int from = s * (32 / QCH) + lane / QCH;
           const long long k = __shfl_sync(0xffffffffu, qrow, from);
-          cp_async_16(op_addr(base, lw * 32 + from, ch),
-                      static_cast<const uint8_t*>(p.q) + (max(k, 0ll) * QCH + ch) * 16, k >= 0 ? 16 : 0);
+          cp_async_16(op_addr(base, lw * 32 + from, lane % QCH), qbase + max(k, 0ll) * (QCH * 16), k >= 0 ? 16 : 0);
         }
         // rows past the end, and rows that saw nothing, count nothing
         l2s[qr.slot * kTile + own] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
@@ -639,62 +741,54 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         lse = lnext;
       }
     }
-    while (np > 0 && live) finish();
+    if constexpr (FP8)
+      while (np > 0 && live) finish();
     cp_async_wait<0>();
-  } else {
-    // ---------------- products ----------------
-    int sn[2] = {0, 0};   // products so far of each tile
+  } else if (lane == 0) {
+    // ---------------- products: one thread ----------------
+    const uint64_t desc0 = smem_desc_sw128(0, 16, 1024);
     bool issued = false;
-    while (live && w.next()) {
-      const Request& rq = w.rq;
-      if (rq.chunks == 0) continue;
-      const int nt = w.tiles_here(), c1 = w.chunk0(1);
-      Ring ks[2] = {kr, kr};
-      kr.step();
-      if (nt == 2) {
-        ks[1] = kr;
-        kr.step();
-      }
-      const int c0 = w.chunk0();
-      for (int c = c0; live && c < rq.chunks; ++c) {
-        int qs, qp;
-        take_chunk(c, &qs, &qp);
-        if (w.fresh || !w.resident()) live = warp_wait(bar(B_FULL + qs), qp, abort_flag);
-        const uint32_t id = idesc_n<FP8>((min(kTile, rq.rows - c * kTile) + 15) & ~15);
+    while (live) {
+      live = mbar_wait(bar(B_UF + ur.slot), ur.round & 1, abort_flag);
+      if (!live) break;
+      const Unit& un = units[ur.slot];
+      const int nt = un.nt, chunks = un.chunks, c0 = un.c0, c1 = un.c1, rows = un.rows;
+      const bool last = un.flags & kLast;
+      const int ks[2] = {un.k_slot, un.k_slot1}, kround[2] = {un.k_round, un.k_round1};
+      int sn[2] = {un.s0, un.s1};
+      Ring qr(nq, un.q_slot, un.q_round);
+      mbar_arrive(bar(B_UE + ur.slot));
+      ur.step();
+      if (nt == 0) break;
+      for (int c = c0; live && c < chunks; ++c) {
+        const int qs = nk + qr.slot;
+        live = mbar_wait(bar(B_FULL + qs), qr.round & 1, abort_flag);
+        qr.step();
+        const uint32_t id = idesc_n<FP8>((min(kTile, rows - c * kTile) + 15) & ~15);
+        const uint64_t qd = desc0 + (uint64_t)((sbase + qs * C::OP) >> 4);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!live || t >= nt || (t == 1 && c < c1)) continue;
-          if (c == (t == 0 ? c0 : max(c0, c1))) live = warp_wait(bar(B_FULL + ks[t].slot), ks[t].round & 1, abort_flag);
+          if (c == (t == 0 ? c0 : c1)) live = mbar_wait(bar(B_FULL + ks[t]), kround[t] & 1, abort_flag);
           const int buf = sn[t] & 1;
-          if (live && sn[t] >= 2) live = warp_wait(bar(B_SE + t * 2 + buf), ((sn[t] >> 1) - 1) & 1, abort_flag);
+          if (live && sn[t] >= 2) live = mbar_wait(bar(B_SE + t * 2 + buf), ((sn[t] >> 1) - 1) & 1, abort_flag);
           if (!live) continue;
           ++sn[t];
-          if (lane == 0) {
-            tc_fence_after();
-            // what the copies and the loaders' stores left is there for the tensor cores: the fence stands here and not
-            // with the loaders, where it would wait for all their copies under way
-            fence_proxy_async();
-            const uint32_t ka = sbase + ks[t].slot * C::OP, qa = sbase + qs * C::OP;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = (k >> 2) * (kTile * 128) + (k & 3) * 32;
-              umma_bf16(tmem + t * 256 + buf * kTile, smem_desc_sw128(ka + off, 16, 1024), smem_desc_sw128(qa + off, 16, 1024),
-                        id, k > 0);
-            }
-            umma_commit(bar(B_SF + t * 2 + buf));
-            if (c == rq.chunks - 1) umma_commit(bar(B_FREE + ks[t].slot));
-          }
+          tc_fence_after();
+          // what the copies and the loaders' stores left is there for the tensor cores: the fence stands here and not
+          // with the loaders, where it would wait for all their copies under way
+          fence_proxy_async();
+          mma_tile<D>(tmem + t * 256 + buf * kTile, desc0 + (uint64_t)((sbase + ks[t] * C::OP) >> 4), qd, id);
+          umma_commit(bar(B_SF + t * 2 + buf));
+          if (c == chunks - 1) umma_commit(bar(B_FREE + ks[t]));
           issued = true;
-          __syncwarp();
         }
-        if (live && (w.last || !w.resident()) && lane == 0) umma_commit(bar(B_FREE + qs));
-        __syncwarp();
+        if (live && last) umma_commit(bar(B_FREE + qs));
       }
     }
     if (issued) {   // every commit has arrived before the CTA's shared memory goes away
-      if (lane == 0) umma_commit(bar(B_DONE));
-      __syncwarp();
-      warp_wait(bar(B_DONE), 0, abort_flag);
+      umma_commit(bar(B_DONE));
+      mbar_wait(bar(B_DONE), 0, abort_flag);
     }
   }
 
