@@ -223,10 +223,10 @@ struct Walk {
   }
   __device__ int page_of(int pos) const { return p.kv_indices[rq.pg0 + (pos >> p.log2_page)]; }
   __device__ long long row_of(int page, int pos) const {
-    if ((unsigned)page >= (unsigned)p.num_pages) return -1;
     const long long slot = pos & (p.page_size - 1);
-    return p.nhd ? ((long long)page * p.page_size + slot) * p.h_kv + h
-                 : ((long long)page * p.h_kv + h) * p.page_size + slot;
+    const long long row = p.nhd ? ((long long)page * p.page_size + slot) * p.h_kv + h
+                                : ((long long)page * p.h_kv + h) * p.page_size + slot;
+    return (unsigned)page < (unsigned)p.num_pages ? row : -1;
   }
 };
 
@@ -424,14 +424,23 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
       long long row[8];
       int bad_page = 0;
       const int key0 = more ? w.key0() : 0, nt = more ? w.tiles_here() : 0;
+      if (more && !rq.bad) {
+        // (all loads first, at clamped positions: behind a branch each they would wait for one another)
+        int src[8], page[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = key0 + i * 32 + lane;
-        row[i] = -1;
-        if (more && i < 4 * sched.kt && j < rq.keys && !rq.bad) {
-          const int src = w.source(j);
-          row[i] = w.row_of(w.page_of(src), src);
-          bad_page |= row[i] < 0;
+        for (int i = 0; i < 8; ++i) src[i] = min(key0 + i * 32 + lane, rq.keys - 1);
+        if (p.accept_len && key0 + 2 * kTile > rq.pre) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) src[i] = w.source(src[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) page[i] = w.page_of(src[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool on = i < 4 * sched.kt && key0 + i * 32 + lane < rq.keys;
+          row[i] = w.row_of(page[i], src[i]);
+          bad_page |= on && row[i] < 0;
+          if (!on) row[i] = -1;
         }
       }
       if (bad_page && p.status) atomicOr(p.status, VA_DEV_BAD_PAGE);
@@ -439,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
       if (ur.round > 0) live = warp_wait(bar(B_UE + ur.slot), (ur.round - 1) & 1, abort_flag);
       if (!live) break;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) unit_rows[ur.slot * 2 * kTile + i * 32 + lane] = row[i];
+      for (int i = 0; i < 8; ++i)
+        unit_rows[ur.slot * 2 * kTile + i * 32 + lane] = more && !rq.bad ? row[i] : -1;
       if (lane == 0) {
         Unit u;
         u.nt = nt;
