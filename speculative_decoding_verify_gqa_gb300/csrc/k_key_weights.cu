@@ -37,6 +37,7 @@
 // Units are dealt in runs of neighbours where rows are few: all cost the same
 // bytes.  Where a request has more than 256 rows they are sorted by their number
 // of chunks and dealt back and forth over the CTAs, the long ones first.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -57,7 +58,7 @@ constexpr int kLoadWarp = kEpiWarps, kMmaWarp = kLoadWarp + 4, kWalkWarp = kMmaW
 constexpr int kList = 512;    // units (of all heads) that are sorted
 constexpr int kResident = 2;  // chunks that stay in shared memory
 constexpr int kFlight = 3;    // e4m3: loads under way per loader thread
-constexpr int kQueue = 3;     // units posted ahead
+constexpr int kQueue = 6;     // units posted ahead
 
 template <int D, bool FP8>
 struct Cfg {
@@ -69,14 +70,14 @@ struct Cfg {
   static constexpr int SLOTS = FP8 ? 5 : 6;
   static constexpr int K_RUNS = SLOTS - kResident, K_SORTED = 2;
   static constexpr int OFF_RAW = SLOTS * OP, OFF_L2 = OFF_RAW + kFlight * RAW, OFF_LIST = OFF_L2 + (SLOTS - K_SORTED) * kTile * 4,
-                       OFF_UNIT = OFF_LIST + kList * 8, OFF_ROW = OFF_UNIT + kQueue * 128,
-                       OFF_BAR = OFF_ROW + kQueue * 2 * kTile * 8, SMEM = OFF_BAR + 256;
+                       OFF_UNIT = OFF_LIST + kList * 8, OFF_PAGE = OFF_UNIT + kQueue * 128,
+                       OFF_BAR = OFF_PAGE + kQueue * 2 * kTile * 4, SMEM = OFF_BAR + 512;
   static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
   static_assert(kList * 12 <= SLOTS * OP, "the unsorted list lies in the operand slots");
 };
 
 // Barriers: a slot full / free, products full / free, a unit posted / taken.
-enum { B_FULL = 0, B_FREE = 6, B_SF = 12, B_SE = 16, B_UF = 20, B_UE = 23, B_DONE = 26, B_COUNT = 27 };
+enum { B_FULL = 0, B_FREE = 6, B_SF = 12, B_SE = 16, B_UF = 20, B_UE = 26, B_RAW = 32, B_DONE = 35, B_COUNT = 36 };
 
 // A place in a ring of n slots and the parity of its round.
 struct Ring {
@@ -221,18 +222,20 @@ struct Walk {
   __device__ int source(int j) const {
     return !p.accept_len || j < rq.pre ? j : rq.pre + min(max(p.path[rq.o + j - rq.pre], 0), rq.L - 1);
   }
-  __device__ int page_of(int pos) const { return p.kv_indices[rq.pg0 + (pos >> p.log2_page)]; }
-  __device__ long long row_of(int page, int pos) const {
-    const long long slot = pos & (p.page_size - 1);
-    const long long row = p.nhd ? ((long long)page * p.page_size + slot) * p.h_kv + h
-                                : ((long long)page * p.h_kv + h) * p.page_size + slot;
-    return (unsigned)page < (unsigned)p.num_pages ? row : -1;
-  }
 };
+
+// cache row of KV head h at position pos of a page, or -1 for a page outside the pool
+__device__ __forceinline__ long long cache_row(const KeyWeightParams& p, int page, int pos, int h) {
+  const long long slot = pos & (p.page_size - 1);
+  const long long row = p.nhd ? ((long long)page * p.page_size + slot) * p.h_kv + h
+                              : ((long long)page * p.h_kv + h) * p.page_size + slot;
+  return (unsigned)page < (unsigned)p.num_pages ? row : -1;
+}
 
 __device__ __forceinline__ uint32_t op_addr(uint32_t base, int row, int chunk) {  // of a 16-byte chunk of an operand row
   return base + (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -244,6 +247,15 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
 // mbar_wait by a whole warp, with one answer
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+// Wait for the tensor-memory loads under way; the registers pass through, so
+// that nothing reads or moves them before.
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
 // f16 instruction descriptor: fp32 accumulator, both operands K-major
 template <bool FP8>
@@ -280,7 +292,8 @@ __device__ __forceinline__ void mma_tile(uint32_t d, uint64_t a, uint64_t b, uin
 }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(const KeyWeightParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    verify_attn_key_weights_kernel(const KeyWeightParams p, const __grid_constant__ CUtensorMap kmap) {
   using C = Cfg<D, FP8>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Sched sched;
@@ -295,9 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
 
   if (tid == 0) {
     for (int i = 0; i < kQueue; ++i) {
-      mbar_init(bar(B_UF + i), 1);
+      mbar_init(bar(B_UF + i), 32 + 1);
       mbar_init(bar(B_UE + i), kEpiWarps + 4 + 1);
     }
+    for (int i = 0; i < kFlight; ++i) mbar_init(bar(B_RAW + i), 4);
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(B_SF + i), 1);
       mbar_init(bar(B_SE + i), 4);
@@ -389,13 +403,13 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         run += __shfl_sync(0xffffffffu, sum, 31);
       }
     if (lane == 0) {
-      // Full: each warp's own arrival for what it has stored (a chunk's lse,
-      // widened rows), and each thread's asynchronous one behind its copies.
+      // Full: each loader warp's own arrival, for what it has stored (a chunk's
+      // lse, widened rows) and behind the asynchronous ones of its copies.
       // A chunk's slot is free when its products are done and the sums' warps
       // have read its lse.
       for (int i = 0; i < C::SLOTS; ++i) {
         const bool k = i < (sorted ? C::K_SORTED : C::K_RUNS);
-        mbar_init(bar(B_FULL + i), FP8 ? 4 : k ? 128 : 128 + 4);
+        mbar_init(bar(B_FULL + i), 4);
         mbar_init(bar(B_FREE + i), k ? 1 : 1 + kEpiWarps);
       }
       mbar_fence_init();
@@ -408,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
 
   const int nk = sorted ? C::K_SORTED : C::K_RUNS, nq = C::SLOTS - nk;
   Unit* const units = reinterpret_cast<Unit*>(smem + C::OFF_UNIT);
-  long long* const unit_rows = reinterpret_cast<long long*>(smem + C::OFF_ROW);
+  int* const unit_pages = reinterpret_cast<int*>(smem + C::OFF_PAGE);   // page of each key of a unit
   Ring ur(kQueue);   // this role's place in the queue
   bool live = true;
 
@@ -420,36 +434,22 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
     while (live) {
       const bool more = w.next();
       const Request& rq = w.rq;
-      // the pages of the unit's keys, before the wait
-      long long row[8];
-      int bad_page = 0;
-      const int key0 = more ? w.key0() : 0, nt = more ? w.tiles_here() : 0;
-      if (more && !rq.bad) {
-        // (all loads first, at clamped positions: behind a branch each they would wait for one another)
-        int src[8], page[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) src[i] = min(key0 + i * 32 + lane, rq.keys - 1);
-        if (p.accept_len && key0 + 2 * kTile > rq.pre) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) src[i] = w.source(src[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) page[i] = w.page_of(src[i]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool on = i < 4 * sched.kt && key0 + i * 32 + lane < rq.keys;
-          row[i] = w.row_of(page[i], src[i]);
-          bad_page |= on && row[i] < 0;
-          if (!on) row[i] = -1;
-        }
-      }
-      if (bad_page && p.status) atomicOr(p.status, VA_DEV_BAD_PAGE);
       if (more && rq.bad && lane == 0 && p.status) atomicOr(p.status, VA_DEV_BAD_TABLE);
       if (ur.round > 0) live = warp_wait(bar(B_UE + ur.slot), (ur.round - 1) & 1, abort_flag);
       if (!live) break;
+      const int key0 = more ? w.key0() : 0, nt = more ? w.tiles_here() : 0;
+      if (more && !rq.bad) {
+        // the pages of the unit's keys arrive by themselves: a load would take its turn behind all of the SM's copies
+        const bool moved = p.accept_len && key0 + 2 * kTile > rq.pre;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        unit_rows[ur.slot * 2 * kTile + i * 32 + lane] = more && !rq.bad ? row[i] : -1;
+        for (int i = 0; i < 8; ++i) {
+          if (i >= 4 * sched.kt) break;
+          const int j = min(key0 + i * 32 + lane, rq.keys - 1), src = moved ? w.source(j) : j;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                           sbase + C::OFF_PAGE + (ur.slot * 2 * kTile + i * 32 + lane) * 4),
+                       "l"(p.kv_indices + rq.pg0 + (src >> p.log2_page)));
+        }
+      }
       if (lane == 0) {
         Unit u;
         u.nt = nt;
@@ -489,21 +489,24 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         }
         units[ur.slot] = u;
       }
-      __syncwarp();
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(B_UF + ur.slot)) : "memory");
       if (lane == 0) mbar_arrive(bar(B_UF + ur.slot));
       ur.step();
       if (!more) break;
     }
+    cp_async_wait_all();
   } else if (warp < kEpiWarps) {
     // ---------------- weights: one thread per key ----------------
     const int t = warp >> 2, slot = (warp & 3) * 32 + lane;
     const uint32_t cols = tmem + t * 256 + ((uint32_t)((warp & 3) * 32) << 16);
     const uint64_t scale = f32x2(p.scale_log2, p.scale_log2);
+    long long late = -1;
+    float late_old = 0.f, late_sum = 0.f;
     while (live) {
       live = warp_wait(bar(B_UF + ur.slot), ur.round & 1, abort_flag);
       if (!live) break;
       const Unit u = units[ur.slot];
-      long long dst = unit_rows[ur.slot * 2 * kTile + t * kTile + slot];
+      int page = unit_pages[ur.slot * 2 * kTile + t * kTile + slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_UE + ur.slot));
       ur.step();
@@ -512,17 +515,16 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
       const int j = u.key0 + t * kTile + slot;
       const bool mine = t < u.nt && j < u.keys;
       const int draft = j - u.pre, tile_last = u.key0 + t * kTile + kTile - 1;
+      long long dst = -1;
       float old = 0.f;
-      if (mine && dst >= 0) {
-        if (draft < 0) {
-          if (p.decay != 0.f) old = p.key_weights[dst];
-        } else if (p.accept_len) {   // read from the node's slot, weighed in the one that it moves to
-          const unsigned page = (unsigned)p.kv_indices[u.pg0 + (j >> p.log2_page)];
-          const long long at = j & (p.page_size - 1);
-          dst = page >= (unsigned)p.num_pages ? -1 : p.nhd ? ((long long)page * p.page_size + at) * p.h_kv + u.h
-                                                           : ((long long)page * p.h_kv + u.h) * p.page_size + at;
-          if (dst < 0 && p.status) atomicOr(p.status, VA_DEV_BAD_PAGE);
-        }
+      if (mine) {
+        bool ok = (unsigned)page < (unsigned)p.num_pages;
+        // a key of the path is read from its node's slot and weighed in the one that it moves to
+        if (p.accept_len && draft >= 0) page = p.kv_indices[u.pg0 + (j >> p.log2_page)];
+        dst = cache_row(p, page, j, u.h);
+        if (!ok) dst = -1;
+        if (dst < 0 && p.status) atomicOr(p.status, VA_DEV_BAD_PAGE);
+        if (dst >= 0 && draft < 0 && p.decay != 0.f) old = p.key_weights[dst];
       }
       float sum = 0.f;
       Ring qr(nq, u.q_slot, u.q_round);
@@ -530,14 +532,19 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
       const int c_mine = t < u.nt ? (t == 0 ? u.c0 : u.c1) : u.chunks;
       for (int c = u.c0; c < u.chunks; ++c) {
         // the chunk's lse are there; a warp that skips the chunk waits as well, so that it frees the slot in its turn
-        const int qs = qr.slot;
-        live = warp_wait(bar(B_FULL + nk + qs), qr.round & 1, abort_flag);
+        const int qs = qr.slot, buf = product & 1;
+        const uint32_t bq = bar(B_FULL + nk + qs), bs = bar(B_SF + t * 2 + buf);
+        const uint32_t pq = qr.round & 1, ps = (product >> 1) & 1;
+        const bool part = c >= c_mine;
+        // (both at once: each takes a few hundred cycles to answer)
+        const bool hit_q = mbar_try_wait(bq, pq), hit_s = !part || mbar_try_wait(bs, ps);
+        if (!__all_sync(0xffffffffu, hit_q && hit_s)) {
+          live = warp_wait(bq, pq, abort_flag);
+          if (live && part) live = warp_wait(bs, ps, abort_flag);
+        }
         qr.step();
         if (!live) break;
-        if (c >= c_mine) {
-          const int buf = product & 1;
-          live = warp_wait(bar(B_SF + t * 2 + buf), (product >> 1) & 1, abort_flag);
-          if (!live) break;
+        if (part) {
           ++product;
           tc_fence_after();
           const int r0 = c * kTile, nr = min(kTile, u.rows - r0);
@@ -546,51 +553,57 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
           const uint32_t at = cols + buf * kTile;
           const float* const l2 = l2s + qs * kTile;
           uint64_t acc0 = 0, acc1 = 0;
-#pragma unroll 1
-          for (int k = 0; k * 32 < nr; ++k) {
-            uint32_t s[32];
-            tmem_ld32(at + k * 32, s);
-            tmem_wait_ld();
-            const float* const lk = l2 + k * 32;
-            if (plain && (k + 1) * 32 <= nr) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(lk + i);
-                const uint64_t a = fma_f32x2(f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale, l.x);
-                const uint64_t b = fma_f32x2(f32x2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scale, l.y);
-                acc0 = add_f32x2(acc0, f32x2(ex2(f32x2_lo(a)), ex2(f32x2_hi(a))));
-                acc1 = add_f32x2(acc1, f32x2(ex2(f32x2_lo(b)), ex2(f32x2_hi(b))));
-              }
+          // 16 rows: which of them see the key -- up to the chunk's end, from the causal border on, or by the mask
+          auto seen = [&](int k) -> uint32_t {
+            uint32_t on = 0;
+            if (!mine) return on;
+            const int first = r0 + k;
+            if (!p.mask || (!p.mask_full && draft < 0)) {
+              const int lo = draft <= 0 ? 0 : (int)min((long long)draft * p.group - first, 16ll);
+              on = 0xffffu << max(lo, 0);
             } else {
-              // which of the 32 rows see the key: up to the chunk's end, from the causal border on, or by the mask
-              uint32_t on = 0;
-              if (mine) {
-                const int first = r0 + k * 32;
-                if (!p.mask || (!p.mask_full && draft < 0)) {
-                  const int lo = draft <= 0 ? 0 : (int)min((long long)draft * p.group - first, 32ll);
-                  on = lo >= 32 ? 0u : 0xffffffffu << max(lo, 0);
-                } else {
-                  const long long row0 = u.mask_row + (p.mask_full ? j : draft);
-                  const int width = p.mask_full ? u.keys : u.L;
-                  for (int tok = first / p.group, e = tok * p.group - first; e < 32 && tok < u.n; ++tok, e += p.group) {
-                    const long long bit = row0 + (long long)tok * width;
-                    if ((p.mask[bit >> 3] >> (bit & 7)) & 1) {
-                      const int z = min(e + p.group, 32);   // rows e .. z - 1 of this token
-                      on |= (z == 32 ? 0xffffffffu : (1u << z) - 1u) & (0xffffffffu << max(e, 0));
-                    }
-                  }
-                }
-                if (nr - k * 32 < 32) on &= (1u << (nr - k * 32)) - 1u;
-              }
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(lk + i);
-                const uint64_t a = fma_f32x2(f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale, l.x);
-                const uint64_t b = fma_f32x2(f32x2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scale, l.y);
-                acc0 = add_f32x2(acc0, f32x2((on >> i) & 1 ? ex2(f32x2_lo(a)) : 0.f, (on >> (i + 1)) & 1 ? ex2(f32x2_hi(a)) : 0.f));
-                acc1 = add_f32x2(acc1, f32x2((on >> (i + 2)) & 1 ? ex2(f32x2_lo(b)) : 0.f, (on >> (i + 3)) & 1 ? ex2(f32x2_hi(b)) : 0.f));
+              const long long row0 = u.mask_row + (p.mask_full ? j : draft);
+              const int width = p.mask_full ? u.keys : u.L;
+              for (int tok = first / p.group, e = tok * p.group - first; e < 16 && tok < u.n; ++tok, e += p.group) {
+                const long long bit = row0 + (long long)tok * width;
+                if ((p.mask[bit >> 3] >> (bit & 7)) & 1)   // rows e .. e + group - 1, those among the 16
+                  on |= ((1u << min(e + p.group, 16)) - 1u) & (0xffffu << max(e, 0));
               }
             }
+            return nr - k < 16 ? on & ((1u << max(nr - k, 0)) - 1u) : on;
+          };
+          auto add = [&](const uint32_t (&s)[16], int k) {
+            const float* const lk = l2 + k;
+            const uint32_t on = plain && k + 16 <= nr ? 0xffffu : seen(k);
+            const bool all = plain && k + 16 <= nr;
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(lk + i);
+              const uint64_t a = fma_f32x2(f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale, l.x);
+              const uint64_t b = fma_f32x2(f32x2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scale, l.y);
+              float e0 = ex2(f32x2_lo(a)), e1 = ex2(f32x2_hi(a)), e2 = ex2(f32x2_lo(b)), e3 = ex2(f32x2_hi(b));
+              if (!all) {
+                e0 = (on >> i) & 1 ? e0 : 0.f;
+                e1 = (on >> (i + 1)) & 1 ? e1 : 0.f;
+                e2 = (on >> (i + 2)) & 1 ? e2 : 0.f;
+                e3 = (on >> (i + 3)) & 1 ? e3 : 0.f;
+              }
+              acc0 = add_f32x2(acc0, f32x2(e0, e1));
+              acc1 = add_f32x2(acc1, f32x2(e2, e3));
+            }
+          };
+          // the next 16 columns come in while these are added
+          uint32_t x[16], y[16];
+          tmem_ld16(at, x);
+          tmem_wait16(x);
+#pragma unroll 1
+          for (int k = 0; k < nr; k += 32) {
+            tmem_ld16(at + k + 16, y);
+            add(x, k);
+            tmem_wait16(y);
+            if (k + 32 < nr) tmem_ld16(at + k + 32, x);
+            add(y, k + 16);
+            tmem_wait16(x);
           }
           tc_fence_before();
           __syncwarp();
@@ -603,27 +616,30 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
           if (lane == 0) mbar_arrive(bar(B_FREE + nk + qs));
         }
       }
-      if (live && mine && dst >= 0) p.key_weights[dst] = fmaf(p.decay, old, sum);
+      // the store of the unit before, whose old weight has had this unit's time to arrive
+      if (late >= 0) p.key_weights[late] = fmaf(p.decay, late_old, late_sum);
+      late = live ? dst : -1;
+      late_old = old;
+      late_sum = sum;
     }
+    if (late >= 0) p.key_weights[late] = fmaf(p.decay, late_old, late_sum);
     tc_fence_before();
   } else if (warp < kMmaWarp) {
     // ---------------- loads ----------------
     constexpr int KCH = (FP8 ? D : 2 * D) / 16, QCH = 2 * D / 16;  // 16-byte chunks of a row
     const int lw = warp - kLoadWarp, own = lw * 32 + lane;          // this thread's row of a chunk
     int p0 = 0, p1 = 0, p2 = 0, np = 0;  // e4m3: loads under way, the oldest first: slot, and 8: a chunk of q
-    Ring rr(kFlight), rf(kFlight);       // raw buffers: of the next load, of the next one widened
+    Ring rr(kFlight), rf(kFlight);       // e4m3: raw buffers of the next load, of the next one widened
     Ring kf(nk);                         // the K slot that is widened into next
     // e4m3: the oldest load has landed: widen it, and pass it on
     auto finish = [&]() {
-      if (np == 3) cp_async_wait<2>();
-      else if (np == 2) cp_async_wait<1>();
-      else cp_async_wait<0>();
       int slot = p0 & 7;
       const bool is_q = p0 & 8;
       p0 = p1;
       p1 = p2;
       --np;
       if (is_q) {
+        cp_async_wait_all();
         const uint32_t base = sbase + slot * C::OP;
 #pragma unroll
         for (int s = 0; s < QCH; ++s) {
@@ -637,6 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         }
       } else {
         slot = kf.slot;
+        live = warp_wait(bar(B_RAW + rf.slot), rf.round & 1, abort_flag);
+        if (!live) return;
         if (kf.round > 0 && !warp_wait(bar(B_FREE + slot), (kf.round - 1) & 1, abort_flag)) {
           live = false;
           return;
@@ -647,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
 #pragma unroll
         for (int s = 0; s < KCH; ++s) {
           const int row = lw * 32 + s * (32 / KCH) + lane / KCH, ch = lane % KCH;
-          const uint4 v = lds128(raw + row * D + ((ch ^ (row & (KCH - 1))) << 4));
+          const uint4 v = lds128(raw + row * D + (ch << 4));
           sts128(op_addr(base, row, 2 * ch), make_uint4(e4m3x2_to_f16x2((uint16_t)v.x), e4m3x2_to_f16x2((uint16_t)(v.x >> 16)),
                                                         e4m3x2_to_f16x2((uint16_t)v.y), e4m3x2_to_f16x2((uint16_t)(v.y >> 16))));
           sts128(op_addr(base, row, 2 * ch + 1), make_uint4(e4m3x2_to_f16x2((uint16_t)v.z), e4m3x2_to_f16x2((uint16_t)(v.z >> 16)),
@@ -668,17 +686,18 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         while (live && np > 0 && !__all_sync(0xffffffffu, mbar_try_wait(b, parity))) finish();
       if (live) live = warp_wait(b, parity, abort_flag);
     };
-    // a load has been issued: its copies arrive at the barrier by themselves, or are widened when they have landed
+    // e4m3: one more load under way
     auto put = [&](int what) {
-      if constexpr (!FP8) {
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(B_FULL + (what & 7))) : "memory");
-      } else {
-        cp_async_commit();
-        if (np == 0) p0 = what;
-        else if (np == 1) p1 = what;
-        else p2 = what;
-        ++np;
-      }
+      if (np == 0) p0 = what;
+      else if (np == 1) p1 = what;
+      else p2 = what;
+      ++np;
+    };
+    // the warp's arrival behind the asynchronous ones of its copies so far
+    auto arrive_behind = [&](uint32_t b) {
+      asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(b) : "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b);
     };
     const uint8_t* const kbase = static_cast<const uint8_t*>(p.k_cache) + (lane % KCH) * 16;
     const uint8_t* const qbase = static_cast<const uint8_t*>(p.q) + (lane % QCH) * 16;
@@ -687,7 +706,6 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
       wait_free(bar(B_UF + ur.slot), ur.round & 1);
       if (!live) break;
       const Unit u = units[ur.slot];
-      const long long* const rows = unit_rows + ur.slot * 2 * kTile + lw * 32 + lane / KCH;
       const int done = ur.slot;
       ur.step();
       if (u.nt > 0 && u.chunks > 0) {
@@ -698,16 +716,43 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
             if (live && round > 0) wait_free(bar(B_FREE + slot), (round - 1) & 1);
           if (!live) break;
           const uint32_t base = sbase + (FP8 ? C::OFF_RAW + rr.slot * C::RAW : slot * C::OP);
-          long long k[KCH];
-#pragma unroll
-          for (int s = 0; s < KCH; ++s) k[s] = rows[t * kTile + s * (32 / KCH)];
-#pragma unroll
-          for (int s = 0; s < KCH; ++s) {
-            const int r = lw * 32 + s * (32 / KCH) + lane / KCH, ch = lane % KCH;
-            if (k[s] >= 0)   // rows past the keys, and bad pages: whatever the buffer holds stays in its own lane
-              cp_async_16(FP8 ? base + r * D + ((ch ^ (r & (KCH - 1))) << 4) : op_addr(base, r, ch), kbase + k[s] * (KCH * 16), 16);
+          const uint32_t full = bar(FP8 ? B_RAW + rr.slot : B_FULL + slot);
+          const int tile0 = u.key0 + t * kTile;
+          const int* const pages = unit_pages + done * 2 * kTile + t * kTile + lw * 32;
+          const bool moved = p.accept_len && tile0 + kTile > u.pre;
+          if (p.box > 0 && !moved) {
+            // whole pages, or 32 rows of one: lane i copies the box of rows i * box ..
+            const int r = lane * p.box, j = tile0 + lw * 32 + r;
+            const int page = lane * p.box < 32 && j < u.keys ? pages[r] : -1;
+            const bool on = (unsigned)page < (unsigned)p.num_pages;   // (the others: whatever the buffer holds stays in its own lane)
+            const int n = __popc(__ballot_sync(0xffffffffu, on));
+            if (lane == 0) {
+              if (n > 0) mbar_expect_tx(full, n * p.box * (FP8 ? D : 2 * D));
+              else mbar_arrive(full);
+            }
+            __syncwarp();
+            if (on) {
+              const int at = j & (p.page_size - 1), row = lw * 32 + r;
+              if constexpr (FP8) {
+                tma_load_4d(base + row * D, &kmap, 0, at, u.h, page, full);
+              } else {
+                tma_load_4d(base + row * 128, &kmap, 0, at, u.h, page, full);
+                if constexpr (D == 128) tma_load_4d(base + kTile * 128 + row * 128, &kmap, 64, at, u.h, page, full);
+              }
+            }
+          } else {
+#pragma unroll 4
+            for (int s = 0; s < KCH; ++s) {
+              const int i = s * (32 / KCH) + lane / KCH, r = lw * 32 + i, j = tile0 + r, ch = lane % KCH;
+              if (j < u.keys) {
+                const int src = moved && j >= u.pre ? u.pre + min(max(p.path[u.o + j - u.pre], 0), u.L - 1) : j;
+                const long long k = cache_row(p, pages[i], src, u.h);
+                if (k >= 0) cp_async_16(FP8 ? base + r * D + (ch << 4) : op_addr(base, r, ch), kbase + k * (KCH * 16), 16);
+              }
+            }
+            arrive_behind(full);
           }
-          put(slot);
+          if constexpr (FP8) put(slot);
           rr.step();
         }
       }
@@ -741,11 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
         }
         // rows past the end, and rows that saw nothing, count nothing
         l2s[qr.slot * kTile + own] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-        if constexpr (!FP8) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_FULL + nk + qr.slot));
-        }
-        put(8 | (nk + qr.slot));
+        if constexpr (FP8) put(8 | (nk + qr.slot));
+        else arrive_behind(bar(B_FULL + nk + qr.slot));
         qr.step();
         qrow = qnext;
         lse = lnext;
@@ -753,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
     }
     if constexpr (FP8)
       while (np > 0 && live) finish();
-    cp_async_wait<0>();
+    cp_async_wait_all();
   } else if (lane == 0) {
     // ---------------- products: one thread ----------------
     const uint64_t desc0 = smem_desc_sw128(0, 16, 1024);
@@ -811,20 +853,21 @@ __global__ void __launch_bounds__(kThreads, 1) verify_attn_key_weights_kernel(co
 }
 
 template <int D, bool FP8>
-cudaError_t launch(const KeyWeightParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const KeyWeightParams& p, const CUtensorMap& kmap, int num_sms, cudaStream_t stream) {
   using C = Cfg<D, FP8>;
   const void* k = reinterpret_cast<const void*>(verify_attn_key_weights_kernel<D, FP8>);
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  void* args[] = {const_cast<KeyWeightParams*>(&p)};
+  void* args[] = {const_cast<KeyWeightParams*>(&p), const_cast<CUtensorMap*>(&kmap)};
   return launch_kernel(k, dim3((unsigned)num_sms), dim3(kThreads), C::SMEM, stream, args, /*pdl=*/true);
 }
 
 }  // namespace
 
-cudaError_t launch_key_weights(const KeyWeightParams& p, int head_dim, bool kv_fp8, int num_sms, cudaStream_t stream) {
-  if (head_dim == 64) return kv_fp8 ? launch<64, true>(p, num_sms, stream) : launch<64, false>(p, num_sms, stream);
-  return kv_fp8 ? launch<128, true>(p, num_sms, stream) : launch<128, false>(p, num_sms, stream);
+cudaError_t launch_key_weights(const KeyWeightParams& p, const CUtensorMap& kmap, int head_dim, bool kv_fp8,
+                               int num_sms, cudaStream_t stream) {
+  if (head_dim == 64) return kv_fp8 ? launch<64, true>(p, kmap, num_sms, stream) : launch<64, false>(p, kmap, num_sms, stream);
+  return kv_fp8 ? launch<128, true>(p, kmap, num_sms, stream) : launch<128, false>(p, kmap, num_sms, stream);
 }
 
 }  // namespace va

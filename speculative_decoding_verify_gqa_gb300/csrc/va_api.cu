@@ -1279,7 +1279,25 @@ int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* k
   p.mask_full = mask_layout == VA_MASK_FULL;
   p.scale_log2 = scale * k_scale * 1.4426950408889634f;
   p.decay = decay;
-  cudaError_t e = launch_key_weights(p, head_dim, kv_dtype == VA_DTYPE_FP8_E4M3, num_sms,
+  CUtensorMap kmap;
+  memset(&kmap, 0, sizeof(kmap));
+  // boxes of 8 to 32 slots; pages of fewer are copied row by row
+  p.box = page_size < 8 ? 0 : std::min(page_size, 32);
+  if (p.box) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return VA_ERR_CUDA;
+    const bool fp8 = kv_dtype == VA_DTYPE_FP8_E4M3;
+    const cuuint64_t row = (cuuint64_t)head_dim * (fp8 ? 1 : 2), H = num_kv_heads, P = page_size;
+    const cuuint64_t dims[4] = {(cuuint64_t)head_dim, P, H, (cuuint64_t)num_pages};
+    const cuuint64_t strides[3] = {p.nhd ? H * row : row, p.nhd ? row : P * row, H * P * row};
+    const cuuint32_t boxes[4] = {fp8 ? (cuuint32_t)head_dim : 64u, (cuuint32_t)p.box, 1, 1}, step[4] = {1, 1, 1, 1};
+    if (enc(&kmap, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(k_cache),
+            dims, strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return VA_ERR_CUDA;
+  }
+  cudaError_t e = launch_key_weights(p, kmap, head_dim, kv_dtype == VA_DTYPE_FP8_E4M3, num_sms,
                                      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }

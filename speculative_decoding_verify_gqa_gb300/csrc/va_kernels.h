@@ -211,8 +211,12 @@ struct KeyWeightParams {
   int nhd, mask_full;
   float scale_log2;           // sm_scale * k_scale * log2(e)
   float decay;
+  int box;                    // rows of a box of the K map (0: no map, rows are copied one by one)
 };
-cudaError_t launch_key_weights(const KeyWeightParams& p, int head_dim, bool kv_fp8, int num_sms, cudaStream_t stream);
+// kmap: the K cache as [page][head][slot][element], boxes of `box` slots of one
+// head: 64 bf16 columns with 128-byte swizzle, or whole e4m3 rows.
+cudaError_t launch_key_weights(const KeyWeightParams& p, const CUtensorMap& kmap, int head_dim, bool kv_fp8,
+                               int num_sms, cudaStream_t stream);
 
 // Eviction of the keys with the least weight (see k_evict.cu).
 constexpr int kEvictMaxKeys = 1 << 19;  // keys of a request: a bit and a count per word in shared memory
