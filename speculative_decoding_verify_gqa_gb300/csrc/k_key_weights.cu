@@ -77,7 +77,7 @@ struct Cfg {
 };
 
 // Barriers: a slot full / free, products full / free, a unit posted / taken.
-enum { B_FULL = 0, B_FREE = 6, B_SF = 12, B_SE = 16, B_UF = 20, B_UE = 26, B_RAW = 32, B_DONE = 35, B_COUNT = 36 };
+enum { B_FULL = 0, B_FREE = 6, B_SF = 12, B_SE = 14, B_UF = 16, B_UE = 22, B_RAW = 28, B_DONE = 31, B_COUNT = 32 };
 
 // A place in a ring of n slots and the parity of its round.
 struct Ring {
@@ -138,9 +138,9 @@ struct __align__(16) Unit {
   int k_slot, k_round;     // ring places of tile 0 ...
   int k_slot1, k_round1;   // ... and 1,
   int q_slot, q_round;     // of chunk c0,
-  int s0, s1;              // and numbers of the first products of tile 0 and 1
+  int s0;                  // and number of the first products
   int pg0;                 // page table of the request
-  int pad[9];
+  int pad[10];
 };
 static_assert(sizeof(Unit) == 128, "Unit");
 enum { kBad = 1, kFresh = 2, kLast = 4 };  // skipped; its chunks are loaded; its chunks' slots are given back
@@ -250,10 +250,12 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 // Wait for the tensor-memory loads under way; the registers pass through, so
 // that nothing reads or moves them before.
-__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_wait32(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
 }
@@ -312,9 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_UE + i), kEpiWarps + 4 + 1);
     }
     for (int i = 0; i < kFlight; ++i) mbar_init(bar(B_RAW + i), 4);
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_SF + i), 1);
-      mbar_init(bar(B_SE + i), 4);
+      mbar_init(bar(B_SE + i), kEpiWarps);
     }
     mbar_init(bar(B_DONE), 1);
     abort_shared = 0;
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- the walk ----------------
     Walk w(p, sched, list);
     Ring kr(nk), qr(nq), hold(nq);
-    int sn[2] = {0, 0};
+    int sn = 0;
     while (live) {
       const bool more = w.next();
       const Request& rq = w.rq;
@@ -481,10 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             u.q_slot = hold.slot;
             u.q_round = hold.round;
-            u.s0 = sn[0];
-            u.s1 = sn[1];
-            sn[0] += rq.chunks - u.c0;
-            sn[1] += rq.chunks - u.c1;
+            u.s0 = sn;
+            sn += rq.chunks - u.c0;
           }
         }
         units[ur.slot] = u;
@@ -528,24 +528,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float sum = 0.f;
       Ring qr(nq, u.q_slot, u.q_round);
-      int product = t == 0 ? u.s0 : u.s1;
+      int product = u.s0;
       const int c_mine = t < u.nt ? (t == 0 ? u.c0 : u.c1) : u.chunks;
       for (int c = u.c0; c < u.chunks; ++c) {
-        // the chunk's lse are there; a warp that skips the chunk waits as well, so that it frees the slot in its turn
+        // the chunk's lse are there, and the products; a warp whose tile skips the chunk keeps in step
         const int qs = qr.slot, buf = product & 1;
-        const uint32_t bq = bar(B_FULL + nk + qs), bs = bar(B_SF + t * 2 + buf);
+        const uint32_t bq = bar(B_FULL + nk + qs), bs = bar(B_SF + buf);
         const uint32_t pq = qr.round & 1, ps = (product >> 1) & 1;
-        const bool part = c >= c_mine;
         // (both at once: each takes a few hundred cycles to answer)
-        const bool hit_q = mbar_try_wait(bq, pq), hit_s = !part || mbar_try_wait(bs, ps);
+        const bool hit_q = mbar_try_wait(bq, pq), hit_s = mbar_try_wait(bs, ps);
         if (!__all_sync(0xffffffffu, hit_q && hit_s)) {
           live = warp_wait(bq, pq, abort_flag);
-          if (live && part) live = warp_wait(bs, ps, abort_flag);
+          if (live) live = warp_wait(bs, ps, abort_flag);
         }
         qr.step();
         if (!live) break;
-        if (part) {
-          ++product;
+        ++product;
+        if (c >= c_mine) {
           tc_fence_after();
           const int r0 = c * kTile, nr = min(kTile, u.rows - r0);
           // all rows of the chunk see all keys of the tile
@@ -553,67 +552,82 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t at = cols + buf * kTile;
           const float* const l2 = l2s + qs * kTile;
           uint64_t acc0 = 0, acc1 = 0;
-          // 16 rows: which of them see the key -- up to the chunk's end, from the causal border on, or by the mask
+          // 32 rows: which of them see the key -- up to the chunk's end, from the causal border on, or by the mask
           auto seen = [&](int k) -> uint32_t {
             uint32_t on = 0;
             if (!mine) return on;
             const int first = r0 + k;
             if (!p.mask || (!p.mask_full && draft < 0)) {
-              const int lo = draft <= 0 ? 0 : (int)min((long long)draft * p.group - first, 16ll);
-              on = 0xffffu << max(lo, 0);
+              const int lo = draft <= 0 ? 0 : (int)min((long long)draft * p.group - first, 32ll);
+              on = lo >= 32 ? 0u : 0xffffffffu << max(lo, 0);
             } else {
               const long long row0 = u.mask_row + (p.mask_full ? j : draft);
               const int width = p.mask_full ? u.keys : u.L;
-              for (int tok = first / p.group, e = tok * p.group - first; e < 16 && tok < u.n; ++tok, e += p.group) {
+              for (int tok = first / p.group, e = tok * p.group - first; e < 32 && tok < u.n; ++tok, e += p.group) {
                 const long long bit = row0 + (long long)tok * width;
-                if ((p.mask[bit >> 3] >> (bit & 7)) & 1)   // rows e .. e + group - 1, those among the 16
-                  on |= ((1u << min(e + p.group, 16)) - 1u) & (0xffffu << max(e, 0));
+                if ((p.mask[bit >> 3] >> (bit & 7)) & 1) {   // rows e .. e + group - 1, those among the 32
+                  const int z = min(e + p.group, 32);
+                  on |= (z == 32 ? 0xffffffffu : (1u << z) - 1u) & (0xffffffffu << max(e, 0));
+                }
               }
             }
-            return nr - k < 16 ? on & ((1u << max(nr - k, 0)) - 1u) : on;
+            return nr - k < 32 ? on & ((1u << max(nr - k, 0)) - 1u) : on;
           };
-          auto add = [&](const uint32_t (&s)[16], int k) {
-            const float* const lk = l2 + k;
-            const uint32_t on = plain && k + 16 <= nr ? 0xffffu : seen(k);
-            const bool all = plain && k + 16 <= nr;
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(lk + i);
-              const uint64_t a = fma_f32x2(f32x2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale, l.x);
-              const uint64_t b = fma_f32x2(f32x2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), scale, l.y);
-              float e0 = ex2(f32x2_lo(a)), e1 = ex2(f32x2_hi(a)), e2 = ex2(f32x2_lo(b)), e3 = ex2(f32x2_hi(b));
-              if (!all) {
-                e0 = (on >> i) & 1 ? e0 : 0.f;
-                e1 = (on >> (i + 1)) & 1 ? e1 : 0.f;
-                e2 = (on >> (i + 2)) & 1 ? e2 : 0.f;
-                e3 = (on >> (i + 3)) & 1 ? e3 : 0.f;
-              }
-              acc0 = add_f32x2(acc0, f32x2(e0, e1));
-              acc1 = add_f32x2(acc1, f32x2(e2, e3));
-            }
+          // two logits at a time: 2^(s c - lse log2 e)
+          auto weight = [&](uint32_t s0, uint32_t s1, uint64_t l) {
+            return fma_f32x2(f32x2(__uint_as_float(s0), __uint_as_float(s1)), scale, l);
           };
-          // the next 16 columns come in while these are added
-          uint32_t x[16], y[16];
-          tmem_ld16(at, x);
-          tmem_wait16(x);
+          int k = 0;
+          if (plain) {
+            // (64 columns at a time: with 32 the way in and out of tensor memory is what a prompt waits for)
 #pragma unroll 1
-          for (int k = 0; k < nr; k += 32) {
-            tmem_ld16(at + k + 16, y);
-            add(x, k);
-            tmem_wait16(y);
-            if (k + 32 < nr) tmem_ld16(at + k + 32, x);
-            add(y, k + 16);
-            tmem_wait16(x);
+            for (; k + 64 <= nr; k += 64) {
+              uint32_t x[64];
+              tmem_ld32(at + k, x);
+              tmem_ld32(at + k + 32, x + 32);
+              tmem_wait32(x);
+              tmem_wait32(x + 32);
+#pragma unroll
+              for (int i = 0; i < 64; i += 4) {
+                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(l2 + k + i);
+                const uint64_t a = weight(x[i], x[i + 1], l.x), b = weight(x[i + 2], x[i + 3], l.y);
+                acc0 = add_f32x2(acc0, f32x2(ex2(f32x2_lo(a)), ex2(f32x2_hi(a))));
+                acc1 = add_f32x2(acc1, f32x2(ex2(f32x2_lo(b)), ex2(f32x2_hi(b))));
+              }
+            }
+          }
+#pragma unroll 1
+          for (; k < nr; k += 32) {
+            uint32_t x[32];
+            tmem_ld32(at + k, x);
+            tmem_wait32(x);
+            if (plain && k + 32 <= nr) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(l2 + k + i);
+                const uint64_t a = weight(x[i], x[i + 1], l.x), b = weight(x[i + 2], x[i + 3], l.y);
+                acc0 = add_f32x2(acc0, f32x2(ex2(f32x2_lo(a)), ex2(f32x2_hi(a))));
+                acc1 = add_f32x2(acc1, f32x2(ex2(f32x2_lo(b)), ex2(f32x2_hi(b))));
+              }
+              continue;
+            }
+            const uint32_t on = seen(k);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(l2 + k + i);
+              const uint64_t a = weight(x[i], x[i + 1], l.x), b = weight(x[i + 2], x[i + 3], l.y);
+              acc0 = add_f32x2(acc0, f32x2((on >> i) & 1 ? ex2(f32x2_lo(a)) : 0.f, (on >> (i + 1)) & 1 ? ex2(f32x2_hi(a)) : 0.f));
+              acc1 = add_f32x2(acc1, f32x2((on >> (i + 2)) & 1 ? ex2(f32x2_lo(b)) : 0.f, (on >> (i + 3)) & 1 ? ex2(f32x2_hi(b)) : 0.f));
+            }
           }
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_SE + t * 2 + buf));
           acc0 = add_f32x2(acc0, acc1);
           sum += f32x2_lo(acc0) + f32x2_hi(acc0);
         }
-        if (u.flags & kLast) {   // the chunk's lse have been read
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_FREE + nk + qs));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(B_SE + buf));
+          if (u.flags & kLast) mbar_arrive(bar(B_FREE + nk + qs));   // the chunk's lse have been read
         }
       }
       // the store of the unit before, whose old weight has had this unit's time to arrive
@@ -662,10 +676,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         kf.step();
         const uint32_t raw = sbase + C::OFF_RAW + rf.slot * C::RAW, base = sbase + slot * C::OP;
         rf.step();
+        uint4 raws[KCH];   // (all loads first)
+#pragma unroll
+        for (int s = 0; s < KCH; ++s)
+          raws[s] = lds128(raw + (lw * 32 + s * (32 / KCH) + lane / KCH) * D + ((lane % KCH) << 4));
 #pragma unroll
         for (int s = 0; s < KCH; ++s) {
           const int row = lw * 32 + s * (32 / KCH) + lane / KCH, ch = lane % KCH;
-          const uint4 v = lds128(raw + row * D + (ch << 4));
+          const uint4 v = raws[s];
           sts128(op_addr(base, row, 2 * ch), make_uint4(e4m3x2_to_f16x2((uint16_t)v.x), e4m3x2_to_f16x2((uint16_t)(v.x >> 16)),
                                                         e4m3x2_to_f16x2((uint16_t)v.y), e4m3x2_to_f16x2((uint16_t)(v.y >> 16))));
           sts128(op_addr(base, row, 2 * ch + 1), make_uint4(e4m3x2_to_f16x2((uint16_t)v.z), e4m3x2_to_f16x2((uint16_t)(v.z >> 16)),
@@ -807,35 +825,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nt = un.nt, chunks = un.chunks, c0 = un.c0, c1 = un.c1, rows = un.rows;
       const bool last = un.flags & kLast;
       const int ks[2] = {un.k_slot, un.k_slot1}, kround[2] = {un.k_round, un.k_round1};
-      int sn[2] = {un.s0, un.s1};
+      int sn = un.s0;
       Ring qr(nq, un.q_slot, un.q_round);
       mbar_arrive(bar(B_UE + ur.slot));
       ur.step();
       if (nt == 0) break;
-      for (int c = c0; live && c < chunks; ++c) {
-        const int qs = nk + qr.slot;
+      for (int c = c0; live && c < chunks; ++c, ++sn) {
+        const int qs = nk + qr.slot, buf = sn & 1;
         live = mbar_wait(bar(B_FULL + qs), qr.round & 1, abort_flag);
         qr.step();
+        if (live && c == c0) live = mbar_wait(bar(B_FULL + ks[0]), kround[0] & 1, abort_flag);
+        if (live && c == c1 && nt == 2) live = mbar_wait(bar(B_FULL + ks[1]), kround[1] & 1, abort_flag);
+        if (live && sn >= 2) live = mbar_wait(bar(B_SE + buf), ((sn >> 1) - 1) & 1, abort_flag);
+        if (!live) break;
+        tc_fence_after();
+        // what the copies and the loaders' stores left is there for the tensor cores: the fence stands here and not
+        // with the loaders, where it would wait for all their copies under way
+        fence_proxy_async();
         const uint32_t id = idesc_n<FP8>((min(kTile, rows - c * kTile) + 15) & ~15);
         const uint64_t qd = desc0 + (uint64_t)((sbase + qs * C::OP) >> 4);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!live || t >= nt || (t == 1 && c < c1)) continue;
-          if (c == (t == 0 ? c0 : c1)) live = mbar_wait(bar(B_FULL + ks[t]), kround[t] & 1, abort_flag);
-          const int buf = sn[t] & 1;
-          if (live && sn[t] >= 2) live = mbar_wait(bar(B_SE + t * 2 + buf), ((sn[t] >> 1) - 1) & 1, abort_flag);
-          if (!live) continue;
-          ++sn[t];
-          tc_fence_after();
-          // what the copies and the loaders' stores left is there for the tensor cores: the fence stands here and not
-          // with the loaders, where it would wait for all their copies under way
-          fence_proxy_async();
-          mma_tile<D>(tmem + t * 256 + buf * kTile, desc0 + (uint64_t)((sbase + ks[t] * C::OP) >> 4), qd, id);
-          umma_commit(bar(B_SF + t * 2 + buf));
-          if (c == chunks - 1) umma_commit(bar(B_FREE + ks[t]));
-          issued = true;
+        mma_tile<D>(tmem + buf * kTile, desc0 + (uint64_t)((sbase + ks[0] * C::OP) >> 4), qd, id);
+        if (nt == 2 && c >= c1)
+          mma_tile<D>(tmem + 256 + buf * kTile, desc0 + (uint64_t)((sbase + ks[1] * C::OP) >> 4), qd, id);
+        umma_commit(bar(B_SF + buf));
+        if (last) umma_commit(bar(B_FREE + qs));
+        if (c == chunks - 1) {
+          umma_commit(bar(B_FREE + ks[0]));
+          if (nt == 2) umma_commit(bar(B_FREE + ks[1]));
         }
-        if (live && last) umma_commit(bar(B_FREE + qs));
+        issued = true;
       }
     }
     if (issued) {   // every commit has arrived before the CTA's shared memory goes away
