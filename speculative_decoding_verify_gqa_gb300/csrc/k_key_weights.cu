@@ -250,6 +250,12 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 // Wait for the tensor-memory loads under way; the registers pass through, so
 // that nothing reads or moves them before.
+__device__ __forceinline__ void tmem_wait8(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait32(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u.flags & kBad) continue;
       const int j = u.key0 + t * kTile + slot;
       const bool mine = t < u.nt && j < u.keys;
-      const int draft = j - u.pre, tile_last = u.key0 + t * kTile + kTile - 1;
+      const int draft = j - u.pre, border = draft - lane;   // the warp's first key among the step's own
       long long dst = -1;
       float old = 0.f;
       if (mine) {
@@ -547,77 +553,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c >= c_mine) {
           tc_fence_after();
           const int r0 = c * kTile, nr = min(kTile, u.rows - r0);
-          // all rows of the chunk see all keys of the tile
-          const bool plain = p.mask ? !p.mask_full && tile_last < u.pre : (long long)(tile_last - u.pre) * p.group <= r0;
+          // of the chunk's rows, those before `from` see none of the warp's keys, those from `vis` on all of them
+          int from = 0, vis = 0;
+          if (p.mask) {
+            if (p.mask_full || border + 31 >= 0) vis = kTile;
+          } else {
+            from = min(max(max(border, -64) * p.group - r0, 0), kTile) & ~31;
+            vis = max(max(border + 31, -64) * p.group - r0, 0);
+          }
           const uint32_t at = cols + buf * kTile;
           const float* const l2 = l2s + qs * kTile;
           uint64_t acc0 = 0, acc1 = 0;
-          // 32 rows: which of them see the key -- up to the chunk's end, from the causal border on, or by the mask
-          auto seen = [&](int k) -> uint32_t {
-            uint32_t on = 0;
-            if (!mine) return on;
-            const int first = r0 + k;
-            if (!p.mask || (!p.mask_full && draft < 0)) {
-              const int lo = draft <= 0 ? 0 : (int)min((long long)draft * p.group - first, 32ll);
-              on = lo >= 32 ? 0u : 0xffffffffu << max(lo, 0);
-            } else {
-              const long long row0 = u.mask_row + (p.mask_full ? j : draft);
-              const int width = p.mask_full ? u.keys : u.L;
-              for (int tok = first / p.group, e = tok * p.group - first; e < 32 && tok < u.n; ++tok, e += p.group) {
-                const long long bit = row0 + (long long)tok * width;
-                if ((p.mask[bit >> 3] >> (bit & 7)) & 1) {   // rows e .. e + group - 1, those among the 32
-                  const int z = min(e + p.group, 32);
-                  on |= (z == 32 ? 0xffffffffu : (1u << z) - 1u) & (0xffffffffu << max(e, 0));
-                }
-              }
-            }
-            return nr - k < 32 ? on & ((1u << max(nr - k, 0)) - 1u) : on;
+          // four logits: 2^(s c - lse log2 e)
+          auto add4 = [&](const uint32_t* x, int k, bool o0, bool o1, bool o2, bool o3) {
+            const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(l2 + k);
+            const uint64_t a = fma_f32x2(f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])), scale, l.x);
+            const uint64_t b = fma_f32x2(f32x2(__uint_as_float(x[2]), __uint_as_float(x[3])), scale, l.y);
+            acc0 = add_f32x2(acc0, f32x2(o0 ? ex2(f32x2_lo(a)) : 0.f, o1 ? ex2(f32x2_hi(a)) : 0.f));
+            acc1 = add_f32x2(acc1, f32x2(o2 ? ex2(f32x2_lo(b)) : 0.f, o3 ? ex2(f32x2_hi(b)) : 0.f));
           };
-          // two logits at a time: 2^(s c - lse log2 e)
-          auto weight = [&](uint32_t s0, uint32_t s1, uint64_t l) {
-            return fma_f32x2(f32x2(__uint_as_float(s0), __uint_as_float(s1)), scale, l);
-          };
-          int k = 0;
-          if (plain) {
-            // (64 columns at a time: with 32 the way in and out of tensor memory is what a prompt waits for)
-#pragma unroll 1
-            for (; k + 64 <= nr; k += 64) {
+          for (int k = from; k < nr;) {
+            if (k >= vis && k + 64 <= nr) {
               uint32_t x[64];
               tmem_ld32(at + k, x);
               tmem_ld32(at + k + 32, x + 32);
               tmem_wait32(x);
               tmem_wait32(x + 32);
 #pragma unroll
-              for (int i = 0; i < 64; i += 4) {
-                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(l2 + k + i);
-                const uint64_t a = weight(x[i], x[i + 1], l.x), b = weight(x[i + 2], x[i + 3], l.y);
-                acc0 = add_f32x2(acc0, f32x2(ex2(f32x2_lo(a)), ex2(f32x2_hi(a))));
-                acc1 = add_f32x2(acc1, f32x2(ex2(f32x2_lo(b)), ex2(f32x2_hi(b))));
+              for (int i = 0; i < 64; i += 4) add4(x + i, k + i, true, true, true, true);
+              k += 64;
+            } else if (k >= vis && k + 8 <= nr) {   // the rest of a chunk, as whole tokens have it
+              uint32_t x[8];
+              tmem_ld8(at + k, x);
+              tmem_wait8(x);
+              add4(x, k, true, true, true, true);
+              add4(x + 4, k + 4, true, true, true, true);
+              k += 8;
+            } else {
+              // 32 rows: which of them see the key -- up to the chunk's end, from the causal border on, or by the mask
+              const int done = k & 31;   // rows that have been added (the load stays within the buffer)
+              k -= done;
+              uint32_t x[32];
+              tmem_ld32(at + k, x);
+              tmem_wait32(x);
+              uint32_t on = 0;
+              const int row = r0 + k;
+              if (!mine) {
+              } else if (!p.mask || (!p.mask_full && draft < 0)) {
+                const int lo = draft <= 0 ? 0 : min(draft * p.group - row, 32);
+                on = lo >= 32 ? 0u : 0xffffffffu << max(lo, 0);
+              } else {
+                const long long row0 = u.mask_row + (p.mask_full ? j : draft);
+                const int width = p.mask_full ? u.keys : u.L;
+                for (int tok = row / p.group, e = tok * p.group - row; e < 32 && tok < u.n; ++tok, e += p.group) {
+                  const long long bit = row0 + (long long)tok * width;
+                  if ((p.mask[bit >> 3] >> (bit & 7)) & 1) {   // rows e .. e + group - 1, those among the 32
+                    const int z = min(e + p.group, 32);
+                    on |= (z == 32 ? 0xffffffffu : (1u << z) - 1u) & (0xffffffffu << max(e, 0));
+                  }
+                }
               }
-            }
-          }
-#pragma unroll 1
-          for (; k < nr; k += 32) {
-            uint32_t x[32];
-            tmem_ld32(at + k, x);
-            tmem_wait32(x);
-            if (plain && k + 32 <= nr) {
+              if (nr - k < 32) on &= (1u << (nr - k)) - 1u;
+              on &= 0xffffffffu << done;
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(l2 + k + i);
-                const uint64_t a = weight(x[i], x[i + 1], l.x), b = weight(x[i + 2], x[i + 3], l.y);
-                acc0 = add_f32x2(acc0, f32x2(ex2(f32x2_lo(a)), ex2(f32x2_hi(a))));
-                acc1 = add_f32x2(acc1, f32x2(ex2(f32x2_lo(b)), ex2(f32x2_hi(b))));
-              }
-              continue;
-            }
-            const uint32_t on = seen(k);
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(l2 + k + i);
-              const uint64_t a = weight(x[i], x[i + 1], l.x), b = weight(x[i + 2], x[i + 3], l.y);
-              acc0 = add_f32x2(acc0, f32x2((on >> i) & 1 ? ex2(f32x2_lo(a)) : 0.f, (on >> (i + 1)) & 1 ? ex2(f32x2_hi(a)) : 0.f));
-              acc1 = add_f32x2(acc1, f32x2((on >> (i + 2)) & 1 ? ex2(f32x2_lo(b)) : 0.f, (on >> (i + 3)) & 1 ? ex2(f32x2_hi(b)) : 0.f));
+              for (int i = 0; i < 32; i += 4)
+                add4(x + i, k + i, (on >> i) & 1, (on >> (i + 1)) & 1, (on >> (i + 2)) & 1, (on >> (i + 3)) & 1);
+              k += 32;
             }
           }
           tc_fence_before();
