@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.mask) {
             if (p.mask_full || border + 31 >= 0) vis = kTile;
           } else {
-            from = min(max(max(border, -64) * p.group - r0, 0), kTile) & ~31;
+            from = min(max(max(border, -64) * p.group - r0, 0), kTile) & ~7;
             vis = max(max(border + 31, -64) * p.group - r0, 0);
           }
           const uint32_t at = cols + buf * kTile;
@@ -573,53 +573,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc1 = add_f32x2(acc1, f32x2(o2 ? ex2(f32x2_lo(b)) : 0.f, o3 ? ex2(f32x2_hi(b)) : 0.f));
           };
           for (int k = from; k < nr;) {
-            if (k >= vis && k + 64 <= nr) {
-              uint32_t x[64];
-              tmem_ld32(at + k, x);
-              tmem_ld32(at + k + 32, x + 32);
-              tmem_wait32(x);
-              tmem_wait32(x + 32);
-#pragma unroll
-              for (int i = 0; i < 64; i += 4) add4(x + i, k + i, true, true, true, true);
-              k += 64;
-            } else if (k >= vis && k + 8 <= nr) {   // the rest of a chunk, as whole tokens have it
-              uint32_t x[8];
-              tmem_ld8(at + k, x);
-              tmem_wait8(x);
-              add4(x, k, true, true, true, true);
-              add4(x + 4, k + 4, true, true, true, true);
-              k += 8;
-            } else {
-              // 32 rows: which of them see the key -- up to the chunk's end, from the causal border on, or by the mask
-              const int done = k & 31;   // rows that have been added (the load stays within the buffer)
-              k -= done;
+            if (k >= vis && k + 32 <= nr) {
               uint32_t x[32];
               tmem_ld32(at + k, x);
               tmem_wait32(x);
-              uint32_t on = 0;
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) add4(x + i, k + i, true, true, true, true);
+              k += 32;
+              continue;
+            }
+            if (!p.mask && k + 32 <= nr) {   // across the causal border
+              uint32_t x[32];
+              tmem_ld32(at + k, x);
+              tmem_wait32(x);
+              const int lo = draft * p.group - (r0 + k);
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) add4(x + i, k + i, i >= lo, i + 1 >= lo, i + 2 >= lo, i + 3 >= lo);
+              k += 32;
+              continue;
+            }
+            // 8 rows: which of them see the key -- up to the chunk's end, from the causal border on, or by the mask
+            uint32_t x[8];
+            tmem_ld8(at + k, x);
+            uint32_t on = 0xffu;
+            if (k < vis) {
               const int row = r0 + k;
               if (!mine) {
+                on = 0;
               } else if (!p.mask || (!p.mask_full && draft < 0)) {
-                const int lo = draft <= 0 ? 0 : min(draft * p.group - row, 32);
-                on = lo >= 32 ? 0u : 0xffffffffu << max(lo, 0);
+                on <<= draft <= 0 ? 0 : min(max(draft * p.group - row, 0), 8);
               } else {
                 const long long row0 = u.mask_row + (p.mask_full ? j : draft);
                 const int width = p.mask_full ? u.keys : u.L;
-                for (int tok = row / p.group, e = tok * p.group - row; e < 32 && tok < u.n; ++tok, e += p.group) {
+                on = 0;
+                for (int tok = row / p.group, e = tok * p.group - row; e < 8 && tok < u.n; ++tok, e += p.group) {
                   const long long bit = row0 + (long long)tok * width;
-                  if ((p.mask[bit >> 3] >> (bit & 7)) & 1) {   // rows e .. e + group - 1, those among the 32
-                    const int z = min(e + p.group, 32);
-                    on |= (z == 32 ? 0xffffffffu : (1u << z) - 1u) & (0xffffffffu << max(e, 0));
-                  }
+                  if ((p.mask[bit >> 3] >> (bit & 7)) & 1)   // rows e .. e + group - 1, those among the 8
+                    on |= ((1u << min(e + p.group, 8)) - 1u) & (0xffu << max(e, 0));
                 }
               }
-              if (nr - k < 32) on &= (1u << (nr - k)) - 1u;
-              on &= 0xffffffffu << done;
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                add4(x + i, k + i, (on >> i) & 1, (on >> (i + 1)) & 1, (on >> (i + 2)) & 1, (on >> (i + 3)) & 1);
-              k += 32;
             }
+            if (nr - k < 8) on &= (1u << (nr - k)) - 1u;
+            tmem_wait8(x);
+            add4(x, k, on & 1, on & 2, on & 4, on & 8);
+            add4(x + 4, k + 4, on & 16, on & 32, on & 64, on & 128);
+            k += 8;
           }
           tc_fence_before();
           acc0 = add_f32x2(acc0, acc1);
