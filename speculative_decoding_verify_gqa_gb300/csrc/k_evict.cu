@@ -4,21 +4,25 @@
 // weights, the lower position among equals -- and moves them to the front in
 // their order, with their weights.
 //
-// A unit (layer, request, KV head) belongs to one cluster of CTAs.  Each CTA
-// finds the unit's survivors for itself: the weight that the last of them has
-// by three passes of an 11-bit radix select over order-preserving integers,
-// then one bit a key and the count of bits before each word in shared memory.
-// Then the CTAs share the columns: CTA c moves its 16-byte column chunks of
-// every surviving row, and CTA 0 the weights.
+// A unit (layer, request, KV head) belongs to one cluster of CTAs, one where
+// there are units enough.  Each CTA holds a slice of the unit's weights as
+// order-preserving integers in shared memory.  The weight of the last survivor
+// is found by a radix select of at most three 11-bit digits, from the top: the
+// CTAs count their slices, and each adds up all counts by reading the others'
+// shared memory.  It ends as soon as all keys that share the digits found
+// survive.  Then each CTA marks its slice, one bit a key, and every CTA gathers
+// all bits and counts them by words, so that the k-th survivor is found by a
+// search over the words.
 //
-// In place: the row of rank k goes to position k and comes from a position >=
-// k.  A batch of rows is read, the CTA meets, and the batch is written: what
-// it overwrites has a rank no higher than its position, so it has been read.
-// Columns are independent, so only the CTA's own threads have to meet; the
-// cluster meets once, before CTA 0 overwrites weights that others still rank.
+// The move is shared by columns: a CTA moves its 16-byte chunks of every
+// surviving row, CTA 0 the weights too.  In place: the row of rank k goes to
+// position k and comes from a position >= k.  A batch of rows is read, the
+// CTA meets, and the batch is written: what it overwrites has a rank no higher
+// than its position, so it has been read.  Columns are independent, so only the
+// CTA's own threads have to meet.
 //
-// Bound by the rows' copy (HBM) where many units move, and by the select's
-// chain of passes where few do.
+// Bound by the rows' copy (HBM) where rows move, and by the chain of loads and
+// meetings of the select where they are few.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -31,11 +35,11 @@
 namespace va {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDigit = 11, kBins = 1 << kDigit;
-constexpr int kBatch = 8;    // rows' chunks in flight per thread
-constexpr int kResolve = 256;  // ranks resolved at a time
+constexpr int kBatch = 8;   // rows' chunks in flight per thread
+constexpr int kAhead = 8;   // weights in flight per thread
 
 // Weights as integers in their order: -0 counts as 0, NaN above everything.
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -45,7 +49,19 @@ __device__ __forceinline__ uint32_t order_of(float w) {
 }
 
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+}
+// shared memory of CTA `rank` of the cluster, at this CTA's address
+__device__ __forceinline__ uint32_t remote(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_remote(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // exclusive sum over the threads of the CTA; *total receives the whole sum
@@ -73,177 +89,252 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
 
 __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictParams p) {
   extern __shared__ uint32_t dyn[];
-  uint32_t* const bits = dyn;                                   // one bit a key: kept
-  int* const before = reinterpret_cast<int*>(dyn + p.words);    // kept keys before each word
-  __shared__ int hist[kBins];
-  __shared__ long long src_row[kResolve], dst_row[kResolve];
-  __shared__ int warp_sums[kWarps], geo[4], pick[3];
+  uint32_t* const bits = dyn;                                  // one bit a key: it survives
+  int* const before = reinterpret_cast<int*>(dyn + p.words);   // survivors before each word
+  uint32_t* const slice = dyn + 2 * p.words;                   // this CTA's weights (slice_cap of them)
+  __shared__ int hist[2][kBins];
+  __shared__ long long src_row[kThreads], dst_row[kThreads];
+  __shared__ int warp_sums[kWarps], geo[5], pick[3], count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = blockIdx.x % p.cluster;
-  const long long unit = blockIdx.x / p.cluster;
+  const int C = p.cluster, rank = blockIdx.x % C;
+  const long long unit = blockIdx.x / C;
   const int head = (int)(unit % p.h_kv);
   const int b = (int)(unit / p.h_kv % p.batch), layer = (int)(unit / p.h_kv / p.batch);
   grid_dependency_wait();
   grid_dependents_launch();
-  if (tid < 3) pick[tid] = 0;
   if (tid < 4) {
     const int32_t* const src[4] = {p.kv_indptr + b, p.kv_indptr + b + 1, p.last_page_len + b, p.keep_len + b};
     geo[tid] = *src[tid];
   }
+  if (tid < 3) pick[tid] = 0;
+  for (int k = tid; k < 2 * kBins; k += kThreads) hist[0][k] = 0;
   __syncthreads();
   const int pg0 = geo[0], npg = geo[1] - pg0, lpl = npg > 0 ? geo[2] : 1;
   const long long len = npg > 0 ? (long long)(npg - 1) * p.page_size + lpl : 0;
   const bool table_ok = npg >= 0 && pg0 >= 0 && lpl >= 1 && lpl <= p.page_size && geo[3] >= 0 && len <= p.max_kv_len;
   const bool first = layer == 0 && head == 0 && rank == 0 && tid == 0;
-  if (!table_ok) {
-    if (first && p.kv_len_out) p.kv_len_out[b] = len >= 0 && len <= 0x7fffffffLL && npg >= 0 ? (int)len : 0;
-    if (first && p.status) atomicOr(p.status, VA_DEV_BAD_TABLE);
-    return;
-  }
-  const int n = (int)len, keep = min(geo[3], n);
+  const int n = table_ok ? (int)len : 0, keep = min(geo[3], n);
   int bad = 0;
   if (keep < n)
-    for (int j = tid; j < npg; j += kThreads) bad |= (unsigned)p.kv_indices[pg0 + j] >= (unsigned)p.num_pages;
+    for (int j = rank * kThreads + tid; j < npg; j += C * kThreads) bad |= (unsigned)p.kv_indices[pg0 + j] >= (unsigned)p.num_pages;
   bad = __syncthreads_or(bad);
-  if (first) {
-    if (p.kv_len_out) p.kv_len_out[b] = bad ? n : keep;
-    if (bad && p.status) atomicOr(p.status, VA_DEV_BAD_PAGE);
+  if (C > 1) {
+    // The CTAs go on or leave together: each has checked its share of the pages,
+    // and all have read the same tables (inputs that are written during the call
+    // end it here).
+    if (tid == 0) geo[4] = bad;
+    cluster_sync();
+    int odd = 0;
+    if (tid < 5 * C) {
+      const int v = (int)ld_remote(remote(smem_u32(geo + tid % 5), tid / 5));
+      odd = tid % 5 == 4 ? v : (v != geo[tid % 5]) << 1;
+    }
+    const int any_bad = __syncthreads_or(odd & 1), differ = __syncthreads_or(odd & 2);
+    bad = any_bad;
+    if (bad || differ || !table_ok || keep == n) cluster_sync();   // nobody leaves while others read
+    if (differ) {
+      if (rank == 0 && tid == 0 && p.status) atomicOr(p.status, VA_DEV_BAD_TABLE);
+      return;
+    }
   }
-  if (bad || keep == n) return;
+  if (first) {
+    if (p.kv_len_out) p.kv_len_out[b] = table_ok ? (bad ? n : keep) : len >= 0 && len <= 0x7fffffffLL && npg >= 0 ? (int)len : 0;
+    if ((bad || !table_ok) && p.status) atomicOr(p.status, table_ok ? VA_DEV_BAD_PAGE : VA_DEV_BAD_TABLE);
+  }
+  if (!table_ok || bad || keep == n) return;
 
   const long long slot_rows = p.nhd ? p.h_kv : 1, page_rows = (long long)p.h_kv * p.page_size;
   const long long layer_row = (long long)layer * p.num_pages * page_rows + (p.nhd ? head : (long long)head * p.page_size);
   float* const w = p.key_weights;
-  // row of position j of this layer and head; a page id that has changed since the check reads page 0
-  auto row_of = [&](int j) {
-    const unsigned page = (unsigned)p.kv_indices[pg0 + (j >> p.log2_page)];
-    return layer_row + (page < (unsigned)p.num_pages ? page : 0u) * page_rows + (j & (p.page_size - 1)) * slot_rows;
+  // row of position j on its page; a page id that has changed since the check reads page 0
+  auto row_at = [&](int page, int j) {
+    return layer_row + ((unsigned)page < (unsigned)p.num_pages ? page : 0) * page_rows + (j & (p.page_size - 1)) * slot_rows;
   };
+  auto row_of = [&](int j) { return row_at(p.kv_indices[pg0 + (j >> p.log2_page)], j); };
 
-  // the middle [lo, hi) competes for `rest` places
+  // the middle [lo, hi) competes for `rest` places; this CTA looks after [s0, s1)
   const int lo = min(p.sinks, keep), hi = n - min(p.recent, keep - lo), rest = keep - lo - (n - hi);
-  uint32_t edge = 0xffffffffu;  // the last survivor's weight, and how many of the keys with just that weight survive
-  int ties = 0;
+  const int per = ((n + C - 1) / C + 31) & ~31, s0 = min(rank * per, n), s1 = min(s0 + per, n);
+  const int m0 = max(s0, lo), m1 = min(s1, hi);
+  const bool held = per <= p.slice_cap;   // (else the weights are read again from the cache)
+  auto weight_at = [&](int j) { return held ? slice[j - s0] : order_of(w[row_of(j)]); };
+
+  // how the last survivor is told from the others: u & mask > fixed survives, `ties` of those with u & mask == fixed too
+  uint32_t fixed = 0, mask = 0;
+  int want = rest, same_all = 0;
   if (rest > 0) {
-    uint32_t fixed = 0;
-    int want = rest;  // rank, from above, of the last survivor among the keys that share the digits found so far
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, nb = pass == 2 ? 1024 : kBins;
-      for (int k = tid; k < nb; k += kThreads) hist[k] = 0;
-      __syncthreads();
-      const uint32_t above = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
-      for (int j = lo + tid; j < hi; j += kThreads) {
-        const uint32_t u = order_of(w[row_of(j)]);
-        if ((u & above) == fixed) atomicAdd(&hist[(u >> shift) & (nb - 1)], 1);
+      int* const h = hist[pass & 1];
+      if (pass == 2) {   // (the first pass's counts have been read by all: they met in the second)
+        for (int k = tid; k < nb; k += kThreads) h[k] = 0;
+        __syncthreads();
       }
+      if (pass == 0) {
+        for (int j0 = m0 + tid; j0 < m1; j0 += kThreads * kAhead) {
+          int page[kAhead];
+          float x[kAhead];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) page[i] = p.kv_indices[pg0 + (min(j0 + i * kThreads, m1 - 1) >> p.log2_page)];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) x[i] = w[row_at(page[i], min(j0 + i * kThreads, m1 - 1))];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const int j = j0 + i * kThreads;
+            if (j < m1) {
+              const uint32_t u = order_of(x[i]);
+              if (held) slice[j - s0] = u;
+              atomicAdd(&h[u >> 21], 1);
+            }
+          }
+        }
+      } else {
+        for (int j = m0 + tid; j < m1; j += kThreads) {
+          const uint32_t u = weight_at(j);
+          if ((u & mask) == fixed) atomicAdd(&h[(u >> shift) & (nb - 1)], 1);
+        }
+      }
+      if (C > 1) cluster_sync();
       __syncthreads();
-      // bins from above: thread t holds bins nb - 1 - t * per ...
-      const int per = nb / kThreads;
-      int sum = 0;
-      for (int k = 0; k < per; ++k) sum += hist[nb - 1 - tid * per - k];
+      // bins from above: thread t holds bins nb - 1 - t * each ..
+      const int each = nb / kThreads;
+      int c[kBins / kThreads], sum = 0;
+#pragma unroll
+      for (int k = 0; k < kBins / kThreads; ++k) {
+        c[k] = 0;
+        if (k < each) {
+          const int bin = nb - 1 - tid * each - k;
+          if (C == 1) {
+            c[k] = h[bin];
+          } else {
+            const uint32_t a = smem_u32(h + bin);
+            for (int r = 0; r < C; ++r) c[k] += (int)ld_remote(remote(a, r));
+          }
+        }
+        sum += c[k];
+      }
       int all;
       int run = block_scan(sum, warp_sums, &all);
       if (run < want && run + sum >= want) {
-        for (int k = 0; k < per; ++k) {
-          const int bin = nb - 1 - tid * per - k, c = hist[bin];
-          if (run + c >= want) {
-            pick[0] = bin;
+#pragma unroll
+        for (int k = 0; k < kBins / kThreads; ++k) {
+          if (run < want && run + c[k] >= want) {
+            pick[0] = nb - 1 - tid * each - k;
             pick[1] = want - run;
-            break;
+            pick[2] = c[k];
           }
-          run += c;
+          run += c[k];
         }
       }
       __syncthreads();
       fixed |= (uint32_t)pick[0] << shift;
+      mask = pass == 0 ? 0xffe00000u : pass == 1 ? 0xfffffc00u : 0xffffffffu;
       want = pick[1];
+      same_all = want == pick[2];   // all that share the digits survive
+      if (same_all) break;
       __syncthreads();
     }
-    edge = fixed;
-    ties = want;
   }
+  const int ties = want;
 
-  // one bit a key, in order: a warp takes a run of words; equals are counted first
-  const int words = (n + 31) >> 5, per = (words + kWarps - 1) / kWarps;
-  const int w0 = min(warp * per, words), w1 = min(w0 + per, words);
+  // the slice's bits, in order: a warp takes a run of words
+  const int words = (n + 31) >> 5, v0 = s0 >> 5, nv = s1 > s0 ? (s1 + 31) / 32 - v0 : 0;
+  const int per_warp = (nv + kWarps - 1) / kWarps;
+  const int w0 = v0 + min(warp * per_warp, nv), w1 = v0 + min((warp + 1) * per_warp, nv);
   int equal = 0;
   for (int k = w0; k < w1; ++k) {
     const int j = k * 32 + lane;
-    const uint32_t u = j >= lo && j < hi && rest > 0 ? order_of(w[row_of(j)]) : 0u;
-    const bool more = j < lo || (j >= hi && j < n) || (j >= lo && j < hi && rest > 0 && u > edge);
-    const bool same = j >= lo && j < hi && rest > 0 && u == edge;
+    const bool mid = j >= lo && j < hi && rest > 0;
+    const uint32_t u = mid ? weight_at(j) & mask : 0u;
+    const bool more = j < lo || (j >= hi && j < n) || (mid && u > fixed), same = mid && u == fixed;
     const uint32_t mm = __ballot_sync(0xffffffffu, more), ms = __ballot_sync(0xffffffffu, same);
     if (lane == 0) {
-      bits[k] = mm;
-      before[k] = (int)ms;  // (until the equals are counted)
+      bits[k] = same_all ? mm | ms : mm;
+      before[k] = (int)ms;   // (until the equals are counted)
     }
     equal += __popc(ms);
   }
   int all;
-  int eq_run = block_scan(lane == 0 ? equal : 0, warp_sums, &all);
-  eq_run = __shfl_sync(0xffffffffu, eq_run, 0);
-  int kept = 0;
-  for (int k0 = w0; k0 < w1; k0 += 32) {
-    // lane: one word; the equals before it in this warp's run
-    const int k = k0 + lane;
-    uint32_t ms = k < w1 ? (uint32_t)before[k] : 0u;
-    const int c = __popc(ms);
-    int s = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += t;
+  if (rest > 0 && !same_all) {
+    // some of the equals go: those behind the first `ties` of all slices
+    int run = block_scan(lane == 0 ? equal : 0, warp_sums, &all);
+    run = __shfl_sync(0xffffffffu, run, 0);
+    if (C > 1) {
+      if (tid == 0) count = all;
+      cluster_sync();
+      for (int r = 0; r < rank; ++r) run += (int)ld_remote(remote(smem_u32(&count), r));
     }
-    int room = ties - (eq_run + s - c);  // equals of this word that still survive
-    eq_run += __shfl_sync(0xffffffffu, s, 31);
-    if (room < c) {
-      uint32_t some = 0;
-      for (; room > 0; --room) {
-        const uint32_t one = ms & (0u - ms);
-        some |= one;
-        ms ^= one;
+    for (int k0 = w0; k0 < w1; k0 += 32) {
+      const int k = k0 + lane;   // lane: one word
+      uint32_t ms = k < w1 ? (uint32_t)before[k] : 0u;
+      const int c = __popc(ms);
+      int s = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += t;
       }
-      ms = some;
-    }
-    if (k < w1) {
-      bits[k] |= ms;
-      kept += __popc(bits[k]);
+      int room = ties - (run + s - c);   // of this word's equals
+      run += __shfl_sync(0xffffffffu, s, 31);
+      if (room < c) {
+        uint32_t some = 0;
+        for (; room > 0; --room) {
+          const uint32_t one = ms & (0u - ms);
+          some |= one;
+          ms ^= one;
+        }
+        ms = some;
+      }
+      if (k < w1) bits[k] |= ms;
     }
   }
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) kept += __shfl_xor_sync(0xffffffffu, kept, m);
-  int run = block_scan(lane == 0 ? kept : 0, warp_sums, &all);
-  run = __shfl_sync(0xffffffffu, run, 0);
-  if (tid == 0) pick[2] = n;
   __syncthreads();
-  for (int k0 = w0; k0 < w1; k0 += 32) {
-    const int k = k0 + lane;
-    const uint32_t m = k < w1 ? bits[k] : 0u;
-    int s = __popc(m);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += t;
-    }
-    if (k < w1) {
-      before[k] = run + s - __popc(m);
-      if (m != 0xffffffffu) atomicMin(&pick[2], k * 32 + __ffs(~m) - 1);  // the first key that goes
-    }
-    run += __shfl_sync(0xffffffffu, s, 31);
+  if (C > 1) {
+    // gather: words of CTA r's slice from its shared memory
+    cluster_sync();
+    const int words_per = per >> 5;
+    for (int k = tid; k < words; k += kThreads)
+      if (k < v0 || k >= v0 + nv) bits[k] = ld_remote(remote(smem_u32(bits + k), k / words_per));
+    if (tid == 0) pick[2] = n;
+    cluster_sync();   // nobody leaves, or moves weights, while others read
+  } else if (tid == 0) {
+    pick[2] = n;
   }
-  if (p.cluster > 1) cluster_sync();
+  __syncthreads();
+  {
+    const int each = (words + kThreads - 1) / kThreads, k0 = min(tid * each, words), k1 = min(k0 + each, words);
+    int sum = 0;
+    for (int k = k0; k < k1; ++k) sum += __popc(bits[k]);
+    int run = block_scan(sum, warp_sums, &all);
+    for (int k = k0; k < k1; ++k) {
+      const uint32_t m = bits[k];
+      before[k] = run;
+      run += __popc(m);
+      if (m != 0xffffffffu) {   // the first key that goes
+        atomicMin(&pick[2], k * 32 + __ffs(~m) - 1);
+        for (++k; k < k1; ++k) {
+          before[k] = run;
+          run += __popc(bits[k]);
+        }
+      }
+    }
+  }
   __syncthreads();
 
   // ranks before the first gap stay where they are
   const int chunks = p.k_chunks + p.v_chunks;
-  const int c0 = (int)((long long)chunks * rank / p.cluster), nc = (int)((long long)chunks * (rank + 1) / p.cluster) - c0;
-  for (int k0 = min(pick[2], keep); k0 < keep; k0 += kResolve) {
-    const int m = min(kResolve, keep - k0);
+  const int c0 = chunks * rank / C, nc = chunks * (rank + 1) / C - c0;
+  const int par = kThreads / nc, my_r = tid / nc, my_c = c0 + tid - my_r * nc;   // this thread's first row, and its column
+  const bool in_k = my_c < p.k_chunks;
+  const int stride = in_k ? p.k_chunks : p.v_chunks;
+  uint4* const col = in_k ? static_cast<uint4*>(p.k_cache) + my_c : static_cast<uint4*>(p.v_cache) + (my_c - p.k_chunks);
+  for (int k0 = min(pick[2], keep); k0 < keep; k0 += kThreads) {
+    const int m = min(kThreads, keep - k0);
     __syncthreads();
     if (tid < m) {
       const int k = k0 + tid;
-      int a = 0, z = words;  // the last word with before[word] <= k
+      int a = 0, z = words;   // the last word with before[word] <= k
       while (z - a > 1) {
         const int mid = (a + z) >> 1;
         if (before[mid] <= k) a = mid; else z = mid;
@@ -254,27 +345,18 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
       dst_row[tid] = row_of(k);
     }
     __syncthreads();
-    const int total = m * nc;
-    for (int i0 = 0; i0 < total; i0 += kThreads * kBatch) {
+    for (int r0 = 0; r0 < m; r0 += par * kBatch) {
       uint4 v[kBatch];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * kThreads + tid;
-        if (i < total) {
-          const int r = i / nc, c = c0 + i - r * nc;
-          v[j] = c < p.k_chunks ? static_cast<const uint4*>(p.k_cache)[src_row[r] * p.k_chunks + c]
-                                : static_cast<const uint4*>(p.v_cache)[src_row[r] * p.v_chunks + c - p.k_chunks];
-        }
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + my_r + i * par;
+        if (r < m && my_r < par) v[i] = col[src_row[r] * stride];
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * kThreads + tid;
-        if (i < total) {
-          const int r = i / nc, c = c0 + i - r * nc;
-          if (c < p.k_chunks) static_cast<uint4*>(p.k_cache)[dst_row[r] * p.k_chunks + c] = v[j];
-          else static_cast<uint4*>(p.v_cache)[dst_row[r] * p.v_chunks + c - p.k_chunks] = v[j];
-        }
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + my_r + i * par;
+        if (r < m && my_r < par) col[dst_row[r] * stride] = v[i];
       }
     }
     if (rank == 0) {
@@ -290,10 +372,10 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
   const long long units = (long long)p.layers * p.batch * p.h_kv;
-  const size_t smem = (size_t)p.words * 8;
+  const size_t smem = (size_t)p.words * 8 + (size_t)p.slice_cap * 4;
   const void* k = reinterpret_cast<const void*>(paged_kv_evict_kernel);
   // (the same value for every call: calls of several threads set it side by side)
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictMaxKeys / 4);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictMaxSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * p.cluster));

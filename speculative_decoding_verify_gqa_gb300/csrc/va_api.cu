@@ -1362,6 +1362,8 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
   }
   p.cluster = 1;
   while (p.cluster < kMaxCluster && units * num_kv_heads * p.cluster * 2 <= 4LL * num_sms) p.cluster *= 2;
+  const int64_t slice = ((max_kv_len + p.cluster - 1) / p.cluster + 31) / 32 * 32;
+  p.slice_cap = slice <= kEvictMaxSlice ? (int)slice : 0;
   cudaError_t e = launch_evict(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }

@@ -220,6 +220,8 @@ cudaError_t launch_key_weights(const KeyWeightParams& p, const CUtensorMap& kmap
 
 // Eviction of the keys with the least weight (see k_evict.cu).
 constexpr int kEvictMaxKeys = 1 << 19;  // keys of a request: a bit and a count per word in shared memory
+constexpr int kEvictMaxSlice = 1 << 14; // weights that a CTA holds in shared memory
+constexpr int kEvictMaxSmem = kEvictMaxKeys / 4 + kEvictMaxSlice * 4;
 struct EvictParams {
   float* key_weights;         // [layers, rows of a layer]
   const int32_t* keep_len;    // [batch]
@@ -235,6 +237,7 @@ struct EvictParams {
   int nhd, sinks, recent;
   int max_kv_len, words;      // words: of 32 keys, that max_kv_len fills
   int cluster;                // CTAs per (layer, request, KV head)
+  int slice_cap;              // weights that a CTA has room for
 };
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 
