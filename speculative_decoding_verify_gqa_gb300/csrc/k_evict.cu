@@ -5,11 +5,14 @@
 // their order, with their weights.
 //
 // A unit (layer, request, KV head) belongs to one cluster of CTAs, one where
-// there are units enough.  Each CTA holds a slice of the unit's weights as
-// order-preserving integers in shared memory.  The weight of the last survivor
-// is found by a radix select of at most three 11-bit digits, from the top: the
-// CTAs count their slices, and each adds up all counts by reading the others'
-// shared memory.  It ends as soon as all keys that share the digits found
+// there are units enough.  Each CTA holds a slice of the unit's weights as the
+// upper halves of order-preserving integers in shared memory (two bytes a key:
+// two CTAs then hold 131,072 keys, where four bytes took eight CTAs, which did
+// not fit the GPU at a time).  The weight of the last survivor is found by a
+// radix select from the top, by digits of 11, 5, 11 and 5 bits: the CTAs count
+// their slices, and each adds up all counts by reading the others' shared
+// memory.  The lower halves are read from the cache again, for the few keys that
+// share the upper one.  It ends as soon as all keys that share the digits found
 // survive.  Then each CTA marks its slice, one bit a key, and every CTA gathers
 // all bits and counts them by words, so that the k-th survivor is found by a
 // search over the words.
@@ -37,7 +40,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kDigit = 11, kBins = 1 << kDigit;
+constexpr int kBins = 1 << 11;
+constexpr int kRanks = kBins;  // survivors whose rows are resolved at a time
 constexpr int kBatch = 8;   // rows' chunks in flight per thread
 constexpr int kAhead = 8;   // weights in flight per thread
 
@@ -87,13 +91,14 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   return before + s - v;
 }
 
-__global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const EvictParams p) {
   extern __shared__ uint32_t dyn[];
   uint32_t* const bits = dyn;                                  // one bit a key: it survives
   int* const before = reinterpret_cast<int*>(dyn + p.words);   // survivors before each word
-  uint32_t* const slice = dyn + 2 * p.words;                   // this CTA's weights (slice_cap of them)
+  uint16_t* const slice = reinterpret_cast<uint16_t*>(dyn + 2 * p.words);   // this CTA's weights, upper halves
   __shared__ int hist[2][kBins];
-  __shared__ long long src_row[kThreads], dst_row[kThreads];
+  uint32_t* const src_row = reinterpret_cast<uint32_t*>(hist[0]);   // (when the counts are done with)
+  uint32_t* const dst_row = reinterpret_cast<uint32_t*>(hist[1]);
   __shared__ int warp_sums[kWarps], geo[5], pick[3], count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = p.cluster, rank = blockIdx.x % C;
@@ -143,12 +148,14 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
   }
   if (!table_ok || bad || keep == n) return;
 
-  const long long slot_rows = p.nhd ? p.h_kv : 1, page_rows = (long long)p.h_kv * p.page_size;
+  // Rows count from the layer's first row of this head (32 bits hold them: a
+  // row of K, V and its weight takes 132 bytes at least); a page id that has
+  // changed since the check reads page 0.
+  const uint32_t slot_rows = p.nhd ? p.h_kv : 1, page_rows = (uint32_t)p.h_kv * p.page_size;
   const long long layer_row = (long long)layer * p.num_pages * page_rows + (p.nhd ? head : (long long)head * p.page_size);
-  float* const w = p.key_weights;
-  // row of position j on its page; a page id that has changed since the check reads page 0
-  auto row_at = [&](int page, int j) {
-    return layer_row + ((unsigned)page < (unsigned)p.num_pages ? page : 0) * page_rows + (j & (p.page_size - 1)) * slot_rows;
+  float* const w = p.key_weights + layer_row;
+  auto row_at = [&](int page, int j) -> uint32_t {
+    return ((unsigned)page < (unsigned)p.num_pages ? (uint32_t)page : 0u) * page_rows + (uint32_t)(j & (p.page_size - 1)) * slot_rows;
   };
   auto row_of = [&](int j) { return row_at(p.kv_indices[pg0 + (j >> p.log2_page)], j); };
 
@@ -157,17 +164,24 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
   const int per = ((n + C - 1) / C + 31) & ~31, s0 = min(rank * per, n), s1 = min(s0 + per, n);
   const int m0 = max(s0, lo), m1 = min(s1, hi);
   const bool held = per <= p.slice_cap;   // (else the weights are read again from the cache)
-  auto weight_at = [&](int j) { return held ? slice[j - s0] : order_of(w[row_of(j)]); };
+  // the weight of key j as far as `mask` tells: the lower half is only looked at where the upper one is `fixed`'s
+  auto weight_at = [&](int j, uint32_t fixed, uint32_t mask) -> uint32_t {
+    if (held) {
+      const uint32_t u = (uint32_t)slice[j - s0] << 16;
+      if ((mask & 0xffffu) == 0 || ((u ^ fixed) >> 16) != 0) return u;
+    }
+    return order_of(w[row_of(j)]);
+  };
 
   // how the last survivor is told from the others: u & mask > fixed survives, `ties` of those with u & mask == fixed too
   uint32_t fixed = 0, mask = 0;
   int want = rest, same_all = 0;
   if (rest > 0) {
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, nb = pass == 2 ? 1024 : kBins;
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 16 : pass == 2 ? 5 : 0, nb = pass & 1 ? 32 : kBins;
       int* const h = hist[pass & 1];
-      if (pass == 2) {   // (the first pass's counts have been read by all: they met in the second)
+      if (pass >= 2) {   // (the counts of two passes before have been read by all: they met in the last one)
         for (int k = tid; k < nb; k += kThreads) h[k] = 0;
         __syncthreads();
       }
@@ -184,27 +198,28 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
             const int j = j0 + i * kThreads;
             if (j < m1) {
               const uint32_t u = order_of(x[i]);
-              if (held) slice[j - s0] = u;
+              if (held) slice[j - s0] = (uint16_t)(u >> 16);
               atomicAdd(&h[u >> 21], 1);
             }
           }
         }
       } else {
         for (int j = m0 + tid; j < m1; j += kThreads) {
-          const uint32_t u = weight_at(j);
+          const uint32_t u = weight_at(j, fixed, pass == 1 ? 0xffff0000u : 0xffffffffu);
           if ((u & mask) == fixed) atomicAdd(&h[(u >> shift) & (nb - 1)], 1);
         }
       }
       if (C > 1) cluster_sync();
       __syncthreads();
       // bins from above: thread t holds bins nb - 1 - t * each ..
-      const int each = nb / kThreads;
-      int c[kBins / kThreads], sum = 0;
+      constexpr int kMost = kBins / kThreads;
+      const int each = nb == kBins ? kMost : 1;
+      int c[kMost], sum = 0;
 #pragma unroll
-      for (int k = 0; k < kBins / kThreads; ++k) {
+      for (int k = 0; k < kMost; ++k) {
         c[k] = 0;
-        if (k < each) {
-          const int bin = nb - 1 - tid * each - k;
+        const int bin = nb - 1 - tid * each - k;
+        if (k < each && bin >= 0) {
           if (C == 1) {
             c[k] = h[bin];
           } else {
@@ -218,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
       int run = block_scan(sum, warp_sums, &all);
       if (run < want && run + sum >= want) {
 #pragma unroll
-        for (int k = 0; k < kBins / kThreads; ++k) {
+        for (int k = 0; k < kMost; ++k) {
           if (run < want && run + c[k] >= want) {
             pick[0] = nb - 1 - tid * each - k;
             pick[1] = want - run;
@@ -229,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
       }
       __syncthreads();
       fixed |= (uint32_t)pick[0] << shift;
-      mask = pass == 0 ? 0xffe00000u : pass == 1 ? 0xfffffc00u : 0xffffffffu;
+      mask = 0xffffffffu << shift;
       want = pick[1];
       same_all = want == pick[2];   // all that share the digits survive
       if (same_all) break;
@@ -246,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
   for (int k = w0; k < w1; ++k) {
     const int j = k * 32 + lane;
     const bool mid = j >= lo && j < hi && rest > 0;
-    const uint32_t u = mid ? weight_at(j) & mask : 0u;
+    const uint32_t u = mid ? weight_at(j, fixed, mask) & mask : 0u;
     const bool more = j < lo || (j >= hi && j < n) || (mid && u > fixed), same = mid && u == fixed;
     const uint32_t mm = __ballot_sync(0xffffffffu, more), ms = __ballot_sync(0xffffffffu, same);
     if (lane == 0) {
@@ -328,12 +343,13 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
   const int par = kThreads / nc, my_r = tid / nc, my_c = c0 + tid - my_r * nc;   // this thread's first row, and its column
   const bool in_k = my_c < p.k_chunks;
   const int stride = in_k ? p.k_chunks : p.v_chunks;
-  uint4* const col = in_k ? static_cast<uint4*>(p.k_cache) + my_c : static_cast<uint4*>(p.v_cache) + (my_c - p.k_chunks);
-  for (int k0 = min(pick[2], keep); k0 < keep; k0 += kThreads) {
-    const int m = min(kThreads, keep - k0);
+  uint4* const col = (in_k ? static_cast<uint4*>(p.k_cache) + my_c : static_cast<uint4*>(p.v_cache) + (my_c - p.k_chunks)) +
+                     layer_row * stride;
+  for (int k0 = min(pick[2], keep); k0 < keep; k0 += kRanks) {
+    const int m = min(kRanks, keep - k0);
     __syncthreads();
-    if (tid < m) {
-      const int k = k0 + tid;
+    for (int i = tid; i < m; i += kThreads) {
+      const int k = k0 + i;
       int a = 0, z = words;   // the last word with before[word] <= k
       while (z - a > 1) {
         const int mid = (a + z) >> 1;
@@ -341,8 +357,8 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
       }
       uint32_t x = bits[a];
       for (int t = k - before[a]; t > 0; --t) x &= x - 1;
-      src_row[tid] = row_of(min(a * 32 + (x ? __ffs(x) - 1 : 0), n - 1));
-      dst_row[tid] = row_of(k);
+      src_row[i] = row_of(min(a * 32 + (x ? __ffs(x) - 1 : 0), n - 1));
+      dst_row[i] = row_of(k);
     }
     __syncthreads();
     for (int r0 = 0; r0 < m; r0 += par * kBatch) {
@@ -350,21 +366,23 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int r = r0 + my_r + i * par;
-        if (r < m && my_r < par) v[i] = col[src_row[r] * stride];
+        if (r < m && my_r < par) v[i] = col[(size_t)src_row[r] * stride];
       }
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int r = r0 + my_r + i * par;
-        if (r < m && my_r < par) col[dst_row[r] * stride] = v[i];
+        if (r < m && my_r < par) col[(size_t)dst_row[r] * stride] = v[i];
       }
     }
-    if (rank == 0) {
-      float v = 0.f;
-      if (tid < m) v = w[src_row[tid]];
-      __syncthreads();
-      if (tid < m) w[dst_row[tid]] = v;
-    }
+    if (rank == 0)
+      for (int r0 = 0; r0 < m; r0 += kThreads) {
+        const int r = r0 + tid;
+        float v = 0.f;
+        if (r < m) v = w[src_row[r]];
+        __syncthreads();
+        if (r < m) w[dst_row[r]] = v;
+      }
   }
 }
 
@@ -372,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) paged_kv_evict_kernel(const EvictPar
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
   const long long units = (long long)p.layers * p.batch * p.h_kv;
-  const size_t smem = (size_t)p.words * 8 + (size_t)p.slice_cap * 4;
+  const size_t smem = evict_smem(p.words, p.slice_cap);
   const void* k = reinterpret_cast<const void*>(paged_kv_evict_kernel);
   // (the same value for every call: calls of several threads set it side by side)
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictMaxSmem);

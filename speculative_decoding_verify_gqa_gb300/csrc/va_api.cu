@@ -1360,10 +1360,21 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
     rc = query_sms(&num_sms);
     if (rc) return rc;
   }
+  // CTAs per unit: twice as many while all CTAs still run at a time and every
+  // one moves 64 bytes of a row -- or 32, where most of the GPU would stay idle.
+  const int64_t all = units * num_kv_heads;
+  const int chunks = p.k_chunks + p.v_chunks;
+  auto slice = [&](int cluster) {
+    const int64_t n = ((max_kv_len + cluster - 1) / cluster + 31) / 32 * 32;
+    return evict_smem(p.words, (int)n) <= (size_t)kEvictMaxSmem ? (int)n : 0;
+  };
   p.cluster = 1;
-  while (p.cluster < kMaxCluster && units * num_kv_heads * p.cluster * 2 <= 4LL * num_sms) p.cluster *= 2;
-  const int64_t slice = ((max_kv_len + p.cluster - 1) / p.cluster + 31) / 32 * 32;
-  p.slice_cap = slice <= kEvictMaxSlice ? (int)slice : 0;
+  for (int c = 2; c <= kMaxCluster; c *= 2) {
+    const int64_t resident = (int64_t)num_sms * std::min<int64_t>(2, 228 * 1024 / (evict_smem(p.words, slice(c)) + kEvictStatic));
+    if (all * c > resident || chunks / c < (all * c * 2 <= num_sms ? 2 : 4)) break;
+    p.cluster = c;
+  }
+  p.slice_cap = slice(p.cluster);
   cudaError_t e = launch_evict(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }

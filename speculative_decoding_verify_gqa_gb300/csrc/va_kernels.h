@@ -220,8 +220,9 @@ cudaError_t launch_key_weights(const KeyWeightParams& p, const CUtensorMap& kmap
 
 // Eviction of the keys with the least weight (see k_evict.cu).
 constexpr int kEvictMaxKeys = 1 << 19;  // keys of a request: a bit and a count per word in shared memory
-constexpr int kEvictMaxSlice = 1 << 14; // weights that a CTA holds in shared memory
-constexpr int kEvictMaxSmem = kEvictMaxKeys / 4 + kEvictMaxSlice * 4;
+constexpr int kEvictStatic = 18 * 1024;   // static shared memory of a CTA, and what the system keeps of it
+constexpr int kEvictMaxSmem = 227 * 1024 - kEvictStatic;
+inline size_t evict_smem(int words, int slice) { return (size_t)words * 8 + (size_t)slice * 2; }
 struct EvictParams {
   float* key_weights;         // [layers, rows of a layer]
   const int32_t* keep_len;    // [batch]
