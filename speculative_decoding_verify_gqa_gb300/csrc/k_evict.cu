@@ -13,7 +13,9 @@
 // their slices, and each adds up all counts by reading the others' shared
 // memory.  The lower halves are read from the cache again, for the few keys that
 // share the upper one.  It ends as soon as all keys that share the digits found
-// survive.  Then each CTA marks its slice, one bit a key, and every CTA gathers
+// survive.  (Up to 16,384 keys every CTA holds all weights and counts for itself:
+// a meeting of the cluster costs about a microsecond, and a select has up to
+// six.)  Then each CTA marks its slice, one bit a key, and every CTA gathers
 // all bits and counts them by words, so that the k-th survivor is found by a
 // search over the words.
 //
@@ -62,10 +64,30 @@ __device__ __forceinline__ uint32_t remote(uint32_t addr, int rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+__device__ __forceinline__ int4 ld_remote4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t ld_remote(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+
+// position of the t-th set bit of x (t < popc(x))
+__device__ __forceinline__ int nth_bit(uint32_t x, int t) {
+  int pos = 0;
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    const int c = __popc(x & ((1u << w) - 1u));
+    if (t >= c) {
+      t -= c;
+      x >>= w;
+      pos += w;
+    }
+  }
+  return pos;
 }
 
 // exclusive sum over the threads of the CTA; *total receives the whole sum
@@ -96,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
   uint32_t* const bits = dyn;                                  // one bit a key: it survives
   int* const before = reinterpret_cast<int*>(dyn + p.words);   // survivors before each word
   uint16_t* const slice = reinterpret_cast<uint16_t*>(dyn + 2 * p.words);   // this CTA's weights, upper halves
-  __shared__ int hist[2][kBins];
+  __shared__ __align__(16) int hist[2][kBins];
   uint32_t* const src_row = reinterpret_cast<uint32_t*>(hist[0]);   // (when the counts are done with)
   uint32_t* const dst_row = reinterpret_cast<uint32_t*>(hist[1]);
   __shared__ int warp_sums[kWarps], geo[5], pick[3], count;
@@ -161,7 +183,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
 
   // the middle [lo, hi) competes for `rest` places; this CTA looks after [s0, s1)
   const int lo = min(p.sinks, keep), hi = n - min(p.recent, keep - lo), rest = keep - lo - (n - hi);
-  const int per = ((n + C - 1) / C + 31) & ~31, s0 = min(rank * per, n), s1 = min(s0 + per, n);
+  const bool alone = n <= kEvictAlone || C == 1;
+  const int S = alone ? 1 : C, srank = alone ? 0 : rank;
+  const int per = ((n + S - 1) / S + 31) & ~31, s0 = min(srank * per, n), s1 = min(s0 + per, n);
   const int m0 = max(s0, lo), m1 = min(s1, hi);
   const bool held = per <= p.slice_cap;   // (else the weights are read again from the cache)
   // the weight of key j as far as `mask` tells: the lower half is only looked at where the upper one is `fixed`'s
@@ -204,38 +228,44 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
           }
         }
       } else {
+#pragma unroll 4
         for (int j = m0 + tid; j < m1; j += kThreads) {
           const uint32_t u = weight_at(j, fixed, pass == 1 ? 0xffff0000u : 0xffffffffu);
           if ((u & mask) == fixed) atomicAdd(&h[(u >> shift) & (nb - 1)], 1);
         }
       }
-      if (C > 1) cluster_sync();
+      if (S > 1) cluster_sync();
       __syncthreads();
-      // bins from above: thread t holds bins nb - 1 - t * each ..
+      // bins from above: thread t holds four, nb - 1 - 4 t ..
       constexpr int kMost = kBins / kThreads;
-      const int each = nb == kBins ? kMost : 1;
-      int c[kMost], sum = 0;
+      static_assert(kMost == 4, "bins of a thread");
+      int c[kMost] = {0, 0, 0, 0};
+      if (tid * kMost < nb) {
+        const int4* const at = reinterpret_cast<const int4*>(h + nb - kMost - tid * kMost);
+        int4 v = *at;
+        if (S > 1) {
+          const uint32_t a = smem_u32(at);
+          int4 o[8];   // (all others' counts under way together)
 #pragma unroll
-      for (int k = 0; k < kMost; ++k) {
-        c[k] = 0;
-        const int bin = nb - 1 - tid * each - k;
-        if (k < each && bin >= 0) {
-          if (C == 1) {
-            c[k] = h[bin];
-          } else {
-            const uint32_t a = smem_u32(h + bin);
-            for (int r = 0; r < C; ++r) c[k] += (int)ld_remote(remote(a, r));
-          }
+          for (int r = 0; r < 8; ++r)
+            if (r < S && r != rank) o[r] = ld_remote4(remote(a, r));
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (r < S && r != rank) v = make_int4(v.x + o[r].x, v.y + o[r].y, v.z + o[r].z, v.w + o[r].w);
         }
-        sum += c[k];
+        c[0] = v.w;
+        c[1] = v.z;
+        c[2] = v.y;
+        c[3] = v.x;
       }
+      const int sum = c[0] + c[1] + c[2] + c[3];
       int all;
       int run = block_scan(sum, warp_sums, &all);
       if (run < want && run + sum >= want) {
 #pragma unroll
         for (int k = 0; k < kMost; ++k) {
           if (run < want && run + c[k] >= want) {
-            pick[0] = nb - 1 - tid * each - k;
+            pick[0] = nb - 1 - tid * kMost - k;
             pick[1] = want - run;
             pick[2] = c[k];
           }
@@ -258,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
   const int per_warp = (nv + kWarps - 1) / kWarps;
   const int w0 = v0 + min(warp * per_warp, nv), w1 = v0 + min((warp + 1) * per_warp, nv);
   int equal = 0;
+#pragma unroll 4
   for (int k = w0; k < w1; ++k) {
     const int j = k * 32 + lane;
     const bool mid = j >= lo && j < hi && rest > 0;
@@ -275,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
     // some of the equals go: those behind the first `ties` of all slices
     int run = block_scan(lane == 0 ? equal : 0, warp_sums, &all);
     run = __shfl_sync(0xffffffffu, run, 0);
-    if (C > 1) {
+    if (S > 1) {
       if (tid == 0) count = all;
       cluster_sync();
       for (int r = 0; r < rank; ++r) run += (int)ld_remote(remote(smem_u32(&count), r));
@@ -305,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
     }
   }
   __syncthreads();
-  if (C > 1) {
+  if (S > 1) {
     // gather: words of CTA r's slice from its shared memory
     cluster_sync();
     const int words_per = per >> 5;
@@ -313,8 +344,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
       if (k < v0 || k >= v0 + nv) bits[k] = ld_remote(remote(smem_u32(bits + k), k / words_per));
     if (tid == 0) pick[2] = n;
     cluster_sync();   // nobody leaves, or moves weights, while others read
-  } else if (tid == 0) {
-    pick[2] = n;
+  } else {
+    if (tid == 0) pick[2] = n;
+    if (C > 1) cluster_sync();   // CTA 0 moves weights when all have read them
   }
   __syncthreads();
   {
@@ -348,17 +380,34 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
   for (int k0 = min(pick[2], keep); k0 < keep; k0 += kRanks) {
     const int m = min(kRanks, keep - k0);
     __syncthreads();
-    for (int i = tid; i < m; i += kThreads) {
-      const int k = k0 + i;
-      int a = 0, z = words;   // the last word with before[word] <= k
-      while (z - a > 1) {
-        const int mid = (a + z) >> 1;
-        if (before[mid] <= k) a = mid; else z = mid;
+    {
+      // four ranks a thread, step by step together: the last word with before[word] <= k, its bit, the pages
+      constexpr int kEach = kRanks / kThreads;
+      int a[kEach], page[kEach], to[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) a[i] = 0;
+      for (int half = 1 << (31 - __clz(words)); half > 0; half >>= 1) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int mid = a[i] + half;
+          if (mid < words && before[mid] <= k0 + tid + i * kThreads) a[i] = mid;
+        }
       }
-      uint32_t x = bits[a];
-      for (int t = k - before[a]; t > 0; --t) x &= x - 1;
-      src_row[i] = row_of(min(a * 32 + (x ? __ffs(x) - 1 : 0), n - 1));
-      dst_row[i] = row_of(k);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int k = min(k0 + tid + i * kThreads, keep - 1);
+        a[i] = min(a[i] * 32 + nth_bit(bits[a[i]], k - before[a[i]]), n - 1);
+        page[i] = p.kv_indices[pg0 + (a[i] >> p.log2_page)];
+        to[i] = p.kv_indices[pg0 + (k >> p.log2_page)];
+      }
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int r = tid + i * kThreads;
+        if (r < m) {
+          src_row[r] = row_at(page[i], a[i]);
+          dst_row[r] = row_at(to[i], k0 + r);
+        }
+      }
     }
     __syncthreads();
     for (int r0 = 0; r0 < m; r0 += par * kBatch) {

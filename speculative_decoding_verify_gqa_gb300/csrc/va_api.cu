@@ -1365,7 +1365,9 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
   const int64_t all = units * num_kv_heads;
   const int chunks = p.k_chunks + p.v_chunks;
   auto slice = [&](int cluster) {
-    const int64_t n = ((max_kv_len + cluster - 1) / cluster + 31) / 32 * 32;
+    // (short requests are ranked whole by every CTA)
+    const int64_t n = std::max(((max_kv_len + cluster - 1) / cluster + 31) / 32 * 32,
+                               (std::min<int64_t>(max_kv_len, kEvictAlone) + 31) / 32 * 32);
     return evict_smem(p.words, (int)n) <= (size_t)kEvictMaxSmem ? (int)n : 0;
   };
   p.cluster = 1;
