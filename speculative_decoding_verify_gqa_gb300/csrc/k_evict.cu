@@ -43,7 +43,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1 << 11;
-constexpr int kRanks = kBins;  // survivors whose rows are resolved at a time
+constexpr int kRanks = 1024;  // most rows of a batch
 constexpr int kBatch = 8;   // rows' chunks in flight per thread
 constexpr int kAhead = 8;   // weights in flight per thread
 
@@ -118,9 +118,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
   uint32_t* const bits = dyn;                                  // one bit a key: it survives
   int* const before = reinterpret_cast<int*>(dyn + p.words);   // survivors before each word
   uint16_t* const slice = reinterpret_cast<uint16_t*>(dyn + 2 * p.words);   // this CTA's weights, upper halves
-  __shared__ __align__(16) int hist[2][kBins];
-  uint32_t* const src_row = reinterpret_cast<uint32_t*>(hist[0]);   // (when the counts are done with)
-  uint32_t* const dst_row = reinterpret_cast<uint32_t*>(hist[1]);
+  // the counts; later the rows of three batches, from and to
+  __shared__ __align__(16) int hist[3][kBins];
+  static_assert(2 * kRanks <= kBins, "a batch's rows");
   __shared__ int warp_sums[kWarps], geo[5], pick[3], count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = p.cluster, rank = blockIdx.x % C;
@@ -377,61 +377,79 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
   const int stride = in_k ? p.k_chunks : p.v_chunks;
   uint4* const col = (in_k ? static_cast<uint4*>(p.k_cache) + my_c : static_cast<uint4*>(p.v_cache) + (my_c - p.k_chunks)) +
                      layer_row * stride;
-  for (int k0 = min(pick[2], keep); k0 < keep; k0 += kRanks) {
-    const int m = min(kRanks, keep - k0);
-    __syncthreads();
-    {
-      // four ranks a thread, step by step together: the last word with before[word] <= k, its bit, the pages
-      constexpr int kEach = kRanks / kThreads;
-      int a[kEach], page[kEach], to[kEach];
+  // The rows of ranks k0 .. k0 + kRanks - 1: the last word with before[word] <=
+  // k, its bit, the pages.  A list is made while rows of the one before are
+  // under way.
+  const int rows = min(par * kBatch, kRanks), top = 1 << (31 - __clz(words));
+  auto resolve = [&](int k0, uint32_t* from, uint32_t* to) {
+    constexpr int kEach = kRanks / kThreads;
+    int a[kEach], page[kEach], page_to[kEach];
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) a[i] = 0;
-      for (int half = 1 << (31 - __clz(words)); half > 0; half >>= 1) {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          const int mid = a[i] + half;
-          if (mid < words && before[mid] <= k0 + tid + i * kThreads) a[i] = mid;
-        }
-      }
+    for (int i = 0; i < kEach; ++i) a[i] = 0;
+#pragma unroll 1
+    for (int half = top; half > 0; half >>= 1) {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int k = min(k0 + tid + i * kThreads, keep - 1);
-        a[i] = min(a[i] * 32 + nth_bit(bits[a[i]], k - before[a[i]]), n - 1);
-        page[i] = p.kv_indices[pg0 + (a[i] >> p.log2_page)];
-        to[i] = p.kv_indices[pg0 + (k >> p.log2_page)];
-      }
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int r = tid + i * kThreads;
-        if (r < m) {
-          src_row[r] = row_at(page[i], a[i]);
-          dst_row[r] = row_at(to[i], k0 + r);
-        }
+        const int mid = a[i] + half;
+        if (mid < words && before[mid] <= k0 + tid + i * kThreads) a[i] = mid;
       }
     }
-    __syncthreads();
-    for (int r0 = 0; r0 < m; r0 += par * kBatch) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int k = min(k0 + tid + i * kThreads, keep - 1);
+      a[i] = min(a[i] * 32 + nth_bit(bits[a[i]], k - before[a[i]]), n - 1);
+      page[i] = p.kv_indices[pg0 + (a[i] >> p.log2_page)];
+      page_to[i] = p.kv_indices[pg0 + (k >> p.log2_page)];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int r = tid + i * kThreads;
+      from[r] = row_at(page[i], a[i]);
+      to[r] = row_at(page_to[i], k0 + r);
+    }
+  };
+  int k0 = min(pick[2], keep);
+  __syncthreads();
+  int next = 0;   // list that is made next
+  uint32_t* list = reinterpret_cast<uint32_t*>(hist[0]);
+  if (k0 < keep) resolve(k0, list, list + kRanks);
+  __syncthreads();
+  for (; k0 < keep; k0 += kRanks) {
+    next = next == 2 ? 0 : next + 1;
+    uint32_t* const list_next = reinterpret_cast<uint32_t*>(hist[next]);
+    const int m = min(kRanks, keep - k0);
+    for (int r0 = 0; r0 < m; r0 += rows) {
       uint4 v[kBatch];
+      float x[kRanks / kThreads];
+      const int end = min(m, r0 + rows);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int r = r0 + my_r + i * par;
-        if (r < m && my_r < par) v[i] = col[(size_t)src_row[r] * stride];
+        if (r < end && my_r < par) v[i] = col[(size_t)list[r] * stride];
       }
+      if (rank == 0) {
+#pragma unroll
+        for (int i = 0; i < kRanks / kThreads; ++i) {
+          const int r = r0 + tid + i * kThreads;
+          if (r < end) x[i] = w[list[r]];
+        }
+      }
+      if (r0 == 0 && k0 + kRanks < keep) resolve(k0 + kRanks, list_next, list_next + kRanks);
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int r = r0 + my_r + i * par;
-        if (r < m && my_r < par) col[(size_t)dst_row[r] * stride] = v[i];
+        if (r < end && my_r < par) col[(size_t)list[kRanks + r] * stride] = v[i];
+      }
+      if (rank == 0) {
+#pragma unroll
+        for (int i = 0; i < kRanks / kThreads; ++i) {
+          const int r = r0 + tid + i * kThreads;
+          if (r < end) w[list[kRanks + r]] = x[i];
+        }
       }
     }
-    if (rank == 0)
-      for (int r0 = 0; r0 < m; r0 += kThreads) {
-        const int r = r0 + tid;
-        float v = 0.f;
-        if (r < m) v = w[src_row[r]];
-        __syncthreads();
-        if (r < m) w[dst_row[r]] = v;
-      }
+    list = list_next;
   }
 }
 

@@ -221,7 +221,7 @@ cudaError_t launch_key_weights(const KeyWeightParams& p, const CUtensorMap& kmap
 // Eviction of the keys with the least weight (see k_evict.cu).
 constexpr int kEvictMaxKeys = 1 << 19;  // keys of a request: a bit and a count per word in shared memory
 constexpr int kEvictAlone = 1 << 14;      // keys up to which every CTA ranks all of a unit's weights by itself
-constexpr int kEvictStatic = 18 * 1024;   // static shared memory of a CTA, and what the system keeps of it
+constexpr int kEvictStatic = 26 * 1024;   // static shared memory of a CTA, and what the system keeps of it
 constexpr int kEvictMaxSmem = 227 * 1024 - kEvictStatic;
 inline size_t evict_smem(int words, int slice) { return (size_t)words * 8 + (size_t)slice * 2; }
 struct EvictParams {
