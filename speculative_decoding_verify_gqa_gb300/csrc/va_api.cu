@@ -1219,7 +1219,10 @@ int paged_qkv_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
     const double part = turns - floor(turns);           // positions are whole: whole turns drop out
     p.turn[j] = part >= 1.0 ? 0 : (uint64_t)ldexp(part, 64);
   }
-  cudaError_t e = launch_qkv_append(p, head_dim, static_cast<cudaStream_t>(stream));
+  int num_sms = 0;
+  rc = query_sms(&num_sms);
+  if (rc) return rc;
+  cudaError_t e = launch_qkv_append(p, head_dim, num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }
 

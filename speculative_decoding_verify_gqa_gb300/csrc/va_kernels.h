@@ -187,9 +187,10 @@ struct QkvParams {
   int quant;                  // e4m3 cache: stored = e4m3(x / scale)
   int nhd;
   float weight_offset, eps, k_scale, v_scale;
+  int per_cta;                // tokens of a CTA (set by the launcher)
   uint64_t turn[64];          // frequency of pair i in turns per position, times 2^64
 };
-cudaError_t launch_qkv_append(const QkvParams& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_qkv_append(const QkvParams& p, int head_dim, int num_sms, cudaStream_t stream);
 
 // Attention weight received by each cached key (see k_key_weights.cu).
 struct KeyWeightParams {

@@ -138,6 +138,11 @@ CASES = [
     dict(lens=[6], pre=[3], far=2 ** 31 - 1, hq=16, h=2, inter=True),
     dict(lens=[1] * 300, pre=[3] * 300, hq=2, h=1, d=64),
     dict(lens=[5, 3], pre=[3, 0], hq=8, h=8, pad=11),
+    # more tokens than CTAs: runs of tokens
+    dict(lens=[700, 0, 1, 411], pre=[5, 0, 77, 0], hq=8, h=2, pad=9),
+    dict(lens=[1500], pre=[0], hq=6, h=3, d=64, dv=128, fp8=True, nhd=True, rot=32, inter=True, weights="f32", offset=1.0),
+    dict(lens=[460, 460], pre=[3, 0], hq=40, h=2, fused=False, page=64),
+    dict(lens=[930], pre=[0], hq=128, h=8, page=32),
 ]
 
 
