@@ -1068,30 +1068,29 @@ def paged_qkv_append(q, k, v, append_indptr, kv_indptr, kv_indices, last_page_le
         q_out = torch.empty((total, h_q, d), dtype=torch.bfloat16, device=q.device)
     elif q_out.shape != (total, h_q, d):
         raise ValueError("q_out must be [%d, %d, %d]" % (total, h_q, d))
-    o = QkvOptions()
-    w = q_weight if q_weight is not None else k_weight
+    w, wc, qw, kw = q_weight if q_weight is not None else k_weight, 0, None, None
     if w is not None:
         if w.dtype not in _CODES:
             raise ValueError("q_weight and k_weight must be bfloat16 or float32")
-        o.weight_dtype = _CODES[w.dtype]
-        o.q_weight = _arg(q_weight, "q_weight", w.dtype, d, dev)
-        o.k_weight = _arg(k_weight, "k_weight", w.dtype, d, dev)
-        o.weight_offset, o.eps = weight_offset, eps
-    freq = None
-    if positions is not None:
-        o.positions = _arg(positions, "positions", i32, total, dev)
-        o.rotary_dim = rotary_dim = d if rotary_dim is None else int(rotary_dim)
-        o.interleaved = 1 if interleaved else 0
-        if inv_freq is None:
-            o.rope_theta, o.rope_scale = rope_theta, rope_scale
-        else:
+        wc = _CODES[w.dtype]
+        qw, kw = _arg(q_weight, "q_weight", w.dtype, d, dev), _arg(k_weight, "k_weight", w.dtype, d, dev)
+    else:
+        weight_offset = eps = 0.0
+    pos, freq, freq_p = None, None, None
+    if positions is None:
+        rotary_dim = 0
+    else:
+        pos = _arg(positions, "positions", i32, total, dev)
+        rotary_dim = d if rotary_dim is None else int(rotary_dim)
+        if inv_freq is not None:
             freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
             if freq.shape != (rotary_dim // 2,):
                 raise ValueError("inv_freq must hold %d frequencies" % (rotary_dim // 2))
-            o.inv_freq = freq.ctypes.data
-    if code == KV_FP8_E4M3:
-        o.k_scale, o.v_scale = k_scale, v_scale
-    o.kv_layout, o.head_dim_v = layout, dv
+            freq_p = freq.ctypes.data
+    if code == KV_BF16:
+        k_scale = v_scale = 0.0
+    o = QkvOptions(qw, kw, wc, weight_offset, eps, pos, rotary_dim, 1 if interleaved else 0, rope_theta, rope_scale,
+                   freq_p, k_scale, v_scale, layout, dv)
     rc = lib().paged_qkv_append(
         qp, qs, kp, ks, vp, vs, _arg(append_indptr, "append_indptr", i32, batch + 1, dev),
         _arg(kv_indptr, "kv_indptr", i32, batch + 1, dev),

@@ -1212,12 +1212,20 @@ int paged_qkv_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
   p.eps = o.eps;
   p.k_scale = o.k_scale;
   p.v_scale = o.v_scale;
+  // theta^(-2j / rotary_dim) as the product of two of sixteen powers (64 powers
+  // took as long as the rest of the call)
+  double lo[8] = {}, hi[8] = {};
+  if (o.rotary_dim > 0 && !o.inv_freq)
+    for (int j = 0; j < 8; ++j) {
+      lo[j] = pow((double)o.rope_theta, -2.0 * j / o.rotary_dim);
+      hi[j] = pow((double)o.rope_theta, -16.0 * j / o.rotary_dim) / (double)rope_scale;
+    }
   for (int j = 0; 2 * j < o.rotary_dim; ++j) {
-    const double f = o.inv_freq ? o.inv_freq[j] : pow((double)o.rope_theta, -2.0 * j / o.rotary_dim) / (double)rope_scale;
+    const double f = o.inv_freq ? o.inv_freq[j] : lo[j & 7] * hi[j >> 3];
     if (!isfinite(f)) return VA_ERR_INVALID_ARGUMENT;
     const double turns = f * 0.15915494309189533577;   // 1 / (2 pi)
     const double part = turns - floor(turns);           // positions are whole: whole turns drop out
-    p.turn[j] = part >= 1.0 ? 0 : (uint64_t)ldexp(part, 64);
+    p.turn[j] = part >= 1.0 ? 0 : (uint64_t)(part * 18446744073709551616.0);   // 2^64, exactly
   }
   int num_sms = 0;
   rc = query_sms(&num_sms);
