@@ -764,9 +764,11 @@ int paged_qkv_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
  * key makes the weights NaN of the keys seen with it.  Masked keys may hold
  * anything.  A request whose tables or path are invalid is skipped with
  * VA_DEV_BAD_TABLE, a key whose page lies outside the pool with VA_DEV_BAD_PAGE
- * (status_d, nullable).  Each sum is made in fp32 in a fixed order.  No
- * workspace; num_sms <= 0 queries the current device.
- * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED, VA_ERR_CUDA.
+ * (status_d, nullable).  With an fp8 cache q is taken as f16, as in the tcgen05
+ * attention kernels: |q| must stay below 65504.  Each sum is made in fp32 in a
+ * fixed order.  No workspace; num_sms <= 0 queries the current device.
+ * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED (among others more than
+ * 65,535 requests), VA_ERR_CUDA.
  */
 int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* kv_indptr,
                             const int32_t* kv_indices, const int32_t* last_page_len,

@@ -16,7 +16,7 @@ LIB = os.path.join(PKG, "libverify_attn.so")
 
 SOURCES = ["va_api.cu", "va_planner.cpp", "va_plan_shared.cpp", "k_partial_mma.cu", "k_partial_tc.cu", "k_merge_append.cu",
            "k_accept.cu", "k_accept_sample.cu", "k_compact.cu", "k_qkv_append.cu", "k_key_weights.cu", "k_evict.cu"]
-HEADERS = ["va_internal.h", "va_planner.h", "va_kernels.h", "va_device.cuh", "va_tc.cuh"]
+HEADERS = ["va_budget.h", "va_internal.h", "va_planner.h", "va_kernels.h", "va_device.cuh", "va_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
                      "-Xcompiler", "-fPIC,-O2", "-I", os.path.join(ROOT, "include"),

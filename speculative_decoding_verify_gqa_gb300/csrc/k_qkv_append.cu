@@ -34,6 +34,7 @@
 #include <algorithm>
 
 #include "../../include/verify_attn.h"
+#include "va_budget.h"
 #include "va_device.cuh"
 #include "va_kernels.h"
 #include "va_tc.cuh"

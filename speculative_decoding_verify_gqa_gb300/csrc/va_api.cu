@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/verify_attn.h"
+#include "va_budget.h"
 #include "va_internal.h"
 #include "va_kernels.h"
 
@@ -1253,7 +1254,7 @@ int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* k
   const float scale = sm_scale > 0.f ? sm_scale : 1.f / sqrtf((float)head_dim);
   if (!(isfinite(k_scale) && k_scale > 0.f) || !isfinite(scale * k_scale) || !(isfinite(decay) && decay >= 0.f))
     return VA_ERR_INVALID_ARGUMENT;
-  if (total_qo > 0x7fffffffLL) return VA_ERR_UNSUPPORTED;
+  if (total_qo > 0x7fffffffLL || batch > 65535) return VA_ERR_UNSUPPORTED;
   if (batch == 0) return VA_OK;
   if (!k_cache || !kv_indptr || !kv_indices || !last_page_len || !qo_indptr || !key_weights || num_pages <= 0 ||
       (total_qo > 0 && (!q || !lse)))
@@ -1379,7 +1380,8 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
     // (short requests are ranked whole by every CTA)
     const int64_t n = std::max(((max_kv_len + cluster - 1) / cluster + 31) / 32 * 32,
                                (std::min<int64_t>(max_kv_len, kEvictAlone) + 31) / 32 * 32);
-    return evict_smem(p.words, (int)n) <= (size_t)kEvictMaxSmem ? (int)n : 0;
+    // as many of them as there is room for: longer slices are read from the cache in every pass
+    return (int)std::min<int64_t>(n, ((int64_t)kEvictMaxSmem - (int64_t)evict_smem(p.words, 0)) / 64 * 32);
   };
   p.cluster = 1;
   for (int c = 2; c <= kMaxCluster; c *= 2) {

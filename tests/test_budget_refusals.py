@@ -78,7 +78,7 @@ def _weights(va, **kw):
     (dict(mask=64, mi=64, acc=64, path=64), INVALID), (dict(ks=0.0), INVALID), (dict(ks=float("inf")), INVALID),
     (dict(scale=1e38, ks=1e38), INVALID), (dict(decay=-0.5), INVALID), (dict(decay=float("nan")), INVALID),
     (dict(q=0), INVALID), (dict(lse=0), INVALID), (dict(w=0), INVALID), (dict(k=A + 8), INVALID), (dict(q=A + 2), INVALID),
-    (dict(pages=0), INVALID), (dict(total=1 << 31), UNSUPPORTED), (dict(batch=0), 0),
+    (dict(pages=0), INVALID), (dict(total=1 << 31), UNSUPPORTED), (dict(batch=65536), UNSUPPORTED), (dict(batch=0), 0),
 ])
 def test_key_weights_refuses(va, kw, status):
     assert _weights(va, **kw) == status

@@ -106,6 +106,14 @@ CASES = [
     dict(lens=[40] * 40, keep=[13] * 40, layers=3, h=2),
     dict(lens=[3000], keep=[0]),
     dict(lens=[9000], keep=[4500], sinks=4, recent=100, h=1, page=128),
+    # longer than what every CTA of a cluster ranks by itself
+    dict(lens=[20001, 300], keep=[5000, 250], sinks=4, recent=100, h=1, d=64),
+    dict(lens=[17000], keep=[9000], h=2, d=64, values="equal", nhd=True, page=8),
+    dict(lens=[18500], keep=[6000], h=1, d=64, values="few", recent=33),
+    dict(lens=[16500], keep=[12000], h=1, d=128, values="special", fp8=True),
+    dict(lens=[30000], keep=[100], h=1, d=64, values="close", sinks=1),
+    # many units: one CTA each
+    dict(lens=[70, 50] * 40, keep=[30, 45] * 40, layers=4, h=2, d=64, values="few", recent=3),
 ]
 
 
@@ -152,6 +160,13 @@ def test_twice_and_graph(va):
     for n in ("kvp", "last", "keep"):
         c.dev[n].copy_(torch.from_numpy(getattr(c, n)))
     g.replay()
+    c.check()
+
+
+def test_longer_than_shared_memory_holds(va):
+    """Slices that are read from the cache in every pass: 310,000 keys with the largest bound."""
+    c = Case(104, [310000], [200000], sinks=3, recent=1000, h=1, d=64, fp8=True, page=256)
+    c.run(va, max_kv_len=1 << 19)
     c.check()
 
 
