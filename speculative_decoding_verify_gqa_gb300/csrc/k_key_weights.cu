@@ -251,12 +251,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 // Wait for the tensor-memory loads under way; the registers pass through, so
 // that nothing reads or moves them before.
-__device__ __forceinline__ void tmem_wait8(uint32_t (&r)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
-               :
-               : "memory");
-}
 __device__ __forceinline__ void tmem_wait32(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
@@ -559,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.mask) {
             if (p.mask_full || border + 31 >= 0) vis = kTile;
           } else {
-            from = min(max(max(border, -64) * p.group - r0, 0), kTile) & ~7;
+            from = min(max(max(border, -64) * p.group - r0, 0), kTile) & ~31;
             vis = max(max(border + 31, -64) * p.group - r0, 0);
           }
           const uint32_t at = cols + buf * kTile;
@@ -583,42 +577,36 @@ __global__ void __launch_bounds__(kThreads, 1)
               k += 32;
               continue;
             }
-            if (!p.mask && k + 32 <= nr) {   // across the causal border
-              uint32_t x[32];
-              tmem_ld32(at + k, x);
-              tmem_wait32(x);
-              const int lo = draft * p.group - (r0 + k);
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) add4(x + i, k + i, i >= lo, i + 1 >= lo, i + 2 >= lo, i + 3 >= lo);
-              k += 32;
-              continue;
-            }
-            // 8 rows: which of them see the key -- up to the chunk's end, from the causal border on, or by the mask
-            uint32_t x[8];
-            tmem_ld8(at + k, x);
-            uint32_t on = 0xffu;
+            // which of the 32 rows see the key: up to the chunk's end, from the causal border on, or by the mask
+            uint32_t x[32];
+            tmem_ld32(at + k, x);
+            uint32_t on = 0xffffffffu;
             if (k < vis) {
               const int row = r0 + k;
-              if (!mine) {
-                on = 0;
-              } else if (!p.mask || (!p.mask_full && draft < 0)) {
-                on <<= draft <= 0 ? 0 : min(max(draft * p.group - row, 0), 8);
+              if (!p.mask || (!p.mask_full && draft < 0)) {
+                const int lo = draft * p.group - row;
+                on = lo >= 32 ? 0u : on << max(lo, 0);
               } else {
-                const long long row0 = u.mask_row + (p.mask_full ? j : draft);
-                const int width = p.mask_full ? u.keys : u.L;
                 on = 0;
-                for (int tok = row / p.group, e = tok * p.group - row; e < 8 && tok < u.n; ++tok, e += p.group) {
-                  const long long bit = row0 + (long long)tok * width;
-                  if ((p.mask[bit >> 3] >> (bit & 7)) & 1)   // rows e .. e + group - 1, those among the 8
-                    on |= ((1u << min(e + p.group, 8)) - 1u) & (0xffu << max(e, 0));
+                if (mine) {
+                  const long long row0 = u.mask_row + (p.mask_full ? j : draft);
+                  const int width = p.mask_full ? u.keys : u.L;
+                  for (int tok = row / p.group, e = tok * p.group - row; e < 32 && tok < u.n; ++tok, e += p.group) {
+                    const long long bit = row0 + (long long)tok * width;
+                    if ((p.mask[bit >> 3] >> (bit & 7)) & 1) {   // rows e .. e + group - 1, those among the 32
+                      const int z = min(e + p.group, 32);
+                      on |= (z == 32 ? 0xffffffffu : (1u << z) - 1u) & (0xffffffffu << max(e, 0));
+                    }
+                  }
                 }
               }
             }
-            if (nr - k < 8) on &= (1u << (nr - k)) - 1u;
-            tmem_wait8(x);
-            add4(x, k, on & 1, on & 2, on & 4, on & 8);
-            add4(x + 4, k + 4, on & 16, on & 32, on & 64, on & 128);
-            k += 8;
+            if (nr - k < 32) on &= (1u << (nr - k)) - 1u;
+            tmem_wait32(x);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              add4(x + i, k + i, on & (1u << i), on & (2u << i), on & (4u << i), on & (8u << i));
+            k += 32;
           }
           tc_fence_before();
           acc0 = add_f32x2(acc0, acc1);
