@@ -6,13 +6,13 @@
 //
 // A unit (layer, request, KV head) belongs to one cluster of CTAs, one where
 // there are units enough.  Each CTA holds a slice of the unit's weights as the
-// upper halves of order-preserving integers in shared memory (two bytes a key:
-// two CTAs then hold 131,072 keys, where four bytes took eight CTAs, which did
-// not fit the GPU at a time).  The weight of the last survivor is found by a
+// order-preserving integers in shared memory, whole or, where they are too many,
+// their upper halves (two CTAs then hold 131,072 keys; with four bytes a key it
+// took eight, which did not fit the GPU at a time).  The weight of the last survivor is found by a
 // radix select from the top, by digits of 11, 5, 11 and 5 bits: the CTAs count
 // their slices, and each adds up all counts by reading the others' shared
-// memory.  The lower halves are read from the cache again, for the few keys that
-// share the upper one.  It ends as soon as all keys that share the digits found
+// memory.  Lower halves that are not held are read from the cache again, for the
+// few keys that share the upper one.  It ends as soon as all keys that share the digits found
 // survive.  (Up to 16,384 keys every CTA holds all weights and counts for itself:
 // a meeting of the cluster costs about a microsecond, and a select has up to
 // six.)  Then each CTA marks its slice, one bit a key, and every CTA gathers
@@ -45,7 +45,10 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1 << 11;
 constexpr int kRanks = 1024;  // most rows of a batch
-constexpr int kBatch = 8;   // rows' chunks in flight per thread
+// Rows' chunks in flight per thread.  One CTA an SM with sixteen of them took the
+// copies of 16 layers 458 us and of 131,072 keys 298 us, two CTAs with
+// eight, whose loop then spills, in 505 and 411.
+constexpr int kBatch = 16;
 constexpr int kAhead = 8;   // weights in flight per thread
 
 // Weights as integers in their order: -0 counts as 0, NaN above everything.
@@ -114,11 +117,12 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   return before + s - v;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const EvictParams p) {
-  extern __shared__ uint32_t dyn[];
+__global__ void __launch_bounds__(kThreads, 1) paged_kv_evict_kernel(const EvictParams p) {
+  extern __shared__ __align__(16) uint32_t dyn[];
   uint32_t* const bits = dyn;                                  // one bit a key: it survives
   int* const before = reinterpret_cast<int*>(dyn + p.words);   // survivors before each word
-  uint16_t* const slice = reinterpret_cast<uint16_t*>(dyn + 2 * p.words);   // this CTA's weights, upper halves
+  uint32_t* const slice32 = dyn + 2 * p.words;                   // this CTA's weights,
+  uint16_t* const slice = reinterpret_cast<uint16_t*>(slice32);  // or their upper halves
   // the counts; later the rows of three batches, from and to
   __shared__ __align__(16) int hist[3][kBins];
   static_assert(2 * kRanks <= kBins, "a batch's rows");
@@ -188,9 +192,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
   const int S = alone ? 1 : C, srank = alone ? 0 : rank;
   const int per = ((n + S - 1) / S + 31) & ~31, s0 = min(srank * per, n), s1 = min(s0 + per, n);
   const int m0 = max(s0, lo), m1 = min(s1, hi);
-  const bool held = per <= p.slice_cap;   // (else the weights are read again from the cache)
+  // held whole, by upper halves, or (neither) read from the cache again by every pass
+  const bool whole = per <= p.slice_cap / 2, held = !whole && per <= p.slice_cap;
   // the weight of key j as far as `mask` tells: the lower half is only looked at where the upper one is `fixed`'s
   auto weight_at = [&](int j, uint32_t fixed, uint32_t mask) -> uint32_t {
+    if (whole) return slice32[j - s0];
     if (held) {
       const uint32_t u = (uint32_t)slice[j - s0] << 16;
       if ((mask & 0xffffu) == 0 || ((u ^ fixed) >> 16) != 0) return u;
@@ -223,16 +229,37 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
             const int j = j0 + i * kThreads;
             if (j < m1) {
               const uint32_t u = order_of(x[i]);
-              if (held) slice[j - s0] = (uint16_t)(u >> 16);
+              if (whole) slice32[j - s0] = u;
+              else if (held) slice[j - s0] = (uint16_t)(u >> 16);
               atomicAdd(&h[u >> 21], 1);
             }
           }
         }
       } else {
-#pragma unroll 4
-        for (int j = m0 + tid; j < m1; j += kThreads) {
+        auto add = [&](int j) {
           const uint32_t u = weight_at(j, fixed, pass == 1 ? 0xffff0000u : 0xffffffffu);
           if ((u & mask) == fixed) atomicAdd(&h[(u >> shift) & (nb - 1)], 1);
+        };
+        if (whole) {
+#pragma unroll 4
+          for (int j = m0 + tid; j < m1; j += kThreads) {
+            const uint32_t u = slice32[j - s0];
+            if ((u & mask) == fixed) atomicAdd(&h[(u >> shift) & (nb - 1)], 1);
+          }
+        } else if (held) {
+          // eight upper halves at a time; few of them share the digits found
+          const uint32_t want16 = fixed >> 16, mask16 = mask >> 16;
+          for (int g = (m0 - s0) / 8 + tid; g * 8 < m1 - s0; g += kThreads) {
+            const uint4 v = reinterpret_cast<const uint4*>(slice)[g];
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int j = s0 + g * 8 + e;
+              if (((u[e / 2] >> (16 * (e & 1))) & mask16) == want16 && j >= m0 && j < m1) add(j);
+            }
+          }
+        } else {
+          for (int j = m0 + tid; j < m1; j += kThreads) add(j);
         }
       }
       if (S > 1) cluster_sync();
@@ -288,23 +315,62 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
   const int words = (n + 31) >> 5, v0 = s0 >> 5, nv = s1 > s0 ? (s1 + 31) / 32 - v0 : 0;
   const int per_warp = (nv + kWarps - 1) / kWarps;
   const int w0 = v0 + min(warp * per_warp, nv), w1 = v0 + min((warp + 1) * per_warp, nv);
-  int equal = 0;
-#pragma unroll 4
-  for (int k = w0; k < w1; ++k) {
-    const int j = k * 32 + lane;
-    const bool mid = j >= lo && j < hi && rest > 0;
-    const uint32_t u = mid ? weight_at(j, fixed, mask) & mask : 0u;
-    const bool more = j < lo || (j >= hi && j < n) || (mid && u > fixed), same = mid && u == fixed;
-    const uint32_t mm = __ballot_sync(0xffffffffu, more), ms = __ballot_sync(0xffffffffu, same);
-    if (lane == 0) {
-      bits[k] = same_all ? mm | ms : mm;
-      before[k] = (int)ms;   // (until the equals are counted)
+  if (held) {
+    // a word a thread: compared by upper halves, the few equal ones with a lower digit by the weight itself
+    const uint32_t want16 = fixed >> 16, mask16 = mask >> 16;
+    const bool lower = (mask & 0xffffu) != 0;
+    for (int k = v0 + tid; k < v0 + nv; k += kThreads) {
+      const int j0 = k * 32;
+      auto below = [&](int j) { return j <= j0 ? 0u : j >= j0 + 32 ? 0xffffffffu : (1u << (j - j0)) - 1u; };
+      const uint32_t mid = rest > 0 ? below(hi) & ~below(lo) : 0u;   // keys that compete
+      uint32_t gt = 0, eq = 0;
+      if (mid) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 v = reinterpret_cast<const uint4*>(slice + (j0 - s0))[q];
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t x = (u[e / 2] >> (16 * (e & 1))) & mask16;
+            gt |= (x > want16 ? 1u : 0u) << (q * 8 + e);
+            eq |= (x == want16 ? 1u : 0u) << (q * 8 + e);
+          }
+        }
+        gt &= mid;
+        eq &= mid;
+        if (lower)
+          for (uint32_t left = eq; left; left &= left - 1) {
+            const uint32_t one = left & (0u - left), u = order_of(w[row_of(j0 + __ffs(left) - 1)]) & mask;
+            if (u > fixed) gt |= one;
+            if (u != fixed) eq &= ~one;
+          }
+      }
+      const uint32_t mm = gt | (below(n) & (below(lo) | ~below(hi)));
+      bits[k] = same_all ? mm | eq : mm;
+      before[k] = (int)eq;   // (until the equals are counted)
     }
-    equal += __popc(ms);
+  } else {
+#pragma unroll 2
+    for (int k = w0; k < w1; ++k) {
+      const int j = k * 32 + lane;
+      const bool mid = j >= lo && j < hi && rest > 0;
+      const uint32_t u = mid ? (whole ? slice32[j - s0] : order_of(w[row_of(j)])) & mask : 0u;
+      const bool more = j < lo || (j >= hi && j < n) || (mid && u > fixed), same = mid && u == fixed;
+      const uint32_t mm = __ballot_sync(0xffffffffu, more), ms = __ballot_sync(0xffffffffu, same);
+      if (lane == 0) {
+        bits[k] = same_all ? mm | ms : mm;
+        before[k] = (int)ms;
+      }
+    }
   }
+  __syncthreads();
   int all;
   if (rest > 0 && !same_all) {
     // some of the equals go: those behind the first `ties` of all slices
+    int equal = 0;
+    for (int k = w0 + lane; k < w1; k += 32) equal += __popc((uint32_t)before[k]);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) equal += __shfl_xor_sync(0xffffffffu, equal, m);
     int run = block_scan(lane == 0 ? equal : 0, warp_sums, &all);
     run = __shfl_sync(0xffffffffu, run, 0);
     if (S > 1) {
@@ -380,48 +446,55 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
                      layer_row * stride;
   // The rows of ranks k0 .. k0 + kRanks - 1: the last word with before[word] <=
   // k, its bit, the pages.  A list is made while rows of the one before are
-  // under way.
+  // under way: its positions and page loads before their loads, its rows behind.
   const int rows = min(par * kBatch, kRanks), top = 1 << (31 - __clz(words));
-  auto resolve = [&](int k0, uint32_t* from, uint32_t* to) {
-    constexpr int kEach = kRanks / kThreads;
-    int a[kEach], page[kEach], page_to[kEach];
+  constexpr int kEach = kRanks / kThreads;
+  int pos[kEach], page[kEach], page_to[kEach];
+  auto find = [&](int k0) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) a[i] = 0;
+    for (int i = 0; i < kEach; ++i) pos[i] = 0;
 #pragma unroll 1
     for (int half = top; half > 0; half >>= 1) {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int mid = a[i] + half;
-        if (mid < words && before[mid] <= k0 + tid + i * kThreads) a[i] = mid;
+        const int mid = pos[i] + half;
+        if (mid < words && before[mid] <= k0 + tid + i * kThreads) pos[i] = mid;
       }
     }
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int k = min(k0 + tid + i * kThreads, keep - 1);
-      a[i] = min(a[i] * 32 + nth_bit(bits[a[i]], k - before[a[i]]), n - 1);
-      page[i] = p.kv_indices[pg0 + (a[i] >> p.log2_page)];
+      pos[i] = min(pos[i] * 32 + nth_bit(bits[pos[i]], k - before[pos[i]]), n - 1);
+      page[i] = p.kv_indices[pg0 + (pos[i] >> p.log2_page)];
       page_to[i] = p.kv_indices[pg0 + (k >> p.log2_page)];
     }
+  };
+  auto put = [&](int k0, uint32_t* list) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int r = tid + i * kThreads;
-      from[r] = row_at(page[i], a[i]);
-      to[r] = row_at(page_to[i], k0 + r);
+      list[r] = row_at(page[i], pos[i]);
+      list[kRanks + r] = row_at(page_to[i], k0 + r);
     }
   };
   int k0 = min(pick[2], keep);
   __syncthreads();
   int next = 0;   // list that is made next
   uint32_t* list = reinterpret_cast<uint32_t*>(hist[0]);
-  if (k0 < keep) resolve(k0, list, list + kRanks);
+  if (k0 < keep) {
+    find(k0);
+    put(k0, list);
+  }
   __syncthreads();
   for (; k0 < keep; k0 += kRanks) {
     next = next == 2 ? 0 : next + 1;
     uint32_t* const list_next = reinterpret_cast<uint32_t*>(hist[next]);
     const int m = min(kRanks, keep - k0);
+    const bool more = k0 + kRanks < keep;
+    if (more) find(k0 + kRanks);
     for (int r0 = 0; r0 < m; r0 += rows) {
       uint4 v[kBatch];
-      float x[kRanks / kThreads];
+      float x[kEach];
       const int end = min(m, r0 + rows);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -430,12 +503,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
       }
       if (rank == 0) {
 #pragma unroll
-        for (int i = 0; i < kRanks / kThreads; ++i) {
+        for (int i = 0; i < kEach; ++i) {
           const int r = r0 + tid + i * kThreads;
           if (r < end) x[i] = w[list[r]];
         }
       }
-      if (r0 == 0 && k0 + kRanks < keep) resolve(k0 + kRanks, list_next, list_next + kRanks);
+      if (r0 == 0 && more) put(k0 + kRanks, list_next);
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -444,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_evict_kernel(const Evict
       }
       if (rank == 0) {
 #pragma unroll
-        for (int i = 0; i < kRanks / kThreads; ++i) {
+        for (int i = 0; i < kEach; ++i) {
           const int r = r0 + tid + i * kThreads;
           if (r < end) w[list[kRanks + r]] = x[i];
         }

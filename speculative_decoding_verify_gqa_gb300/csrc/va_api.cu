@@ -1361,7 +1361,7 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
   p.sinks = sinks;
   p.recent = recent;
   p.max_kv_len = (int)max_kv_len;
-  p.words = (int)((max_kv_len + 31) / 32);
+  p.words = (int)((max_kv_len + 63) / 64 * 2);   // (what follows them starts on 16 bytes)
   // all three move in place: no pool may reach into another
   const unsigned __int128 rows = (unsigned __int128)num_layers * num_kv_heads * page_size * num_pages;
   if (overlap(k_cache, rows * p.k_chunks * 16, v_cache, rows * p.v_chunks * 16) ||
@@ -1372,7 +1372,7 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
     rc = query_sms(&num_sms);
     if (rc) return rc;
   }
-  // CTAs per unit: twice as many while all CTAs still run at a time and every
+  // CTAs per unit: twice as many while all CTAs still run at a time, one an SM, and every
   // one moves 64 bytes of a row -- or 32, where most of the GPU would stay idle.
   const int64_t all = units * num_kv_heads;
   const int chunks = p.k_chunks + p.v_chunks;
@@ -1380,13 +1380,14 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
     // (short requests are ranked whole by every CTA)
     const int64_t n = std::max(((max_kv_len + cluster - 1) / cluster + 31) / 32 * 32,
                                (std::min<int64_t>(max_kv_len, kEvictAlone) + 31) / 32 * 32);
-    // as many of them as there is room for: longer slices are read from the cache in every pass
-    return (int)std::min<int64_t>(n, ((int64_t)kEvictMaxSmem - (int64_t)evict_smem(p.words, 0)) / 64 * 32);
+    // room for whole weights, four bytes each, of up to 16,384 keys; for upper halves, two bytes, of as many as
+    // shared memory takes (longer slices are read from the cache in every pass)
+    const int64_t room = ((int64_t)kEvictMaxSmem - (int64_t)evict_smem(p.words, 0)) / 64 * 32;
+    return (int)std::min(n <= kEvictAlone ? 2 * n : n, room);
   };
   p.cluster = 1;
   for (int c = 2; c <= kMaxCluster; c *= 2) {
-    const int64_t resident = (int64_t)num_sms * std::min<int64_t>(2, 228 * 1024 / (evict_smem(p.words, slice(c)) + kEvictStatic));
-    if (all * c > resident || chunks / c < (all * c * 2 <= num_sms ? 2 : 4)) break;
+    if (all * c > num_sms || chunks / c < (all * c * 2 <= num_sms ? 2 : 4)) break;
     p.cluster = c;
   }
   p.slice_cap = slice(p.cluster);
