@@ -49,6 +49,11 @@ constexpr int kTokens = 8;    // tokens whose slots and angles are found at a ti
 // of two tokens took a prompt's rows in 83.5 us, three of three in 89.2
 constexpr int kResident = 4, kStages = 2;
 constexpr int kMaxStages = 45 * 1024;
+// How a CTA gets its rows: one token's into registers, all that it likes while
+// there is a CTA an SM at most (1 to 8 tokens of 64 + 16 heads 3.9 us, 4.6 with
+// the registers of the next), or so that three CTAs share an SM (334 tokens 7.5
+// us, 7.9 with two); a run of tokens' through shared memory.
+enum { kFew, kDirect, kStaged };
 
 __device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -126,9 +131,10 @@ __device__ __forceinline__ void head(uint4 raw, const Coef& c, bool norm, bool r
   }
 }
 
-template <int D, bool PAIRS, bool STAGED>
-__global__ void __launch_bounds__(kThreads, STAGED ? kResident : 3) paged_qkv_append_kernel(const QkvParams p) {
+template <int D, bool PAIRS, int MODE>
+__global__ void __launch_bounds__(kThreads, MODE == kStaged ? kResident : MODE == kDirect ? 3 : 1) paged_qkv_append_kernel(const QkvParams p) {
   constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
+  constexpr bool STAGED = MODE == kStaged;
   __shared__ __align__(16) float cs[kTokens][D], sn[kTokens][D];   // by column: cos (1 where nothing turns), -+ sin (0)
   __shared__ __align__(16) float wt[2][D];
   __shared__ long long first_row[kTokens];   // cache row of the token's KV head 0, or -1
@@ -345,12 +351,13 @@ __global__ void __launch_bounds__(kThreads, STAGED ? kResident : 3) paged_qkv_ap
 }
 
 template <int D, bool PAIRS>
-cudaError_t launch(const QkvParams& p, size_t stages, cudaStream_t stream) {
+cudaError_t launch(const QkvParams& p, size_t stages, int num_sms, cudaStream_t stream) {
   void* args[] = {const_cast<QkvParams*>(&p)};
   const dim3 grid((unsigned)((p.total_new + p.per_cta - 1) / p.per_cta));
-  const void* k = reinterpret_cast<const void*>(paged_qkv_append_kernel<D, PAIRS, false>);
+  const void* k = p.total_new <= num_sms ? reinterpret_cast<const void*>(paged_qkv_append_kernel<D, PAIRS, kFew>)
+                                         : reinterpret_cast<const void*>(paged_qkv_append_kernel<D, PAIRS, kDirect>);
   if (stages) {
-    k = reinterpret_cast<const void*>(paged_qkv_append_kernel<D, PAIRS, true>);
+    k = reinterpret_cast<const void*>(paged_qkv_append_kernel<D, PAIRS, kStaged>);
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStages);
     if (e != cudaSuccess) return e;
   }
@@ -372,8 +379,8 @@ cudaError_t launch_qkv_append(const QkvParams& params, int head_dim, int num_sms
     p.per_cta = 1;
     stages = 0;
   }
-  if (head_dim == 64) return p.interleaved ? launch<64, true>(p, stages, stream) : launch<64, false>(p, stages, stream);
-  return p.interleaved ? launch<128, true>(p, stages, stream) : launch<128, false>(p, stages, stream);
+  if (head_dim == 64) return p.interleaved ? launch<64, true>(p, stages, num_sms, stream) : launch<64, false>(p, stages, num_sms, stream);
+  return p.interleaved ? launch<128, true>(p, stages, num_sms, stream) : launch<128, false>(p, stages, num_sms, stream);
 }
 
 }  // namespace va
