@@ -1303,10 +1303,15 @@ int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* k
     const cuuint64_t dims[4] = {(cuuint64_t)head_dim, P, H, (cuuint64_t)num_pages};
     const cuuint64_t strides[3] = {p.nhd ? H * row : row, p.nhd ? row : P * row, H * P * row};
     const cuuint32_t boxes[4] = {fp8 ? (cuuint32_t)head_dim : 64u, (cuuint32_t)p.box, 1, 1}, step[4] = {1, 1, 1, 1};
+    // what a fetch brings into L2: no more than a head's row where the next row is another head's (NHD rows of 128
+    // bytes, 32,768 keys: 256 bytes brought 418 MB where 290 are asked for)
+    const CUtensorMapL2promotion fetch = !p.nhd || row >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                         : row >= 128         ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                              : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
     if (enc(&kmap, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(k_cache),
             dims, strides, boxes, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, fetch, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
+        CUDA_SUCCESS)
       return VA_ERR_CUDA;
   }
   cudaError_t e = launch_key_weights(p, kmap, head_dim, kv_dtype == VA_DTYPE_FP8_E4M3, num_sms,
