@@ -1177,6 +1177,8 @@ int paged_qkv_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
     return VA_ERR_INVALID_ARGUMENT;
   if (overlap(q_out, out_bytes, k, (n1 * k_stride + k_row) * 2) || overlap(q_out, out_bytes, v, (n1 * v_stride + v_row) * 2))
     return VA_ERR_INVALID_ARGUMENT;
+  const uintptr_t ws = o.weight_dtype == VA_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(o.q_weight) % ws || reinterpret_cast<uintptr_t>(o.k_weight) % ws) return VA_ERR_INVALID_ARGUMENT;
   QkvParams p;
   memset(&p, 0, sizeof(p));
   p.q = q;
@@ -1259,7 +1261,9 @@ int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* k
   if (!k_cache || !kv_indptr || !kv_indices || !last_page_len || !qo_indptr || !key_weights || num_pages <= 0 ||
       (total_qo > 0 && (!q || !lse)))
     return VA_ERR_INVALID_ARGUMENT;
-  if ((q && !aligned16(q)) || !aligned16(k_cache)) return VA_ERR_INVALID_ARGUMENT;
+  if ((q && !aligned16(q)) || !aligned16(k_cache) || reinterpret_cast<uintptr_t>(key_weights) % 4 ||
+      reinterpret_cast<uintptr_t>(lse) % 4)
+    return VA_ERR_INVALID_ARGUMENT;
   if (num_sms <= 0) {
     rc = query_sms(&num_sms);
     if (rc) return rc;
@@ -1367,6 +1371,8 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
   p.recent = recent;
   p.max_kv_len = (int)max_kv_len;
   p.words = (int)((max_kv_len + 63) / 64 * 2);   // (what follows them starts on 16 bytes)
+  // the kernel counts a layer's rows in 32 bits
+  if ((unsigned __int128)num_kv_heads * page_size * num_pages > 0xffffffffu) return VA_ERR_UNSUPPORTED;
   // all three move in place: no pool may reach into another
   const unsigned __int128 rows = (unsigned __int128)num_layers * num_kv_heads * page_size * num_pages;
   if (overlap(k_cache, rows * p.k_chunks * 16, v_cache, rows * p.v_chunks * 16) ||

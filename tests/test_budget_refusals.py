@@ -48,6 +48,7 @@ def _qkv(va, options=None, **kw):
     ({}, dict(qs=248), INVALID), ({}, dict(ks=260), INVALID), ({}, dict(vs=128), INVALID),
     ({}, dict(q=A + 8), INVALID), ({}, dict(vc=6 * A + 4), INVALID), ({}, dict(kc=0), INVALID), ({}, dict(pages=0), INVALID),
     ({}, dict(out=A + 512), INVALID), ({}, dict(out=2 * A), INVALID), ({}, dict(out=3 * A + 16), INVALID),
+    (dict(q_weight=A + 1), {}, INVALID), (dict(k_weight=A + 2, weight_dtype=2), {}, INVALID),
     ({}, dict(out=A, qs=512), INVALID), ({}, dict(total=1 << 31), UNSUPPORTED), ({}, dict(qs=1 << 40), UNSUPPORTED),
 ])
 def test_qkv_append_refuses(va, options, kw, status):
@@ -77,7 +78,7 @@ def _weights(va, **kw):
     (dict(mask=64), INVALID), (dict(mi=64), INVALID), (dict(acc=64), INVALID), (dict(path=64), INVALID),
     (dict(mask=64, mi=64, acc=64, path=64), INVALID), (dict(ks=0.0), INVALID), (dict(ks=float("inf")), INVALID),
     (dict(scale=1e38, ks=1e38), INVALID), (dict(decay=-0.5), INVALID), (dict(decay=float("nan")), INVALID),
-    (dict(q=0), INVALID), (dict(lse=0), INVALID), (dict(w=0), INVALID), (dict(k=A + 8), INVALID), (dict(q=A + 2), INVALID),
+    (dict(q=0), INVALID), (dict(lse=0), INVALID), (dict(w=0), INVALID), (dict(lse=66), INVALID), (dict(w=A + 2), INVALID), (dict(k=A + 8), INVALID), (dict(q=A + 2), INVALID),
     (dict(pages=0), INVALID), (dict(total=1 << 31), UNSUPPORTED), (dict(batch=65536), UNSUPPORTED), (dict(batch=0), 0),
 ])
 def test_key_weights_refuses(va, kw, status):
@@ -98,7 +99,7 @@ def _evict(va, **kw):
     (dict(most=(1 << 19) + 1), UNSUPPORTED), (dict(batch=1 << 28, layers=64), UNSUPPORTED), (dict(w=0), INVALID),
     (dict(keep=0), INVALID), (dict(ids=0), INVALID), (dict(k=16 * A + 8), INVALID), (dict(w=A + 2), INVALID),
     (dict(pages=0), INVALID), (dict(v=16 * A + 16), INVALID), (dict(w=16 * A + 64), INVALID), (dict(w=32 * A), INVALID),
-    (dict(batch=0), 0),
+    (dict(pages=1 << 27, page=16), UNSUPPORTED), (dict(batch=0), 0),
 ])
 def test_evict_refuses(va, kw, status):
     assert _evict(va, **kw) == status
