@@ -16,19 +16,27 @@
 // is fixed.  K is read once and V not at all: HBM bounds the step of a serving
 // batch, the tensor cores and the SFU's 2^x (one for each pair) a prompt's.
 //
+// On one GB300: 64 chains of up to 8 tokens behind up to 8,192 keys (64/8 heads,
+// bf16) 118 us, 5.1 TB/s, of which 105 remain with products and 2^x taken out;
+// 8 trees of 64 nodes behind 32,768 fp8 keys (32/8 heads) 200 us, 688 TFLOP/s;
+// 10 prompts of 1,024 tokens (64/8 heads) 131 us, 655 TFLOP/s of visible pairs.
+// The hand-offs between the roles are what the latter two wait for: an mbarrier
+// operation takes a warp some 150 cycles, and a chunk has four to six.
+//
 // A unit is one or two tiles of 128 keys of one (request, KV head).  One CTA per
 // SM, its warps in roles that run through the same units:
-//  * one warp walks the schedule: it looks the pages of a unit's keys up and
-//    posts the unit -- its geometry, its places in all rings, its cache rows --
-//    in a queue in shared memory, so that the others' loops stay short;
-//  * 4 loader warps gather K rows by 16-byte asynchronous copies into the
-//    128-byte-swizzled operand layout (any page size and layout; a tile's rows
-//    need not be neighbours), and the query rows of 128-row chunks the same
-//    way.  The copies arrive at an mbarrier by themselves.  e4m3 rows are widened to f16 between a raw
-//    buffer and the operand (exact), and bf16 queries with them, as the
-//    attention kernels do;
+//  * one warp walks the schedule: it posts a unit -- its geometry, its places in
+//    all rings, the pages of its keys, which arrive by asynchronous copies -- in
+//    a queue in shared memory, so that the others' loops stay short;
+//  * 4 loader warps bring the tiles of K into the 128-byte-swizzled operand
+//    layout: by TMA, a page or 32 slots of one a box, or for pages of fewer than
+//    8 slots and tiles with keys of an accepted path row by row, in 16-byte
+//    asynchronous copies; and the query rows of 128-row chunks by such copies.
+//    e4m3 rows are widened to f16 between a raw buffer and the operand (exact),
+//    and bf16 queries with them, as the attention kernels do;
 //  * one thread issues tcgen05.mma: for each chunk of rows and tile of keys 4 or
-//    8 steps of K = 16 into one of two buffers of the tile;
+//    8 steps of K = 16 into one of two buffers of the tile, and passes a chunk's
+//    products on together;
 //  * 4 warps per tile take 2^(s c - lse log2 e) of their lane's columns and add.
 // Chunks of a (request, head) of up to 256 rows stay in shared memory from unit
 // to unit.  Longer ones (prompts) are streamed, from the first chunk that sees
@@ -60,6 +68,7 @@ constexpr int kList = 512;    // units (of all heads) that are sorted
 constexpr int kResident = 2;  // chunks that stay in shared memory
 constexpr int kFlight = 3;    // e4m3: loads under way per loader thread
 constexpr int kQueue = 6;     // units posted ahead
+constexpr int kDrain = 1024;  // tries for a load under way when the CTA has given up
 
 template <int D, bool FP8>
 struct Cfg {
@@ -418,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_fence_init();
       sched.kt = kt;
       sched.sorted = sorted;
-      sched.count = sorted ? total : hi - lo;
+      // (as many as are listed, should the tables change during the call)
+      sched.count = sorted ? min(total, (long long)min(sched.entries, kList) * p.h_kv) : hi - lo;
     }
   }
   __syncthreads();
@@ -630,8 +640,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- loads ----------------
     constexpr int KCH = (FP8 ? D : 2 * D) / 16, QCH = 2 * D / 16;  // 16-byte chunks of a row
     const int lw = warp - kLoadWarp, own = lw * 32 + lane;          // this thread's row of a chunk
-    int p0 = 0, p1 = 0, p2 = 0, np = 0;  // e4m3: loads under way, the oldest first: slot, and 8: a chunk of q
-    Ring rr(kFlight), rf(kFlight);       // e4m3: raw buffers of the next load, of the next one widened
+    int p0 = 0, p1 = 0, p2 = 0, np = 0;  // e4m3: loads under way, the oldest first: 0: K, 8 and its slot: a chunk of q
+    Ring rr(FP8 ? kFlight : nk);         // the next load's buffer: raw, or the tile's slot
+    Ring rf(kFlight);                    // e4m3: the raw buffer that is widened next
     Ring kf(nk);                         // the K slot that is widened into next
     // e4m3: the oldest load has landed: widen it, and pass it on
     auto finish = [&]() {
@@ -716,13 +727,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ur.step();
       if (u.nt > 0 && u.chunks > 0) {
         for (int t = 0; t < u.nt && live; ++t) {
-          const int slot = t == 0 ? u.k_slot : u.k_slot1, round = t == 0 ? u.k_round : u.k_round1;
           room();
           if constexpr (!FP8)
-            if (live && round > 0) wait_free(bar(B_FREE + slot), (round - 1) & 1);
+            if (live && rr.round > 0) wait_free(bar(B_FREE + rr.slot), (rr.round - 1) & 1);
           if (!live) break;
-          const uint32_t base = sbase + (FP8 ? C::OFF_RAW + rr.slot * C::RAW : slot * C::OP);
-          const uint32_t full = bar(FP8 ? B_RAW + rr.slot : B_FULL + slot);
+          const uint32_t base = sbase + (FP8 ? C::OFF_RAW + rr.slot * C::RAW : rr.slot * C::OP);
+          const uint32_t full = bar((FP8 ? B_RAW : B_FULL) + rr.slot);
           const int tile0 = u.key0 + t * kTile;
           const int* const pages = unit_pages + done * 2 * kTile + t * kTile + lw * 32;
           const bool moved = p.accept_len && tile0 + kTile > u.pre;
@@ -758,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             arrive_behind(full);
           }
-          if constexpr (FP8) put(slot);
+          if constexpr (FP8) put(0);
           rr.step();
         }
       }
@@ -802,6 +812,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (FP8)
       while (np > 0 && live) finish();
     cp_async_wait_all();
+    if (!live)   // given up: nothing may still be on its way into the CTA's shared memory
+      for (int i = 0; i < rr.n; ++i) {   // (every buffer's last load)
+        const int round = i < rr.slot ? rr.round : rr.round - 1;
+        for (int k = 0; k < kDrain && round >= 0 && !mbar_try_wait(bar((FP8 ? B_RAW : B_FULL) + i), round & 1); ++k) {}
+      }
   } else if (lane == 0) {
     // ---------------- products: one thread ----------------
     const uint64_t desc0 = smem_desc_sw128(0, 16, 1024);

@@ -22,7 +22,8 @@
 // into shared memory by bulk copies, a token ahead of the one in work: rows
 // loaded into registers one token ahead kept too little under way (10,240 tokens
 // of 64 + 16 heads: 38 % of the DRAM's cycles, warps waiting for loads half of
-// their time).
+// their time).  On one GB300 these 10,240 tokens take 83.5 us (5.0 TB/s), 288
+// tokens in 64 chains into an fp8 cache 8.6 us, one token (32 + 16 heads) 3.2 us.
 //
 // Angles: the frequency is kept in turns as a 64-bit binary fraction, so
 // position * frequency modulo one turn is one integer product, exact for any
@@ -49,6 +50,7 @@ constexpr int kTokens = 8;    // tokens whose slots and angles are found at a ti
 // of two tokens took a prompt's rows in 83.5 us, three of three in 89.2
 constexpr int kResident = 4, kStages = 2;
 constexpr int kMaxStages = 45 * 1024;
+constexpr int kDrain = 1024;  // tries for a copy under way when the CTA gives up
 // How a CTA gets its rows: one token's into registers, all that it likes while
 // there is a CTA an SM at most (1 to 8 tokens of 64 + 16 heads 3.9 us, 4.6 with
 // the registers of the next), or so that three CTAs share an SM (334 tokens 7.5
@@ -337,7 +339,14 @@ __global__ void __launch_bounds__(kThreads, MODE == kStaged ? kResident : MODE =
       if constexpr (STAGED) {
         // all have read the token's rows: its place is another's
         if (!__syncthreads_and(ok)) {
-          if (tid == 0 && p.status) atomicOr(p.status, VA_DEV_TIMEOUT);
+          if (tid == 0) {
+            // nothing may still be on its way into the CTA's shared memory
+            for (int s = 0; s < kStages && i + s < i1; ++s) {
+              const int at_stage = (stage + s) % kStages, at_round = round + (stage + s) / kStages;
+              for (int n = 0; n < kDrain && !mbar_try_wait(smem_u32(full + at_stage), at_round & 1); ++n) {}
+            }
+            if (p.status) atomicOr(p.status, VA_DEV_TIMEOUT);
+          }
           return;
         }
         if (tid == 0 && i + kStages < i1) bring(i + kStages, stage);
