@@ -188,3 +188,21 @@ def test_far_rows(va):
         assert x[2, at, 0, :20, 0].float().tolist() == [float(sign * r) for r in rows]
         assert x[2, at, 1, 20:, 5].float().tolist() == [float(sign * r) for r in range(20, P)]
         assert int((x[1] != 0).any()) == 0
+
+
+def test_padded_batch(va):
+    """Requests of no pages behind the last one: their new length is 0, whatever they may keep."""
+    c = Case(90, [900, 40, 0, 0, 0], [300, 17, 0, 5, 1 << 30], sinks=2, recent=9, layers=2)
+    c.run(va)
+    c.check()
+
+
+def test_two_calls_at_once(va):
+    cases = [Case(91, [3000, 1200], [1500, 60], h=4, d=128, layers=3), Case(92, [20001], [5000], h=1, values="few", recent=5)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for c, s in zip(cases, streams):
+        with torch.cuda.stream(s):
+            c.run(va)
+    for c in cases:
+        c.check()

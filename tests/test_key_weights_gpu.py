@@ -282,3 +282,61 @@ def test_far_rows(va):
     va.verify_attn_key_weights(q, k, i([0, 1]), i([pages - 1]), i([P]), i([0, 1]), lse.float()[None], w)
     assert torch.allclose(w[pages - 1].double(), torch.exp(s - lse[:, None]), rtol=1e-4)
     assert int((w != 0).sum()) == 2 * P
+
+
+# Calls whose CTAs have several units each: with the rows held, streamed in order
+# of cost (some request has more than 256 rows), and streamed as they come (more
+# than 512 units of a head besides).
+MANY = [
+    dict(lens=[8, 3, 1, 5] * 10, pre=list(range(300, 3500, 80)), hq=16, h=4),
+    dict(lens=[8, 3, 1, 5] * 10, pre=list(range(300, 3500, 80)), hq=16, h=4, fp8=True, nhd=True, page=64, mask="qlen-holes"),
+    dict(lens=[60, 2, 33] * 8, pre=[1500, 17, 900] * 8, hq=12, h=6, d=64, path=True, decay=0.9),
+    dict(lens=[50, 2, 33] * 8, pre=[1500, 17, 900] * 8, hq=30, h=6, d=64, fp8=True, page=4, path=True),
+    dict(lens=[300, 40, 1, 0], pre=[2500, 1000, 3000, 100], hq=32, h=8),
+    dict(lens=[300, 40, 1, 0], pre=[2500, 1000, 3000, 100], hq=32, h=8, fp8=True, nhd=True, page=64),
+    dict(lens=[0, 129, 260, 7], pre=[90, 2000, 1001, 2222], hq=40, h=8, d=64, mask="qlen-holes", page=4),
+    dict(lens=[129, 260, 7], pre=[2000, 1001, 2222], hq=40, h=8, d=64, mask="full-holes", fp8=True, page=32),
+    dict(lens=[200, 260, 7], pre=[2000, 1001, 2222], hq=40, h=8, path=True, decay=0.5),
+    dict(lens=[200, 260, 7], pre=[2000, 1001, 2222], hq=40, h=8, path=True, fp8=True, d=64, page=128),
+    dict(lens=[700, 900], pre=[0, 128], hq=64, h=16, nhd=True),
+    dict(lens=[2] * 300 + [200] + [2] * 250, pre=[9] * 551, hq=4, h=2, d=64),
+    dict(lens=[2] * 300 + [200] + [2] * 250, pre=[9] * 551, hq=4, h=2, fp8=True, page=8, path=True),
+]
+
+
+@pytest.mark.parametrize("n", range(len(MANY)))
+def test_many_units(va, n):
+    c = Case(100 + n, **MANY[n])
+    c.run(va)
+    torch.cuda.synchronize()
+    assert int(c.status) == 0
+    c.check()
+
+
+def test_padded_batch(va):
+    """Requests of no pages and no tokens behind the last one, and query rows behind the last request's."""
+    c = Case(120, [5, 3, 0, 0, 0], [200, 31, 0, 0, 0])
+    o = int(c.indptr[-1])
+    c.q = torch.cat([c.q, torch.full_like(c.q[:4], float("nan"))])
+    c.lse = torch.cat([c.lse, torch.full_like(c.lse[:4], float("nan"))])
+    assert c.q.shape[0] == o + 4
+    c.run(va)
+    torch.cuda.synchronize()
+    assert int(c.status) == 0
+    c.q, c.lse = c.q[:o], c.lse[:o]
+    c.check()
+
+
+def test_two_calls_at_once(va):
+    cases = [Case(121, **MANY[4]), Case(122, **MANY[1])]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                c.w.copy_(torch.from_numpy(c.w0))
+                c.run(va)
+    torch.cuda.synchronize()
+    for c in cases:
+        assert int(c.status) == 0
+        c.check()

@@ -255,3 +255,26 @@ def test_far_slots(va):
     va.paged_qkv_append(q, kn, vn, i([0, 1]), i([0, 1]), i([pages - 1]), i([16]), k, v)
     assert torch.equal(k[pages - 1, :, 15], kn[0]) and torch.equal(v[pages - 1, :, 15], vn[0])
     assert int((k != 0).any(-1).sum()) == 2
+
+
+@pytest.mark.parametrize("kw", [dict(lens=[3, 5, 0, 0, 0], pre=[40, 2, 0, 0, 0], pad=6),
+                                dict(lens=[500, 300] + [0] * 140, pre=[40, 2] + [0] * 140, pad=30, fp8=True)])
+def test_padded_batch(va, kw):
+    """Requests of no pages and no tokens behind the last one, and rows behind the last token."""
+    c = Case(40, **kw)
+    c.q[c.used:] = float("nan")
+    c.run(va)
+    c.check()
+
+
+def test_two_calls_at_once(va):
+    cases = [Case(41, [700, 411], [5, 0], fp8=True), Case(42, [4, 1, 9], [5, 60, 0], hq=32, h=8)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                c.run(va)
+    torch.cuda.synchronize()
+    for c in cases:
+        c.check()
