@@ -17,11 +17,15 @@
 // batch, the tensor cores and the SFU's 2^x (one for each pair) a prompt's.
 //
 // On one GB300: 64 chains of up to 8 tokens behind up to 8,192 keys (64/8 heads,
-// bf16) 118 us, 5.1 TB/s, of which 105 remain with products and 2^x taken out;
-// 8 trees of 64 nodes behind 32,768 fp8 keys (32/8 heads) 200 us, 688 TFLOP/s;
-// 10 prompts of 1,024 tokens (64/8 heads) 131 us, 655 TFLOP/s of visible pairs.
-// The hand-offs between the roles are what the latter two wait for: an mbarrier
-// operation takes a warp some 150 cycles, and a chunk has four to six.
+// bf16) 106 us, 5.7 TB/s;
+// 8 trees of 64 nodes behind 32,768 fp8 keys (32/8 heads) 190 us, 725 TFLOP/s;
+// 10 prompts of 1,024 tokens (64/8 heads) 123 us, 697 TFLOP/s of visible pairs.
+// The latter two wait for the warps that add: 32 rows take them some 500 cycles
+// where the SFU needs 256 for the two of a scheduler, and a chunk's hand-offs --
+// an mbarrier operation takes some 150 cycles -- come on top.  All roles share
+// the instruction caches (87 % of requests hit), so the loops are kept short: the
+// look at a mask out of line took the chains from 119 to 116 us, rows that all
+// see the keys in a loop of their own the prompts from 131 to 124.
 //
 // A unit is one or two tiles of 128 keys of one (request, KV head).  One CTA per
 // SM, its warps in roles that run through the same units:
@@ -42,8 +46,8 @@
 // to unit.  Longer ones (prompts) are streamed, from the first chunk that sees
 // the unit's keys on.
 //
-// Units are dealt in runs of neighbours where rows are few: all cost the same
-// bytes.  Where a request has more than 256 rows they are sorted by their number
+// Units are dealt in runs of neighbours where rows are few: they cost the same
+// bytes, and the beginnings of heads are counted with them.  Where a request has more than 256 rows they are sorted by their number
 // of chunks and dealt back and forth over the CTAs, the long ones first.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -129,7 +133,7 @@ __device__ __forceinline__ Request load_request(const KeyWeightParams& p, int b)
 
 // What the roles share of the schedule.
 struct Sched {
-  unsigned long long tiles1, tiles2;  // tiles of 128 keys, units of 256, of all heads
+  unsigned tiles1, tiles2;            // tiles of 128 keys, units of 256, of all heads, counted as far as it matters
   int most_rows, entries;             // rows of the longest request, units of one head
   int kt;                             // tiles of a unit
   int sorted;                         // units are dealt from the sorted list
@@ -303,6 +307,19 @@ __device__ __forceinline__ void mma_tile(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
+// which of 32 query rows from `row` on see the key by the mask, bit row0 + token * width (out of line: rarely called)
+__device__ __noinline__ uint32_t mask_bits(const uint8_t* mask, long long row0, int width, int row, int group, int n) {
+  uint32_t on = 0;
+  for (int tok = row / group, e = tok * group - row; e < 32 && tok < n; ++tok, e += group) {
+    const long long bit = row0 + (long long)tok * width;
+    if ((mask[bit >> 3] >> (bit & 7)) & 1) {   // rows e .. e + group - 1, those among the 32
+      const int z = min(e + group, 32);
+      on |= (z == 32 ? 0xffffffffu : (1u << z) - 1u) & (0xffffffffu << max(e, 0));
+    }
+  }
+  return on;
+}
+
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
     verify_attn_key_weights_kernel(const KeyWeightParams p, const __grid_constant__ CUtensorMap kmap) {
@@ -347,15 +364,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rq.bad && blockIdx.x == 0 && p.status) atomicOr(p.status, VA_DEV_BAD_TABLE);
     if (rq.keys == 0) continue;
     const int one = (rq.keys + kTile - 1) / kTile, two = (one + 1) / 2;
-    atomicAdd(&sched.tiles1, (unsigned long long)one * p.h_kv);
-    atomicAdd(&sched.tiles2, (unsigned long long)two * p.h_kv);
+    // (65,535 requests at most: 32 bits hold the sums)
+    atomicAdd(&sched.tiles1, (unsigned)min((long long)one * p.h_kv, 65536ll));
+    atomicAdd(&sched.tiles2, (unsigned)min((long long)two * p.h_kv, 65536ll));
     atomicMax(&sched.most_rows, rq.rows);
     atomicAdd(&sched.entries, min(two, kList + 1));
   }
   __syncthreads();
-  const int kt = sched.tiles1 <= gridDim.x ? 1 : 2;
+  const unsigned most = min(gridDim.x, 65535u);
+  const int kt = sched.tiles1 <= most ? 1 : 2;
   const bool sorted = kt == 2 && sched.most_rows > kResident * kTile && sched.entries <= kList;
-  const long long total = (long long)(kt == 1 ? sched.tiles1 : sched.tiles2);
   if (sorted) {
     // rank = units with more chunks, or as many and listed before
     int* const cost = reinterpret_cast<int*>(smem);
@@ -389,31 +407,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (warp == 0) {
-    const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
-    long long run = 0;
-    if (!sorted && lo < hi)
-      for (int b0 = 0; b0 < p.batch; b0 += 32) {
-        long long units = 0;
-        if (b0 + lane < p.batch) {
-          const int keys = load_request(p, b0 + lane).keys;
-          units = (long long)((keys + kTile * kt - 1) / (kTile * kt)) * p.h_kv;
-        }
-        long long sum = units;
+    long long first = -1, end = 0;   // this CTA's units
+    const unsigned all = kt == 1 ? sched.tiles1 : sched.tiles2;
+    if (!sorted && all <= most) {
+      // one at most
+      const int at = blockIdx.x;
+      end = at + 1;
+      for (int b0 = 0, run = 0; b0 < p.batch && at < (int)all; b0 += 32) {
+        int units = 0;
+        if (b0 + lane < p.batch) units = (load_request(p, b0 + lane).keys + kTile * kt - 1) / (kTile * kt) * p.h_kv;
+        int sum = units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long t = __shfl_up_sync(0xffffffffu, sum, o);
+          const int t = __shfl_up_sync(0xffffffffu, sum, o);
           if (lane >= o) sum += t;
         }
-        const uint32_t hit = __ballot_sync(0xffffffffu, run + sum > lo);
+        const uint32_t hit = __ballot_sync(0xffffffffu, run + sum > at);
         if (hit) {
           if (lane == __ffs(hit) - 1) {
             sched.b0 = b0 + lane;
-            sched.off = lo - (run + sum - units);
+            sched.off = at - (run + sum - units);
           }
+          first = at;
           break;
         }
         run += __shfl_sync(0xffffffffu, sum, 31);
       }
+    } else if (!sorted) {
+      // units, and their cost by halves of a unit: two for a unit, and one for each chunk that is loaded when a
+      // request's head begins (64 chains, 2 to 17 beginnings a CTA: 115 -> 106 us)
+      long long total = 0, cost = 0;
+      for (int b = lane; b < p.batch; b += 32) {
+        const Request rq = load_request(p, b);
+        const long long units = (rq.keys + 2 * kTile - 1) / (2 * kTile);
+        total += units * p.h_kv;
+        cost += (2 * units + (units ? min(rq.chunks, kResident) : 0)) * p.h_kv;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        cost += __shfl_xor_sync(0xffffffffu, cost, o);
+      }
+      // Runs of equal cost.  Unit i of a head lies at half `loads` + 2 i + 1 of its cost and belongs to the run that
+      // this half lies in.
+      const long long lo = cost * blockIdx.x / gridDim.x, hi = cost * (blockIdx.x + 1) / gridDim.x;
+      long long run = 0, before = 0;   // cost and units before the 32 requests
+      end = total;
+      if (lo < hi)
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+          long long units = 0, each = 0, loads = 0;   // of a head; its cost
+          if (b0 + lane < p.batch) {
+            const Request rq = load_request(p, b0 + lane);
+            units = (rq.keys + 2 * kTile - 1) / (2 * kTile);
+            loads = units == 0 ? 0 : min(rq.chunks, kResident);
+            each = 2 * units + loads;
+          }
+          long long sum = each * p.h_kv, tiles = units * p.h_kv;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, sum, o), v = __shfl_up_sync(0xffffffffu, tiles, o);
+            if (lane >= o) {
+              sum += t;
+              tiles += v;
+            }
+          }
+          // units before half x of the cost, of this lane's request
+          auto units_before = [&](long long x) {
+            const long long at = x - (run + sum - each * p.h_kv), h = at / each;
+            return h * units + max(0ll, at - h * each - loads) / 2;
+          };
+          const uint32_t hit_lo = first < 0 ? __ballot_sync(0xffffffffu, run + sum > lo) : 0u;
+          if (hit_lo) {
+            const int from = __ffs(hit_lo) - 1;
+            if (lane == from) {
+              sched.b0 = b0 + lane;
+              sched.off = units_before(lo);
+              first = before + tiles - units * p.h_kv + sched.off;
+            }
+            first = __shfl_sync(0xffffffffu, first, from);
+          }
+          const uint32_t hit_hi = __ballot_sync(0xffffffffu, run + sum > hi);
+          if (hit_hi) {
+            const int from = __ffs(hit_hi) - 1;
+            if (lane == from) end = before + tiles - units * p.h_kv + units_before(hi);
+            end = __shfl_sync(0xffffffffu, end, from);
+            break;
+          }
+          run += __shfl_sync(0xffffffffu, sum, 31);
+          before += __shfl_sync(0xffffffffu, tiles, 31);
+        }
+    }
     if (lane == 0) {
       // Full: each loader warp's own arrival, for what it has stored (a chunk's
       // lse, widened rows) and behind the asynchronous ones of its copies.
@@ -427,8 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_fence_init();
       sched.kt = kt;
       sched.sorted = sorted;
-      // (as many as are listed, should the tables change during the call)
-      sched.count = sorted ? min(total, (long long)min(sched.entries, kList) * p.h_kv) : hi - lo;
+      sched.count = sorted ? (long long)min(sched.entries, kList) * p.h_kv : first < 0 ? 0 : end - first;
     }
   }
   __syncthreads();
@@ -577,16 +659,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc0 = add_f32x2(acc0, f32x2(o0 ? ex2(f32x2_lo(a)) : 0.f, o1 ? ex2(f32x2_hi(a)) : 0.f));
             acc1 = add_f32x2(acc1, f32x2(o2 ? ex2(f32x2_lo(b)) : 0.f, o3 ? ex2(f32x2_hi(b)) : 0.f));
           };
-          for (int k = from; k < nr;) {
-            if (k >= vis && k + 32 <= nr) {
-              uint32_t x[32];
-              tmem_ld32(at + k, x);
-              tmem_wait32(x);
+          // 32 rows at a time: those that all see the warp's keys, then the others
+          const int k0 = min(max(from, (vis + 31) & ~31), nr), k1 = max(k0, nr & ~31);
+#pragma unroll 1
+          for (int k = k0; k < k1; k += 32) {
+            uint32_t x[32];
+            tmem_ld32(at + k, x);
+            tmem_wait32(x);
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) add4(x + i, k + i, true, true, true, true);
-              k += 32;
-              continue;
-            }
+            for (int i = 0; i < 32; i += 4) add4(x + i, k + i, true, true, true, true);
+          }
+          for (int k = from == k0 ? k1 : from; k < nr; k = k + 32 == k0 ? k1 : k + 32) {
             // which of the 32 rows see the key: up to the chunk's end, from the causal border on, or by the mask
             uint32_t x[32];
             tmem_ld32(at + k, x);
@@ -601,13 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (mine) {
                   const long long row0 = u.mask_row + (p.mask_full ? j : draft);
                   const int width = p.mask_full ? u.keys : u.L;
-                  for (int tok = row / p.group, e = tok * p.group - row; e < 32 && tok < u.n; ++tok, e += p.group) {
-                    const long long bit = row0 + (long long)tok * width;
-                    if ((p.mask[bit >> 3] >> (bit & 7)) & 1) {   // rows e .. e + group - 1, those among the 32
-                      const int z = min(e + p.group, 32);
-                      on |= (z == 32 ? 0xffffffffu : (1u << z) - 1u) & (0xffffffffu << max(e, 0));
-                    }
-                  }
+                  on = mask_bits(p.mask, row0, width, row, p.group, u.n);
                 }
               }
             }
@@ -616,7 +693,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
               add4(x + i, k + i, on & (1u << i), on & (2u << i), on & (4u << i), on & (8u << i));
-            k += 32;
           }
           tc_fence_before();
           acc0 = add_f32x2(acc0, acc1);
