@@ -1065,9 +1065,12 @@ def paged_qkv_append(q, k, v, append_indptr, kv_indptr, kv_indices, last_page_le
     kp, ks = _token_rows(k, "k", h_kv, d, total, dev)
     vp, vs = _token_rows(v, "v", h_kv, dv, total, dev)
     if q_out is None:
-        q_out = torch.empty((total, h_q, d), dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = q_out.data_ptr()
     elif q_out.shape != (total, h_q, d):
         raise ValueError("q_out must be [%d, %d, %d]" % (total, h_q, d))
+    else:
+        out = _arg(q_out, "q_out", torch.bfloat16, total * h_q * d, dev)
     w, wc, qw, kw = q_weight if q_weight is not None else k_weight, 0, None, None
     if w is not None:
         if w.dtype not in _CODES:
@@ -1096,8 +1099,7 @@ def paged_qkv_append(q, k, v, append_indptr, kv_indptr, kv_indices, last_page_le
         _arg(kv_indptr, "kv_indptr", i32, batch + 1, dev),
         _arg(kv_indices, "kv_indices", i32, kv_indices.shape[0], dev),
         _arg(last_page_len, "last_page_len", i32, batch, dev),
-        _arg(q_out, "q_out", torch.bfloat16, total * h_q * d, dev),
-        _arg(k_cache, "k_cache", k_cache.dtype, k_cache.numel(), dev),
+        out, _arg(k_cache, "k_cache", k_cache.dtype, k_cache.numel(), dev),
         _arg(v_cache, "v_cache", k_cache.dtype, v_cache.numel(), dev), batch, h_q, h_kv, d, page_size, pages,
         code, total, ctypes.byref(o), _arg(status, "status", i32, 1, dev), _device_stream(stream, dev))
     _check("paged_qkv_append", rc)
