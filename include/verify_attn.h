@@ -800,7 +800,8 @@ int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* k
  * a page outside the pool with VA_DEV_BAD_PAGE (status_d, nullable); kv_len_out
  * then receives the unchanged length.  Requests that share pages are not
  * supported.  No workspace; num_sms <= 0 queries the current device.
- * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED, VA_ERR_CUDA.
+ * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED (among others a layer of
+ * 2^32 cache rows or more), VA_ERR_CUDA.
  */
 int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* kv_indptr,
                    const int32_t* kv_indices, const int32_t* last_page_len, void* k_cache, void* v_cache,
