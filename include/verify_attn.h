@@ -762,11 +762,12 @@ int paged_qkv_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
  *
  * A query whose lse is -inf saw nothing and counts nothing; NaN in lse, q or a
  * key makes the weights NaN of the keys seen with it.  Masked keys may hold
- * anything.  A request whose tables or path are invalid is skipped with
- * VA_DEV_BAD_TABLE, a key whose page lies outside the pool with VA_DEV_BAD_PAGE
- * (status_d, nullable).  With an fp8 cache q is taken as f16, as in the tcgen05
- * attention kernels: |q| must stay below 65504.  Each sum is made in fp32 in a
- * fixed order.  No workspace; num_sms <= 0 queries the current device.
+ * anything.  A request whose tables, mask offsets (below 0, or of another span
+ * than the plan takes) or path are invalid is skipped with VA_DEV_BAD_TABLE, a
+ * key whose page lies outside the pool with VA_DEV_BAD_PAGE (status_d,
+ * nullable).  With an fp8 cache q is taken as f16, as in the tcgen05 attention
+ * kernels: |q| must stay below 65504.  Each sum is made in fp32 in a fixed
+ * order.  No workspace; num_sms <= 0 queries the current device.
  * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED (among others more than
  * 65,535 requests), VA_ERR_CUDA.
  */

@@ -148,7 +148,7 @@ struct __align__(16) Unit {
   int flags;               // kBad ..
   int rows, keys, pre;     // of the request, as in Request
   int key0, h, o, L;
-  int n, mask_row;         // mask_indptr of the request
+  int n, mask_row;         // first bit of the request's mask
   int k_slot, k_round;     // ring places of tile 0 ...
   int k_slot1, k_round1;   // ... and 1,
   int q_slot, q_round;     // of chunk c0,
@@ -167,14 +167,19 @@ struct Walk {
   Request rq;
   long long at, left;
   int b, h, tile, tiles;
+  int mask0;         // first bit of the request's mask
   bool fresh, last;  // first / last unit of this (request, head) in a row
   bool first;
 
-  __device__ Walk(const KeyWeightParams& p_, const Sched& s_, const int2* l) : p(p_), s(s_), list(l), at(0), left(s_.count), b(-1), h(0), tile(0), tiles(0), first(true) {}
+  __device__ Walk(const KeyWeightParams& p_, const Sched& s_, const int2* l) : p(p_), s(s_), list(l), at(0), left(s_.count), b(-1), h(0), tile(0), tiles(0), mask0(0), first(true) {}
 
   __device__ void enter(int nb) {
     b = nb;
+    mask0 = p.mask ? p.mask_indptr[b] : 0;
+    const long long bits = p.mask ? (long long)p.mask_indptr[b + 1] - mask0 : 0;
     rq = load_request(p, b);
+    // a mask is read where its offsets say: they span what the attention's plan takes, no other
+    if (p.mask && (mask0 < 0 || bits != (long long)rq.L * (p.mask_full ? rq.keys : rq.L))) rq.bad = true;
     if (!rq.bad && p.accept_len) {
       bool bad = false;
       for (int k = threadIdx.x & 31; k < rq.n; k += 32) {
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           u.L = rq.L;
           u.pg0 = rq.pg0;
           u.n = rq.n;
-          u.mask_row = p.mask ? p.mask_indptr[w.b] : 0;
+          u.mask_row = w.mask0;
           if (rq.chunks > 0) {
             u.k_slot = kr.slot;
             u.k_round = kr.round;

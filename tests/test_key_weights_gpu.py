@@ -340,3 +340,31 @@ def test_two_calls_at_once(va):
     for c in cases:
         assert int(c.status) == 0
         c.check()
+
+
+@pytest.mark.parametrize("mask", ["qlen", "full-holes"])
+def test_mask_offsets_that_disagree(va, mask):
+    """Mask offsets below 0, or of another span than L * L (L * kv_len for the
+    full layout), leave their requests alone; the mask is not read there."""
+    lens, pre = [5, 7, 300, 4], [40, 0, 60, 9]
+    c = Case(130, lens, pre, mask=mask)
+    c.dev["mask_indptr"][1] = -16           # the end of request 0's mask, the beginning of request 1's
+    c.run(va)
+    assert int(c.status) == 2
+    c.check(skip=[0, 1])
+    c = Case(131, lens, pre, mask=mask, fp8=True, nhd=True)
+    c.dev["mask_indptr"][4] -= 1
+    c.run(va)
+    assert int(c.status) == 2
+    c.check(skip=[3])
+    c = Case(132, lens, pre, mask=mask, hq=16)
+    c.dev["mask_indptr"][3:] += 1 << 30     # two spans too long
+    c.dev["mask_indptr"][4] += 8
+    c.run(va)
+    assert int(c.status) == 2
+    c.check(skip=[2, 3])
+    c = Case(133, [0, 3], [10, 20], mask=mask)
+    c.dev["mask_indptr"][0] = -1            # a request without tokens, too
+    c.run(va)
+    assert int(c.status) == 2
+    c.check(skip=[0])
