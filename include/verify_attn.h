@@ -703,8 +703,9 @@ int paged_kv_compact(const int32_t* accept_len, const int32_t* accepted_nodes,
  * leaves its row of q_out as it was.  Rows at or behind append_indptr[batch]
  * are padding and left alone without a status bit.  q_out may be q itself when
  * q is contiguous; it may not overlap q, k or v otherwise.  NaN and infinity
- * go their way within their head.  All-zero options with options->eps = 0 and
- * no weights: a bf16 HND append that also copies q.
+ * go their way within their head: where it is not normalised they reach no
+ * element but their own and, below rotary_dim, its pair's.  All-zero options
+ * (options->eps = 0, no weights): a bf16 HND append that also copies q.
  * Errors: VA_ERR_INVALID_ARGUMENT (null or misaligned pointers: rows start on
  * 16 bytes; strides below a row; eps negative; scales, theta, positions
  * without rotary_dim or the other way round; overlap), VA_ERR_UNSUPPORTED

@@ -13,7 +13,10 @@
 // lanes, 16 bytes each, so a lane has the same columns of all rows and keeps
 // for them, weight and rotation in one,
 //   y = (x A + x' B) / rms,  A = w cos, B = -+ w' sin,  x' and w' the pair's other
-// -- of which the raw 16 bytes come from the other lane by four shuffles.
+// -- of which the raw 16 bytes come from the other lane by four shuffles.  In
+// columns that do not turn x' may not come in by B = 0, which makes NaN of an
+// infinity: there x' is x itself and A = B = w / 2 (exact without weights); with
+// pairs of neighbours x' is masked to 0.
 //
 // A CTA takes a run of tokens, one each where they are few.  It finds the slots
 // of eight tokens (a warp a token) and their angles at a time.  With one token
@@ -94,8 +97,9 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
 }
 
 // y = (x A + x' B) / rms of this lane's columns; all lanes of the warp call.
+// (keep: all bits, or none where pairs of neighbours do not turn)
 template <int D, bool PAIRS>
-__device__ __forceinline__ void head(uint4 raw, const Coef& c, bool norm, bool rot, int partner, float eps, float (&y)[8]) {
+__device__ __forceinline__ void head(uint4 raw, const Coef& c, bool norm, bool rot, uint32_t keep, int partner, float eps, float (&y)[8]) {
   constexpr int LANES = D / 8;
   const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
   uint64_t x[4], v[4];
@@ -107,7 +111,7 @@ __device__ __forceinline__ void head(uint4 raw, const Coef& c, bool norm, bool r
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if constexpr (PAIRS) {
-        v[k] = fma_f32x2(f32x2(f32x2_hi(x[k]), f32x2_lo(x[k])), c.b[k], v[k]);
+        v[k] = fma_f32x2(f32x2(__uint_as_float(u[k] & 0xffff0000u & keep), __uint_as_float((u[k] << 16) & keep)), c.b[k], v[k]);
       } else {
         const uint32_t o = __shfl_sync(0xffffffffu, u[k], partner, LANES);
         v[k] = fma_f32x2(f32x2(__uint_as_float(o << 16), __uint_as_float(o & 0xffff0000u)), c.b[k], v[k]);
@@ -137,7 +141,7 @@ template <int D, bool PAIRS, int MODE>
 __global__ void __launch_bounds__(kThreads, MODE == kStaged ? kResident : MODE == kDirect ? 3 : 1) paged_qkv_append_kernel(const QkvParams p) {
   constexpr int LANES = D / 8, GROUPS = kThreads / LANES;
   constexpr bool STAGED = MODE == kStaged;
-  __shared__ __align__(16) float cs[kTokens][D], sn[kTokens][D];   // by column: cos (1 where nothing turns), -+ sin (0)
+  __shared__ __align__(16) float cs[kTokens][D], sn[kTokens][D];   // by column: cos, -+ sin
   __shared__ __align__(16) float wt[2][D];
   __shared__ long long first_row[kTokens];   // cache row of the token's KV head 0, or -1
   extern __shared__ __align__(128) uint8_t stages[];   // STAGED: kStages x (q, k, v rows of a token)
@@ -188,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kStaged ? kResident : MODE =
   }
   const int e0 = lane * 8, half = p.rot / 2;
   const bool rot = p.rot > 0, q_norm = p.q_weight != nullptr, k_norm = p.k_weight != nullptr;
+  const uint32_t keep = !PAIRS || e0 < p.rot ? 0xffffffffu : 0u;
   const int partner = e0 >= p.rot ? lane : e0 < half ? lane + half / 8 : lane - half / 8;
   const long long step = p.nhd ? 1 : p.page_size;
 
@@ -247,13 +252,13 @@ __global__ void __launch_bounds__(kThreads, MODE == kStaged ? kResident : MODE =
       const int t = c / (D / 2), j = c % (D / 2);
       const bool turns = j < half;
       const int lo = PAIRS ? 2 * j : turns ? j : half + j, hi = PAIRS ? 2 * j + 1 : turns ? half + j : j + D / 2;
-      float co = 1.f, si = 0.f;
+      float co = PAIRS || !rot ? 1.f : 0.5f, si = PAIRS ? -0.f : 0.5f;   // (-0: x A = -0 stays)
       if (turns) {
         const uint64_t a = (uint64_t)(int64_t)p.positions[g0 + t] * p.turn[j];
         sincospif((float)(int32_t)(uint32_t)(a >> 32) * 0x1p-31f, &si, &co);
       }
       cs[t][lo] = cs[t][hi] = co;
-      sn[t][lo] = -si;
+      sn[t][lo] = turns ? -si : si;
       sn[t][hi] = si;
     }
     __syncthreads();
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kStaged ? kResident : MODE =
             const int rn = r + kRows * GROUPS;
             if (rn < p.h_q) x[j] = *reinterpret_cast<const uint4*>(q + i * p.q_stride + (size_t)rn * D);
           }
-          head<D, PAIRS>(raw, co, q_norm, rot, partner, p.eps, y);
+          head<D, PAIRS>(raw, co, q_norm, rot, keep, partner, p.eps, y);
           if (live && ok && r < p.h_q) qd[(size_t)r * LANES] = pack8(y);
         }
       }
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, MODE == kStaged ? kResident : MODE =
           if constexpr (STAGED) raw = *reinterpret_cast<const uint4*>(at + q_bytes + (r * LANES + lane) * 16);
           else raw = r0 == 0 ? kx : *reinterpret_cast<const uint4*>(k + i * p.k_stride + (size_t)r * D);
         }
-        head<D, PAIRS>(raw, co, k_norm, rot, partner, p.eps, y);
+        head<D, PAIRS>(raw, co, k_norm, rot, keep, partner, p.eps, y);
         if (live && ok && r < p.h_kv) {
           const long long row = row0 + r * step;
           if (p.quant)

@@ -278,3 +278,33 @@ def test_two_calls_at_once(va):
     torch.cuda.synchronize()
     for c in cases:
         c.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("lens, d, rot", [([3], 64, 32), ([2, 200], 128, 48), ([700, 411], 64, 16), ([640, 9], 128, 112)])
+def test_special_values_past_the_rotation(va, lens, d, rot, inter, fp8):
+    """Columns behind rotary_dim go as they are, whatever they hold: infinity and
+    NaN reach neither their neighbours nor the columns that turn."""
+    c = Case(60, lens, [5] * len(lens), hq=5, h=5, d=d, rot=rot, inter=inter, fp8=fp8, weights=None)
+    gen = torch.Generator().manual_seed(61)
+    for x in (c.q, c.k):
+        at = torch.rand((c.total, 5, d - rot), generator=gen).cuda()
+        for n, special in enumerate((float("inf"), -float("inf"), float("nan"), -0.0)):
+            x[..., rot:][(at >= n / 16) & (at < (n + 1) / 16)] = special
+    c.run(va)
+    torch.cuda.synchronize()
+    assert int(c.status) == 0
+    same = lambda a, b: bool(((a == b) | (a.isnan() & b.isnan())).all())  # noqa: E731
+    assert same(c.q_out[..., rot:], c.q[..., rot:])
+    assert bool(c.q_out[..., :rot].isfinite().all())
+    # the keys: as the append without rotation stores them, bit for bit but for NaN
+    k2, v2 = (x.clone().cuda().view(c.kc.dtype) for x in (c.k0, c.v0))
+    va.paged_kv_append(c.k.contiguous(), c.v.contiguous(), c.dev["indptr"], c.dev["kvp"], c.dev["ids"], c.dev["last"],
+                       k2, v2, k_scale=c.scales[0], v_scale=c.scales[1])
+    for b, n in enumerate(lens):
+        pages, slots = (torch.from_numpy(x[5:]).cuda().long() for x in budget.slots_of(c.t["kvp"], c.t["ids"], c.t["last"], c.page, b))
+        got, want = c.kc[pages, :, slots].float(), k2[pages, :, slots].float()
+        assert same(got[..., rot:], want[..., rot:])
+        assert bool(got[..., :rot].isfinite().all())
+        assert torch.equal(torch.signbit(got[..., rot:]) | got[..., rot:].isnan(), torch.signbit(want[..., rot:]) | want[..., rot:].isnan())
