@@ -761,9 +761,11 @@ int paged_qkv_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
  * next with the same tables, moves the key.  Slots of the other drafts are
  * not touched.
  *
- * A query whose lse is -inf saw nothing and counts nothing; NaN in lse, q or a
- * key makes the weights NaN of the keys seen with it.  Masked keys may hold
- * anything.  A request whose tables, mask offsets (below 0, or of another span
+ * A query whose lse is -inf saw nothing and counts nothing, whatever its row of
+ * q holds (so lse = -inf also leaves out queries that should not count).  NaN in
+ * lse or q of any other makes the weights NaN of the keys that the query sees;
+ * NaN in a key that some query sees, left out or not, makes its own weight NaN,
+ * and an infinity may.  Masked keys may hold anything.  A request whose tables, mask offsets (below 0, or of another span
  * than the plan takes) or path are invalid is skipped with VA_DEV_BAD_TABLE, a
  * key whose page lies outside the pool with VA_DEV_BAD_PAGE (status_d,
  * nullable).  With an fp8 cache q is taken as f16, as in the tcgen05 attention

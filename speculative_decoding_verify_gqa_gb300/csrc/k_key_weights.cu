@@ -325,6 +325,20 @@ __device__ __noinline__ uint32_t mask_bits(const uint8_t* mask, long long row0, 
   return on;
 }
 
+// A warp's rows of a chunk of q that count nothing (`out`: this lane's own row)
+// become 0: 2^(s c - lse log2 e) is 0 for lse = -inf where s is finite, and NaN
+// where such a row holds NaN or infinity.  Behind the copies, which so need not
+// wait for lse, and out of line: rarely called.
+template <int QCH>
+__device__ __noinline__ void leave_out(uint32_t base, int own, bool out) {
+  cp_async_wait_all();
+  __syncwarp();
+  if (out)
+#pragma unroll 1
+    for (int ch = 0; ch < QCH; ++ch) sts128(op_addr(base, own, ch), make_uint4(0, 0, 0, 0));
+  __syncwarp();
+}
+
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
     verify_attn_key_weights_kernel(const KeyWeightParams p, const __grid_constant__ CUtensorMap kmap) {
@@ -883,6 +897,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // rows past the end, and rows that saw nothing, count nothing
         l2s[qr.slot * kTile + own] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+        const bool out = qrow >= 0 && lse == -INFINITY;
+        if (__any_sync(0xffffffffu, out)) leave_out<QCH>(base, own, out);
         if constexpr (FP8) put(8 | (nk + qr.slot));
         else arrive_behind(bar(B_FULL + nk + qr.slot));
         qr.step();

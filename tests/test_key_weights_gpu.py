@@ -368,3 +368,56 @@ def test_mask_offsets_that_disagree(va, mask):
     c.run(va)
     assert int(c.status) == 2
     c.check(skip=[0])
+
+
+LEFT_OUT = [
+    dict(lens=[4, 9, 1], pre=[40, 200, 0], hq=8, h=2),
+    dict(lens=[4, 9, 1], pre=[40, 200, 0], hq=6, h=2, d=64, fp8=True, page=4, decay=0.5),
+    dict(lens=[17, 30], pre=[300, 10], hq=32, h=8, mask="qlen-holes"),
+    dict(lens=[12, 40], pre=[30, 140], hq=8, h=2, d=64, mask="full-holes", fp8=True, nhd=True, page=32),
+    dict(lens=[40, 7], pre=[90, 500], hq=16, h=2, path=True),
+    dict(lens=[700, 300], pre=[100, 2000], hq=16, h=4),
+    dict(lens=[700, 300], pre=[100, 2000], hq=16, h=4, fp8=True, nhd=True, mask="qlen"),
+    dict(lens=[8, 3, 1, 5] * 10, pre=list(range(300, 3500, 80)), hq=16, h=4),
+]
+
+
+@pytest.mark.parametrize("n", range(len(LEFT_OUT)))
+def test_queries_left_out(va, n):
+    """A query whose lse is -inf counts nothing, whatever its row and the keys that it would see hold."""
+    c = Case(140 + n, **LEFT_OUT[n])
+    out = torch.from_numpy(c.rng.random(c.lse.shape) < 0.2).cuda()
+    out[::5] = True                          # whole tokens among them
+    c.lse[out] = -float("inf")
+    row = torch.from_numpy(c.rng.integers(0, 4, c.lse.shape)).cuda()
+    for k, special in enumerate((float("nan"), float("inf"), -float("inf"), 3e38)):
+        c.q[out & (row == k)] = special
+    c.run(va)
+    torch.cuda.synchronize()
+    assert int(c.status) == 0
+    c.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_all_queries_left_out(va, fp8):
+    """Nothing is added where every lse is -inf, whatever q holds; a key of NaN or
+    infinity harms no weight but its own."""
+    c = Case(150, [6, 300], [150, 40], hq=8, h=2, fp8=fp8, decay=0.5)
+    c.lse.fill_(-float("inf"))
+    c.q[::2] = float("nan")
+    c.q[1::2] = float("inf")
+    bad = []
+    for b in range(2):
+        pages, slots = budget.slots_of(c.kvp, c.ids, c.last, c.page, b)
+        bad.append(torch.arange(b, len(pages), 3, device="cuda"))
+        c.kc.view(torch.uint8)[torch.from_numpy(pages[b::3]).cuda().long(), :, torch.from_numpy(slots[b::3]).cuda().long()] = 0x7f   # NaN
+    c.run(va)
+    for b in range(2):
+        pages, slots = budget.slots_of(c.kvp, c.ids, c.last, c.page, b)
+        at = (torch.from_numpy(pages).cuda().long(), slice(None), torch.from_numpy(slots).cuda().long())
+        want = 0.5 * torch.from_numpy(c.w0).cuda()[at]
+        want[c.pre[b]:] = 0
+        got = c.w[at]
+        good = torch.ones(len(pages), dtype=torch.bool, device="cuda")
+        good[bad[b]] = False
+        assert torch.equal(got[good], want[good])
