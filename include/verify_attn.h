@@ -741,11 +741,11 @@ int paged_qkv_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
  * by.  For key j of request b and KV head h,
  *   w[j] = base + sum_t sum_g exp(s(t, g, j) - lse[t, g])
  * over the query tokens t that see j, s and what they see as in
- * verify_attn_run (the same q, k_cache, tables, mask, sm_scale, k_scale; a plan
- * with RoPE or e4m3 queries has no counterpart: give the rotated q), and lse
- * [total_qo, num_qo_heads] fp32 that call's result.  base = decay * w[j] for
- * the keys of the prefix (decay 0: the old value is not read), 0 for the
- * step's own L_b keys.
+ * verify_attn_run (the same q, k_cache, tables, mask, sm_scale, k_scale, with
+ * the same scales refused; a plan with RoPE or e4m3 queries has no counterpart:
+ * give the rotated q), and lse [total_qo, num_qo_heads] fp32 that call's result.
+ * base = decay * w[j] for the keys of the prefix (decay 0: the old value is not
+ * read), 0 for the step's own L_b keys.
  *
  * key_weights: fp32, one per cache row in the cache's order of rows,
  * [num_pages, num_kv_heads, page_size] (HND) or [num_pages, page_size,

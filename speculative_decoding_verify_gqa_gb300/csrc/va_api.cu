@@ -1254,7 +1254,10 @@ int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* k
       (mask && accept_len))
     return VA_ERR_INVALID_ARGUMENT;
   const float scale = sm_scale > 0.f ? sm_scale : 1.f / sqrtf((float)head_dim);
-  if (!(isfinite(k_scale) && k_scale > 0.f) || !isfinite(scale * k_scale) || !(isfinite(decay) && decay >= 0.f))
+  // (the scales that verify_attn_run takes, and the product that it makes of them)
+  const float scale_log2 = scale * k_scale * 1.4426950408889634f;
+  if (!isfinite(sm_scale) || !(isfinite(k_scale) && k_scale > 0.f) || !isfinite(scale_log2) ||
+      !(isfinite(decay) && decay >= 0.f))
     return VA_ERR_INVALID_ARGUMENT;
   if (total_qo > 0x7fffffffLL || batch > 65535) return VA_ERR_UNSUPPORTED;
   if (batch == 0) return VA_OK;
@@ -1293,7 +1296,7 @@ int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* k
   p.num_pages = num_pages;
   p.nhd = kv_layout == VA_LAYOUT_NHD;
   p.mask_full = mask_layout == VA_MASK_FULL;
-  p.scale_log2 = scale * k_scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.decay = decay;
   CUtensorMap kmap;
   memset(&kmap, 0, sizeof(kmap));

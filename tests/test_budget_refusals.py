@@ -126,3 +126,10 @@ def test_options_layout(va, tmp_path):
     subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", exe], check=True)
     got = [int(x) for x in subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split()]
     assert got == [getattr(va.QkvOptions, n).offset for n in names] + [ctypes.sizeof(va.QkvOptions)]
+
+
+@pytest.mark.parametrize("kw", [dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=-float("inf")),
+                                dict(scale=3e38, ks=1.0), dict(scale=1.0, ks=3e38), dict(ks=float("nan"))])
+def test_key_weights_refuse_the_attentions_refused_scales(va, kw):
+    """Scales that verify_attn_run refuses: not finite, or with a product that is not, times log2(e)."""
+    assert _weights(va, **kw) == INVALID
