@@ -792,7 +792,8 @@ int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* k
  * move, bit for bit and in place, to the front in their order: the k-th
  * survivor's K and V rows and its weight to position k.  Slots past them, and
  * requests with keep_len[b] >= kv_len_b, are left as they are.  kv_len_out
- * (nullable, [batch]) receives the new lengths; the pages past them are free.
+ * (nullable, [batch]; an array of its own) receives the new lengths; the pages
+ * past them are free.
  * Keys keep the rotation that they were stored with, so the queries' positions
  * go on counting.
  *

@@ -1382,6 +1382,11 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
       overlap(key_weights, rows * 4, k_cache, rows * p.k_chunks * 16) ||
       overlap(key_weights, rows * 4, v_cache, rows * p.v_chunks * 16))
     return VA_ERR_INVALID_ARGUMENT;
+  // the new lengths are written while other CTAs still read the tables
+  const unsigned __int128 nb = (unsigned __int128)batch * 4;
+  if (kv_len_out && (overlap(kv_len_out, nb, keep_len, nb) || overlap(kv_len_out, nb, last_page_len, nb) ||
+                     overlap(kv_len_out, nb, kv_indptr, nb + 4)))
+    return VA_ERR_INVALID_ARGUMENT;
   if (num_sms <= 0) {
     rc = query_sms(&num_sms);
     if (rc) return rc;

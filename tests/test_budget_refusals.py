@@ -133,3 +133,12 @@ def test_options_layout(va, tmp_path):
 def test_key_weights_refuse_the_attentions_refused_scales(va, kw):
     """Scales that verify_attn_run refuses: not finite, or with a product that is not, times log2(e)."""
     assert _weights(va, **kw) == INVALID
+
+
+@pytest.mark.parametrize("at", [4000, 4012, 8000, 8016, 7996, 12012, 11988])
+def test_evict_refuses_lengths_over_its_tables(va, at):
+    """kv_len_out is written while other CTAs still read keep_len, kv_indptr and last_page_len."""
+    base = 64 * A
+    tables = [base + 4000, base + 8000, 64, base + 12000]     # of 4 requests: 16, 20 and 16 bytes, and the page ids
+    assert va.lib().paged_kv_evict(A, *tables, 16 * A, 32 * A, 1, 4, 2, 128, 0, 16, 4, 0, 0, 64, 0, 0, base + at,
+                                   None, 1, None) == INVALID
