@@ -193,10 +193,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kv_evict_kernel(const Evict
   const int lo = min(p.sinks, keep), hi = n - min(p.recent, keep - lo), rest = keep - lo - (n - hi);
   const bool alone = n <= kEvictAlone || C == 1;
   const int S = alone ? 1 : C, srank = alone ? 0 : rank;
-  const int per = ((n + S - 1) / S + 31) & ~31, s0 = min(srank * per, n), s1 = min(s0 + per, n);
+  const int per = evict_slice(n, C), s0 = min(srank * per, n), s1 = min(s0 + per, n);
   const int m0 = max(s0, lo), m1 = min(s1, hi);
   // held whole, by upper halves, or (neither) read from the cache again by every pass
-  const bool whole = per <= p.slice_cap / 2, held = !whole && per <= p.slice_cap;
+  const int how = evict_held(per, p.slice_cap);
+  const bool whole = how == kEvictWhole, held = how == kEvictHalves;
   // the weight of key j as far as `mask` tells: the lower half is only looked at where the upper one is `fixed`'s
   auto weight_at = [&](int j, uint32_t fixed, uint32_t mask) -> uint32_t {
     if (whole) return slice32[j - s0];

@@ -1340,9 +1340,8 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
   if (head_dim_v != 64 && head_dim_v != 128) return VA_ERR_UNSUPPORTED;
   if (kv_layout != VA_LAYOUT_HND && kv_layout != VA_LAYOUT_NHD) return VA_ERR_INVALID_ARGUMENT;
   if (max_kv_len > kEvictMaxKeys) return VA_ERR_UNSUPPORTED;
-  constexpr int kMaxCluster = 8;
   const int64_t units = (int64_t)num_layers * batch;   // (both below 2^31)
-  if (units > 0x7fffffffLL / kMaxCluster / num_kv_heads) return VA_ERR_UNSUPPORTED;
+  if (units > 0x7fffffffLL / kEvictMaxCluster / num_kv_heads) return VA_ERR_UNSUPPORTED;
   if (batch == 0) return VA_OK;
   if (!key_weights || !keep_len || !kv_indptr || !last_page_len || !k_cache || !v_cache || num_pages <= 0 ||
       (max_kv_len > 0 && !kv_indices))
@@ -1373,7 +1372,7 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
   p.sinks = sinks;
   p.recent = recent;
   p.max_kv_len = (int)max_kv_len;
-  p.words = (int)((max_kv_len + 63) / 64 * 2);   // (what follows them starts on 16 bytes)
+  p.words = evict_words(max_kv_len);
   // the kernel counts a layer's rows in 32 bits
   if ((unsigned __int128)num_kv_heads * page_size * num_pages > 0xffffffffu) return VA_ERR_UNSUPPORTED;
   // all three move in place: no pool may reach into another
@@ -1391,25 +1390,8 @@ int paged_kv_evict(float* key_weights, const int32_t* keep_len, const int32_t* k
     rc = query_sms(&num_sms);
     if (rc) return rc;
   }
-  // CTAs per unit: twice as many while all CTAs still run at a time, one an SM, and every
-  // one moves 64 bytes of a row -- or 32, where most of the GPU would stay idle.
-  const int64_t all = units * num_kv_heads;
-  const int chunks = p.k_chunks + p.v_chunks;
-  auto slice = [&](int cluster) {
-    // (short requests are ranked whole by every CTA)
-    const int64_t n = std::max(((max_kv_len + cluster - 1) / cluster + 31) / 32 * 32,
-                               (std::min<int64_t>(max_kv_len, kEvictAlone) + 31) / 32 * 32);
-    // room for whole weights, four bytes each, of up to 16,384 keys; for upper halves, two bytes, of as many as
-    // shared memory takes (longer slices are read from the cache in every pass)
-    const int64_t room = ((int64_t)kEvictMaxSmem - (int64_t)evict_smem(p.words, 0)) / 64 * 32;
-    return (int)std::min(n <= kEvictAlone ? 2 * n : n, room);
-  };
-  p.cluster = 1;
-  for (int c = 2; c <= kMaxCluster; c *= 2) {
-    if (all * c > num_sms || chunks / c < (all * c * 2 <= num_sms ? 2 : 4)) break;
-    p.cluster = c;
-  }
-  p.slice_cap = slice(p.cluster);
+  p.cluster = evict_cluster(units * num_kv_heads, p.k_chunks + p.v_chunks, num_sms);
+  p.slice_cap = evict_slice_cap(max_kv_len, p.cluster);
   cudaError_t e = launch_evict(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }

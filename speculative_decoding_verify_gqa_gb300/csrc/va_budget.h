@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace va {
 
 // Norm, rotation and append of new queries, keys and values (see k_qkv_append.cu).
@@ -70,9 +72,42 @@ cudaError_t launch_key_weights(const KeyWeightParams& p, const CUtensorMap& kmap
 // Eviction of the keys with the least weight (see k_evict.cu).
 constexpr int kEvictMaxKeys = 1 << 19;  // keys of a request: a bit and a count per word in shared memory
 constexpr int kEvictAlone = 1 << 14;      // keys up to which every CTA ranks all of a unit's weights by itself
+constexpr int kEvictMaxCluster = 8;
 constexpr int kEvictStatic = 26 * 1024;   // static shared memory of a CTA, and what the system keeps of it
 constexpr int kEvictMaxSmem = 227 * 1024 - kEvictStatic;
 inline size_t evict_smem(int words, int slice) { return (size_t)words * 8 + (size_t)slice * 2; }
+inline int evict_words(int64_t max_kv_len) { return (int)((max_kv_len + 63) / 64 * 2); }   // (what follows them starts on 16 bytes)
+
+// CTAs per unit (layer, request, KV head), `units` of them: twice as many while
+// all CTAs still run at a time, one an SM, and every one moves 64 bytes of a
+// row of `chunks` 16-byte chunks -- or 32, where most of the GPU would stay idle.
+inline int evict_cluster(int64_t units, int chunks, int num_sms) {
+  int cluster = 1;
+  for (int c = 2; c <= kEvictMaxCluster; c *= 2) {
+    if (units * c > num_sms || chunks / c < (units * c * 2 <= num_sms ? 2 : 4)) break;
+    cluster = c;
+  }
+  return cluster;
+}
+// Weights, two bytes each, that a CTA has room for: whole weights of up to 16,384
+// keys; upper halves of as many as shared memory takes.  (Every CTA of a cluster
+// ranks a request of up to 16,384 keys for itself.)
+inline int evict_slice_cap(int64_t max_kv_len, int cluster) {
+  const int64_t n = std::max(((max_kv_len + cluster - 1) / cluster + 31) / 32 * 32,
+                             (std::min<int64_t>(max_kv_len, kEvictAlone) + 31) / 32 * 32);
+  const int64_t room = ((int64_t)kEvictMaxSmem - (int64_t)evict_smem(evict_words(max_kv_len), 0)) / 64 * 32;
+  return (int)std::min(n <= kEvictAlone ? 2 * n : n, room);
+}
+// Keys of a unit of n that each CTA of its cluster looks after, and how it holds
+// their weights: whole, by upper halves, or not at all (every pass reads the cache).
+__host__ __device__ inline int evict_slice(int n, int cluster) {
+  const int ctas = n <= kEvictAlone ? 1 : cluster;
+  return ((n + ctas - 1) / ctas + 31) & ~31;
+}
+enum { kEvictWhole, kEvictHalves, kEvictReread };
+__host__ __device__ inline int evict_held(int slice, int slice_cap) {
+  return slice <= slice_cap / 2 ? kEvictWhole : slice <= slice_cap ? kEvictHalves : kEvictReread;
+}
 struct EvictParams {
   float* key_weights;         // [layers, rows of a layer]
   const int32_t* keep_len;    // [batch]

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from evict_modes import shapes
 from oracle import budget
 
 pytestmark = pytest.mark.gpu
@@ -206,3 +207,90 @@ def test_two_calls_at_once(va):
             c.run(va)
     for c in cases:
         c.check()
+
+
+class Long(Case):
+    """A case of long requests: the moves of a request, layer and head are made together."""
+
+    def expect(self, skip=()):
+        w5 = self.w if self.layers is not None else self.w[None]
+        out = [x.copy() for x in (self.k, self.v, self.w)]
+        for b in range(len(self.lens)):
+            pages, slots = budget.slots_of(self.kvp, self.ids, self.last, self.page, b)
+            for layer in range(w5.shape[0]):
+                for h in range(w5.shape[3] if self.nhd else w5.shape[2]):
+                    at = (lambda r: (layer, pages[r], slots[r], h)) if self.nhd else (lambda r: (layer, pages[r], h, slots[r]))  # noqa: E731
+                    rows = np.array(budget.survivors(w5[at(slice(None))], int(self.keep[b]), self.sinks, self.recent), int)
+                    for x, y in zip((self.k, self.v, self.w), out):
+                        x5, y5 = (x, y) if self.layers is not None else (x[None], y[None])
+                        y5[at(slice(0, len(rows)))] = x5[at(rows)]
+        return out
+
+    def run_on(self, va, num_sms, max_kv_len):
+        """The call with a number of SMs of the caller's, which bounds the CTAs that share a request."""
+        x, dims = self.dev, self.dev["k"].shape[-4:]
+        page, h = (dims[1], dims[2]) if self.nhd else (dims[2], dims[1])
+        p = lambda t: t.data_ptr()  # noqa: E731
+        rc = va.lib().paged_kv_evict(
+            p(x["w"]), p(x["keep"]), p(x["kvp"]), p(x["ids"]), p(x["last"]), p(x["k"]), p(x["v"]), self.layers or 1,
+            len(self.lens), h, dims[3], x["v"].shape[-1], page, dims[0],
+            va.KV_FP8_E4M3 if self.dt is torch.float8_e4m3fn else va.KV_BF16, 1 if self.nhd else 0, max_kv_len, self.sinks,
+            self.recent, p(self.kv_len), p(self.status), num_sms, torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+
+
+# What a CTA holds of its weights: all of them, their upper halves, or none; by one
+# CTA a unit, and by two, four and eight.  (case, SMs, max_kv_len: None the
+# longest request's, CTAs a unit, mode)
+HELD = [
+    (dict(lens=[20000], keep=[7001], sinks=5, recent=77, h=1), 1, None, 1, "halves"),
+    (dict(lens=[20000], keep=[7001], sinks=5, recent=77, h=1, values="close"), 1, None, 1, "halves"),
+    (dict(lens=[16385], keep=[16000], sinks=1, h=1, values="equal", nhd=True, page=1, fp8=True), 1, None, 1, "halves"),
+    (dict(lens=[17001, 300, 0, 16500], keep=[4003, 299, 0, 16499], sinks=33, recent=3, h=3, values="few", nhd=True, fp8=True), 12, None, 1, "halves"),
+    (dict(lens=[16401], keep=[555], recent=50, h=1, values="special", page=256), 1, None, 1, "halves"),
+    (dict(lens=[18000], keep=[60], sinks=9, recent=51, h=1, values="few"), 1, None, 1, "halves"),      # no key competes for a place
+    (dict(lens=[18000], keep=[17990], sinks=9000, recent=8995, h=1, values="close"), 1, None, 1, "halves"),   # none between the ends
+    (dict(lens=[40000, 33001], keep=[9999, 32990], sinks=3, recent=1001, h=1, d=128, values="close", page=64), 4, None, 2, "halves"),
+    (dict(lens=[40001], keep=[20000], sinks=13, recent=100, h=1, values="few", fp8=True, nhd=True), 2, None, 2, "halves"),
+    (dict(lens=[33333], keep=[11111], h=2, values="equal", recent=7), 4, None, 2, "halves"),
+    (dict(lens=[35007], keep=[30000], h=1, values="special", sinks=17, nhd=True, page=32), 2, None, 2, "halves"),
+    (dict(lens=[70001], keep=[33333], sinks=4, recent=37, h=1, d=128, values="close", page=128), 4, None, 4, "halves"),
+    (dict(lens=[140003], keep=[70001], sinks=4, recent=37, h=1, d=128, values="few", page=128), 8, None, 8, "halves"),
+    (dict(lens=[140003], keep=[139000], sinks=1, h=1, d=64, values="close", page=256), 8, None, 4, "halves"),
+    # ranked whole by every CTA, from upper halves: short requests in a batch of long ones
+    (dict(lens=[12001], keep=[6000], sinks=3, recent=40, h=1, values="close"), 1, 16500, 1, "halves"),
+    (dict(lens=[15000, 9000], keep=[1000, 8999], sinks=3, recent=40, h=1, values="few"), 4, 33000, 2, "halves"),
+    (dict(lens=[16384], keep=[9000], sinks=3, h=1, d=128, values="special", nhd=True), 8, 140000, 8, "halves"),
+    # more room than keys: whole weights of more than a CTA of a cluster ranks by itself
+    (dict(lens=[18000], keep=[6000], h=1, values="close", recent=5), 1, 1 << 19, 1, "whole"),
+    (dict(lens=[30000], keep=[6000], h=1, values="special", recent=5, sinks=2), 2, 1 << 19, 2, "whole"),
+    # more keys than room
+    (dict(lens=[38001], keep=[16001], h=1, values="few", recent=5, sinks=2), 1, 1 << 19, 1, "reread"),
+    (dict(lens=[38001], keep=[30000], h=1, values="close", nhd=True, fp8=True), 1, 1 << 19, 1, "reread"),
+    (dict(lens=[75500], keep=[7000], h=1, values="special", sinks=40, d=128), 2, 1 << 19, 2, "reread"),
+    (dict(lens=[75001], keep=[74000], h=1, values="equal", sinks=4, recent=99, page=64), 2, 1 << 19, 2, "reread"),
+]
+
+
+@pytest.mark.parametrize("n", range(len(HELD)))
+def test_each_way_to_hold_the_weights(va, tmp_path, n):
+    case, sms, most, cluster, mode = HELD[n]
+    c = Long(200 + n, **case)
+    most = most or max(c.lens)
+    units = (c.layers or 1) * len(c.lens) * case["h"]
+    chunks = (c.k.shape[-1] + c.v.shape[-1]) // 16
+    got = shapes(tmp_path, [(units, chunks, sms, most, max(c.lens))])[0]
+    assert (got[0], got[3]) == (cluster, mode)
+    c.run_on(va, sms, most)
+    c.check()
+
+
+def test_upper_halves_of_many_units(va, tmp_path):
+    """The binding's own call: more units than half the SMs, one CTA each."""
+    sms = va.num_sms()
+    layers = sms // 16 + 1
+    c = Long(230, [17500, 16390], [9001, 16389], sinks=3, recent=45, h=8, d=64, fp8=True, nhd=True, layers=layers, values="close")
+    got = shapes(tmp_path, [(layers * 2 * 8, 8, sms, 17500, n) for n in c.lens])
+    assert [(g[0], g[3]) for g in got] == [(1, "halves")] * 2
+    c.run(va, max_kv_len=17500)
+    c.check()
