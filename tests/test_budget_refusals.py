@@ -142,3 +142,10 @@ def test_evict_refuses_lengths_over_its_tables(va, at):
     tables = [base + 4000, base + 8000, 64, base + 12000]     # of 4 requests: 16, 20 and 16 bytes, and the page ids
     assert va.lib().paged_kv_evict(A, *tables, 16 * A, 32 * A, 1, 4, 2, 128, 0, 16, 4, 0, 0, 64, 0, 0, base + at,
                                    None, 1, None) == INVALID
+
+
+def test_qkv_append_refuses_null_options(va):
+    """NULL options beside arguments that are valid otherwise, and with nothing to append."""
+    for total in (2, 0):
+        args = (A, 256, 2 * A, 256, 3 * A, 256, 64, 64, 64, 64, 4 * A, 5 * A, 6 * A, 1, 2, 2, 128, 16, 4, 0, total)
+        assert va.lib().paged_qkv_append(*args, None, None, None) == INVALID

@@ -308,3 +308,38 @@ def test_special_values_past_the_rotation(va, lens, d, rot, inter, fp8):
         assert same(got[..., rot:], want[..., rot:])
         assert bool(got[..., :rot].isfinite().all())
         assert torch.equal(torch.signbit(got[..., rot:]) | got[..., rot:].isnan(), torch.signbit(want[..., rot:]) | want[..., rot:].isnan())
+
+
+def test_same_as_the_rotating_append(va):
+    """Without weights the rotated keys are paged_kv_append's at the same positions,
+    up to what both may lose: the angle and its sine and cosine (32 half steps of
+    fp32 of what is added, the tolerance against the definition, in either), and
+    half a step of bf16 or e4m3 in either."""
+    for fp8 in (False, True):
+        for nhd in (False, True):
+            c = Case(62, [6, 2, 90], [11, 0, 300], weights=None, fused=False, fp8=fp8, nhd=nhd, far=8191)
+            c.run(va)
+            k2, v2 = (x.clone().cuda().view(c.kc.dtype) for x in (c.k0, c.v0))
+            va.paged_kv_append(c.k, c.v, c.dev["indptr"], c.dev["kvp"], c.dev["ids"], c.dev["last"], k2, v2,
+                               k_scale=c.scales[0], v_scale=c.scales[1], kv_layout="nhd" if nhd else "hnd",
+                               positions=c.positions, rope_theta=c.theta)
+            assert torch.equal(v2.view(torch.uint8), c.vc.view(torch.uint8))
+            _, (k, size), _ = c.expect()
+            for b, n in enumerate(c.lens):
+                pages, slots = budget.slots_of(c.t["kvp"], c.t["ids"], c.t["last"], c.page, b)
+                new = slice(c.pre[b], c.pre[b] + n)
+                rows = slice(int(c.t["indptr"][b]), int(c.t["indptr"][b]) + n)
+                pages, slots = (torch.from_numpy(x[new]).cuda().long() for x in (pages, slots))
+                a, e = ((x[pages, slots] if nhd else x[pages, :, slots]).float().double().cpu().numpy() for x in (c.kc, k2))
+                if fp8:
+                    y = np.clip(k[rows] / np.float64(np.float32(c.scales[0])), -448, 448)
+                    tol = 2 * (2.0 ** -4 * np.abs(y) + 2.0 ** -10 + 34 * 2.0 ** -24 * size[rows] / c.scales[0])
+                else:
+                    tol = 2 * (2.0 ** -8 * np.abs(k[rows]) + 32 * 2.0 ** -24 * size[rows] + 1e-38)
+                assert np.all(np.abs(a - e) <= tol)
+            free = torch.ones(c.kc.shape[:3], dtype=torch.bool, device="cuda")
+            for b, n in enumerate(c.lens):
+                pages, slots = budget.slots_of(c.t["kvp"], c.t["ids"], c.t["last"], c.page, b)
+                pages, slots = (torch.from_numpy(x[c.pre[b]:]).cuda().long() for x in (pages, slots))
+                free[(pages, slots) if nhd else (pages, slice(None), slots)] = False
+            assert torch.equal(k2.view(torch.uint8)[free], c.kc.view(torch.uint8)[free])
