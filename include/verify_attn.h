@@ -691,8 +691,10 @@ int paged_kv_compact(const int32_t* accept_len, const int32_t* accepted_nodes,
  * 2, in pairs (j, j + rotary_dim / 2) -- paged_kv_append_ex's pairing -- or
  * (2j, 2j + 1) when interleaved.  inv_freq (host, rotary_dim / 2 doubles,
  * finite; NULL: the formula) replaces rope_theta^(-2j / rotary_dim) /
- * rope_scale: scaled rotations of long contexts.  The angle is exact to 2^-64
- * of the position and 1e-9 of a radian before its sine and cosine (fp32).
+ * rope_scale: scaled rotations of long contexts.  The angle is reduced to one
+ * turn in 64-bit integers and goes to the sine and cosine as fp32: it is good to
+ * 1e-7 of a radian, and position * 2^-53 of a turn (the frequency's double) for
+ * frequencies up to 2.
  * Everything is computed in fp32 and rounded once: q to q_out ([total_new,
  * num_qo_heads, head_dim] bf16), k into the token's slot of k_cache, v as it is
  * into v_cache, which are bf16, or e4m3 codes of x / k_scale and x / v_scale as
@@ -706,6 +708,7 @@ int paged_kv_compact(const int32_t* accept_len, const int32_t* accepted_nodes,
  * go their way within their head: where it is not normalised they reach no
  * element but their own and, below rotary_dim, its pair's.  All-zero options
  * (options->eps = 0, no weights): a bf16 HND append that also copies q.
+ * VA_DEV_TIMEOUT: a bounded wait gave up; rows may then be missing.
  * Errors: VA_ERR_INVALID_ARGUMENT (null or misaligned pointers: rows start on
  * 16 bytes; strides below a row; eps negative; scales, theta, positions
  * without rotary_dim or the other way round; overlap), VA_ERR_UNSUPPORTED
@@ -750,8 +753,9 @@ int paged_qkv_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
  * key_weights: fp32, one per cache row in the cache's order of rows,
  * [num_pages, num_kv_heads, page_size] (HND) or [num_pages, page_size,
  * num_kv_heads] (NHD), updated in place.  Slots that no request's keys lie in
- * are not touched.  Requests that share pages are not supported (their sums
- * for the shared keys would race).
+ * are not touched.  Requests that share pages, as verify_attn_plan_shared takes
+ * them, and a page listed twice are not supported (the sums for the shared keys
+ * would race) and not looked for.
  *
  * accept_len / accepted_nodes (both or neither; verify_accept_greedy's or
  * verify_accept_sample's results for this step; mask and mask_indptr must then
@@ -770,7 +774,8 @@ int paged_qkv_append(const void* q, int64_t q_stride, const void* k, int64_t k_s
  * key whose page lies outside the pool with VA_DEV_BAD_PAGE (status_d,
  * nullable).  With an fp8 cache q is taken as f16, as in the tcgen05 attention
  * kernels: |q| must stay below 65504.  Each sum is made in fp32 in a fixed
- * order.  No workspace; num_sms <= 0 queries the current device.
+ * order.  VA_DEV_TIMEOUT: a bounded wait gave up; weights may then be as they
+ * were.  No workspace; num_sms <= 0 queries the current device.
  * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED (among others more than
  * 65,535 requests), VA_ERR_CUDA.
  */
@@ -790,7 +795,8 @@ int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* k
  * for), then of the keys between them those with the largest key_weights -- the
  * lower position among equal ones; -0 equals 0, NaN counts as largest.  They
  * move, bit for bit and in place, to the front in their order: the k-th
- * survivor's K and V rows and its weight to position k.  Slots past them, and
+ * survivor's K and V rows and its weight to position k -- so all survivors
+ * behind the first key that goes move, however few go.  Slots past them, and
  * requests with keep_len[b] >= kv_len_b, are left as they are.  kv_len_out
  * (nullable, [batch]; an array of its own) receives the new lengths; the pages
  * past them are free.
@@ -803,8 +809,9 @@ int verify_attn_key_weights(const void* q, const void* k_cache, const int32_t* k
  * bound of the requests' lengths, at most 524288.  A request that exceeds it,
  * or whose tables are invalid, is skipped with VA_DEV_BAD_TABLE, one that lists
  * a page outside the pool with VA_DEV_BAD_PAGE (status_d, nullable); kv_len_out
- * then receives the unchanged length.  Requests that share pages are not
- * supported.  No workspace; num_sms <= 0 queries the current device.
+ * then receives the unchanged length.  Requests that share pages, and a page
+ * listed twice, are not supported and not looked for: the keys of one would
+ * overwrite the other's.  No workspace; num_sms <= 0 queries the current device.
  * Errors: VA_ERR_INVALID_ARGUMENT, VA_ERR_UNSUPPORTED (among others a layer of
  * 2^32 cache rows or more), VA_ERR_CUDA.
  */

@@ -8,12 +8,13 @@
 // there are units enough.  Each CTA holds a slice of the unit's weights as the
 // order-preserving integers in shared memory, whole or, where they are too many,
 // their upper halves (two CTAs then hold 131,072 keys; with four bytes a key it
-// took eight, which did not fit the GPU at a time).  The weight of the last survivor is found by a
-// radix select from the top, by digits of 11, 5, 11 and 5 bits: the CTAs count
+// took eight, which did not fit the GPU at a time); where those are too many,
+// too, every pass reads the cache.  The weight of the last survivor is found by
+// a radix select from the top, by digits of 11, 5, 11 and 5 bits: the CTAs count
 // their slices, and each adds up all counts by reading the others' shared
 // memory.  Lower halves that are not held are read from the cache again, for the
-// few keys that share the upper one.  It ends as soon as all keys that share the digits found
-// survive.  (Up to 16,384 keys every CTA holds all weights and counts for itself:
+// few keys that share the upper one.  It ends as soon as all keys that share the
+// digits found survive.  (Up to 16,384 keys every CTA holds all weights and counts for itself:
 // a meeting of the cluster costs about a microsecond, and a select has up to
 // six.)  Then each CTA marks its slice, one bit a key, and every CTA gathers
 // all bits and counts them by words, so that the k-th survivor is found by a

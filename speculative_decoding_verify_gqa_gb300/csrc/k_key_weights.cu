@@ -18,8 +18,9 @@
 //
 // On one GB300: 64 chains of up to 8 tokens behind up to 8,192 keys (64/8 heads,
 // bf16) 106 us, 5.7 TB/s;
-// 8 trees of 64 nodes behind 32,768 fp8 keys (32/8 heads) 190 us, 725 TFLOP/s;
-// 10 prompts of 1,024 tokens (64/8 heads) 123 us, 697 TFLOP/s of visible pairs.
+// 8 trees of 64 nodes behind 32,768 fp8 keys (32/8 heads) 191 us, 720 TFLOP/s;
+// 10 prompts of 1,024 tokens (64/8 heads) 123 us, 697 TFLOP/s of visible pairs
+// (345 us over an fp8 cache, where the loaders widen every chunk of q, too).
 // The latter two wait for the warps that add: 32 rows take them some 500 cycles
 // where the SFU needs 256 for the two of a scheduler, and a chunk's hand-offs --
 // an mbarrier operation takes some 150 cycles -- come on top.  All roles share

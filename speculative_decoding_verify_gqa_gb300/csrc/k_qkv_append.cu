@@ -25,13 +25,15 @@
 // into shared memory by bulk copies, a token ahead of the one in work: rows
 // loaded into registers one token ahead kept too little under way (10,240 tokens
 // of 64 + 16 heads: 38 % of the DRAM's cycles, warps waiting for loads half of
-// their time).  On one GB300 these 10,240 tokens take 83.5 us (5.0 TB/s), 288
-// tokens in 64 chains into an fp8 cache 8.6 us, one token (32 + 16 heads) 3.2 us.
+// their time).  On one GB300 these 10,240 tokens take 83.5 us (5.0 TB/s; 90 into
+// an fp8 cache), 334 tokens in 64 chains into an fp8 cache 8.6 us, one token (32
+// + 16 heads) 3.2 us.
 //
 // Angles: the frequency is kept in turns as a 64-bit binary fraction, so
-// position * frequency modulo one turn is one integer product, exact for any
-// position to 2^-64 of the position; its top 32 bits go through sincospi.  (A
-// float product is off by position * 2^-24 of a radian.)
+// position * frequency modulo one turn is one integer product, which adds
+// position * 2^-64 turns to what the frequency's double has lost (below 2^-53 of
+// a turn); its top 32 bits, rounded to fp32 (1e-7 of a radian), go through
+// sincospi.  (A float product is off by position * 2^-24 of a radian.)
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -383,7 +385,8 @@ cudaError_t launch(const QkvParams& p, size_t stages, int num_sms, cudaStream_t 
 cudaError_t launch_qkv_append(const QkvParams& params, int head_dim, int num_sms, cudaStream_t stream) {
   // One wave of CTAs, each with a run of tokens whose rows are brought into
   // shared memory; a token each where all are resident that way, or where a
-  // token's rows leave no room for that many CTAs on an SM.
+  // token's rows leave no room for that many CTAs on an SM (more than 22.5 KB:
+  // 10,240 tokens of 72 + 16 heads of 128 take 91 us, of 80 + 16 146 us).
   QkvParams p = params;
   const size_t token = ((size_t)(p.h_q + p.h_kv) * head_dim + (size_t)p.h_kv * p.head_dim_v) * 2;
   const long long most = (long long)num_sms * kResident;
