@@ -57,9 +57,10 @@ constexpr int kResident = 4, kStages = 2;
 constexpr int kMaxStages = 45 * 1024;
 constexpr int kDrain = 1024;  // tries for a copy under way when the CTA gives up
 // How a CTA gets its rows: one token's into registers, all that it likes while
-// there is a CTA an SM at most (1 to 8 tokens of 64 + 16 heads 3.9 us, 4.6 with
-// the registers of the next), or so that three CTAs share an SM (334 tokens 7.5
-// us, 7.9 with two); a run of tokens' through shared memory.
+// there is a CTA an SM at most (1 to 8 tokens of 64 + 16 heads 3.7 us, 4.4 with
+// the registers of the next), or so that three CTAs share an SM, which spills
+// (334 tokens 8.4 us, 9.3 with two and no spill); a run of tokens' through shared
+// memory.
 enum { kFew, kDirect, kStaged };
 
 __device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
