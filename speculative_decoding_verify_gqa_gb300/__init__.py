@@ -1129,6 +1129,8 @@ def verify_attn_key_weights(q, k_cache, kv_indptr, kv_indices, last_page_len, qo
     if mask is not None and mask.dtype != torch.uint8:
         raise ValueError("mask must be uint8")
     batch, i32, f32 = qo_indptr.shape[0] - 1, torch.int32, torch.float32
+    if kv_indices.shape[0] == 0:   # no request has a page: there is no key (and no address to hand on)
+        return key_weights
     rc = lib().verify_attn_key_weights(
         _arg(q, "q", torch.bfloat16, total * h_q * d, dev),
         _arg(k_cache, "k_cache", k_cache.dtype, k_cache.numel(), dev),

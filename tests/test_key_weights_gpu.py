@@ -421,3 +421,13 @@ def test_all_queries_left_out(va, fp8):
         good = torch.ones(len(pages), dtype=torch.bool, device="cuda")
         good[bad[b]] = False
         assert torch.equal(got[good], want[good])
+
+
+def test_no_pages_at_all(va):
+    """An idle step: requests, none of which has a page or a token."""
+    c = Case(151, [0, 0, 0], [0, 0, 0])
+    c.dev["ids"] = c.dev["ids"][:0]
+    assert c.run(va) is c.w
+    torch.cuda.synchronize()
+    assert int(c.status) == 0
+    assert torch.equal(c.w, torch.from_numpy(c.w0).cuda())
